@@ -258,6 +258,121 @@ int kmoe_forward_router(const kmoe_params* p, const void* x_bf16, const void* w_
                         const uint8_t* w13_k, const uint8_t* w2_k, void* out_bf16, void* workspace, size_t ws_bytes,
                         cudaStream_t stream, const kmoe_stage_events* ev /* host */);
 
+/* ---- the operators around the experts: the norm in front of the layer,
+ * routing with groups, and the gradients of what trains beside the frozen
+ * MXFP4 experts (norm weight, gate weight through the logits, residual
+ * stream).  Their values are checked on the host like the forward's; they need
+ * no device error word. */
+
+/* kmoe_rmsnorm, kmoe_rmsnorm_backward: types of the residual stream (residual,
+ * h, dh_in, dh) and of the norm's weight; bf16 without the flag. */
+#define KMOE_NORM_STREAM_F32 1u
+#define KMOE_NORM_WEIGHT_F32 2u
+
+/* Residual addition, root-mean-square norm and MXFP8 quantisation of the rows
+ * that enter the layer, in one pass:
+ *   h = x + residual,  y = bf16(h * rsqrt(mean(h^2) + eps) * weight),
+ *   (codes, scales) = kmoe_quantize_mx(y, KMOE_MXFP8_E4M3)
+ * Sums and products are fp32; y is computed from the unrounded h; the stored h
+ * is rounded once to the stream's type.  The codes are bit for bit those
+ * kmoe_quantize_mx gives for the y of the same call, so kmoe_forward_mx on
+ * them equals kmoe_forward on y.
+ *   x [T, H] bf16; residual [T, H] of the stream's type, or null (h = x);
+ *   weight [H]; h [T, H] of the stream's type (out, or null; needs residual;
+ *   may be residual itself); y [T, H] bf16 (out, or null); codes [T, H] and
+ *   scales [T, H/32] uint8 (out, both or neither, H a multiple of 32).  At
+ *   least one output; no other outputs overlap an input.  H <= 32768, any
+ *   H >= 1 without codes.  codes 16-byte aligned, everything else aligned to
+ *   its elements (rows that are 16-byte aligned throughout run faster).
+ *   eps finite and >= 0. */
+int kmoe_rmsnorm(const void* x_bf16, const void* residual, const void* weight, int T, int H, float eps, uint32_t flags,
+                 void* h, void* y_bf16, uint8_t* codes, uint8_t* scales, cudaStream_t stream);
+
+/* Gradient of kmoe_rmsnorm.  With n = h * rsqrt(mean(h^2) + eps) and
+ * g = dy * weight:
+ *   dh = dh_in + rsqrt(mean(h^2) + eps) * (g - n * mean(g * n))
+ *   dweight = sum over rows of dy * n
+ * dh is the gradient of x and of residual alike; dh_in (null: 0) is what the
+ * stored h received elsewhere (the residual connection).  The factor is
+ * recomputed from the stored h.  dweight is summed in a fixed order that
+ * depends only on (T, H).
+ *   dy [T, H] bf16; h, dh_in, dh [T, H] of the stream's type; weight [H];
+ *   dh (out) may be dh_in itself; dweight [H] float (out, written even for
+ *   T = 0: zeros).  H <= 32768.  workspace: kmoe_rmsnorm_workspace_size(T, H)
+ *   bytes of device memory (0 for invalid sizes), 256-byte aligned. */
+size_t kmoe_rmsnorm_workspace_size(int T, int H);
+int kmoe_rmsnorm_backward(const void* dy_bf16, const void* h, const void* weight, const void* dh_in, int T, int H,
+                          float eps, uint32_t flags, void* dh, float* dweight, void* workspace, size_t ws_bytes,
+                          cudaStream_t stream);
+
+/* Parameters of kmoe_route_grouped and kmoe_route_backward (host struct). */
+#define KMOE_ROUTE_SOFTMAX 1u      /* softmax scores over all E experts; sigmoid without the flag */
+#define KMOE_ROUTE_RENORMALIZE 2u  /* divide the chosen scores by their sum */
+typedef struct kmoe_route_params {
+  int T;           /* tokens, >= 0 */
+  int E;           /* experts, 1..1024, a multiple of n_group */
+  int k;           /* experts per token, 1..min(32, topk_group * E / n_group) */
+  int n_group;     /* groups of E / n_group consecutive experts, 1..32 */
+  int topk_group;  /* groups whose experts can be chosen, 1..n_group */
+  uint32_t flags;  /* KMOE_ROUTE_* */
+  float scale;     /* factor of the weights (routed_scaling_factor), finite */
+} kmoe_route_params;
+
+/* Routing with score functions and groups (the pages name a grouped top-k
+ * beside the plain one of kmoe_route).
+ *   score[e]  = sigmoid(logit[e]) or softmax(logits)[e]
+ *   key[e]    = fp32(score[e]) + bias[e] (one fp32 add; the score rounded once,
+ *               as kmoe_route's), or, without a bias, the logit itself (it has
+ *               the scores' order)
+ *   group     = the sum of its two largest keys (the one key, where only one
+ *               expert can be chosen), or, without a bias, its largest key
+ * The topk_group best groups are kept, the k largest keys among their experts
+ * are chosen; equal groups and keys go to the lower index; slot j holds the
+ * j-th largest key.
+ *   topk_w[t, j] = scale * s_j / sum_j' s_j' with KMOE_ROUTE_RENORMALIZE,
+ *   scale * s_j without
+ * (a few fp32 units in the last place; 0 where the sum is 0).  An expert whose
+ * logit is -inf or NaN, or whose key is, cannot be chosen (and is no part of
+ * the softmax); slots that stay empty get id -1 and weight 0, which the
+ * forward skips.  A +inf logit takes the softmax's whole weight.
+ *   logits [T, E] float; bias [E] float or null; topk_ids [T, k] int32 (out),
+ *   topk_w [T, k] float (out). */
+int kmoe_route_grouped(const kmoe_route_params* p, const float* logits, const float* bias, int32_t* topk_ids,
+                       float* topk_w, cudaStream_t stream);
+
+/* Gradient of topk_w with respect to the logits, for the ids that were chosen
+ * (the choice itself and the bias have none):
+ *   d_logits[t, e] = sum_j d_w[t, j] * d topk_w[t, j] / d logit[t, e]
+ * with the scores recomputed from the logits.  Slots with an id outside
+ * [0, E) take no part (their d_w is not read).  Every element of d_logits is
+ * written; n_group and topk_group are checked but play no part.
+ *   d_w [T, k] float, logits [T, E] float, topk_ids [T, k] int32, d_logits
+ *   [T, E] float (out). */
+int kmoe_route_backward(const kmoe_route_params* p, const float* d_w, const float* logits, const int32_t* topk_ids,
+                        float* d_logits, cudaStream_t stream);
+
+/* Gradient of the combine with respect to the routing weights:
+ *   d_w[t, j] = routed_scaling_factor * sum_h d_out[t, h] * y[t*k + j, h]
+ * and 0 for slots with an id outside [0, E) (their y rows are not read).
+ *   d_out [T, H] bf16, 8-byte aligned; y [T*k, H] float in slot order, 16-byte
+ *   aligned: the stage tensor that a forward leaves in its workspace
+ *   (kmoe_ws_layout.y, valid until the next call on that workspace); topk_ids
+ *   [T, k] int32; d_w [T, k] float (out).  H a multiple of 4, E <= 1024,
+ *   k <= min(E, 32). */
+int kmoe_combine_backward(const void* d_out_bf16, const float* y, const int32_t* topk_ids, int T, int H, int k, int E,
+                          float routed_scaling_factor, float* d_w, cudaStream_t stream);
+
+/* kmoe_forward on rows that are quantised already (kmoe_rmsnorm's codes and
+ * scales, or kmoe_quantize_mx's E4M3 output): x_codes [T, H] uint8, 16-byte
+ * aligned, x_scales [T, H/32] uint8, 4-byte aligned, both token-major.  The
+ * codes are finite E4M3 and the scale bytes below 0xFF, as those two write
+ * them.  Routing is given (topk_ids, topk_w as for kmoe_forward).  The result
+ * equals kmoe_forward's on the bf16 rows that the codes were made from, bit
+ * for bit. */
+int kmoe_forward_mx(const kmoe_params* p, const uint8_t* x_codes, const uint8_t* x_scales, const int32_t* topk_ids,
+                    const float* topk_w, const uint8_t* w13_k, const uint8_t* w2_k, void* out_bf16, void* workspace,
+                    size_t ws_bytes, cudaStream_t stream);
+
 /* Reads the device error word of `workspace` (synchronises `stream`), clears
  * it, and returns KMOE_OK, KMOE_ERR_TIMEOUT or KMOE_ERR_DEVICE.  *word (host,
  * may be null) receives the raw bits (1: a bounded wait timed out, 2: an

@@ -27,7 +27,9 @@ EXPORTS = ("kmoe_status_string", "kmoe_check_device", "kmoe_workspace_size", "km
            "kmoe_route", "kmoe_quantize_mx", "kmoe_prepared_weight_bytes", "kmoe_prepare_weights",
            "kmoe_forward", "kmoe_forward_ex", "kmoe_device_error", "kmoe_tile_sf_offset",
            "kmoe_selftest_wait_timeout", "kmoe_forward_noalloc", "kmoe_mma_peak_run",
-           "kmoe_router_workspace_size", "kmoe_router", "kmoe_forward_router", "kmoe_selftest_activation")
+           "kmoe_router_workspace_size", "kmoe_router", "kmoe_forward_router", "kmoe_selftest_activation",
+           "kmoe_rmsnorm", "kmoe_rmsnorm_workspace_size", "kmoe_rmsnorm_backward", "kmoe_route_grouped",
+           "kmoe_route_backward", "kmoe_combine_backward", "kmoe_forward_mx")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -45,6 +47,11 @@ class kmoe_ws_layout(ctypes.Structure):
                 ("logits", ctypes.c_size_t), ("tile_start_big", ctypes.c_size_t), ("xsf_big", ctypes.c_size_t),
                 ("isf_big", ctypes.c_size_t), ("tile_rows_big", ctypes.c_int), ("max_tiles_big", ctypes.c_int),
                 ("big_rows", ctypes.c_int)]
+
+
+class kmoe_route_params(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("E", ctypes.c_int), ("k", ctypes.c_int), ("n_group", ctypes.c_int),
+                ("topk_group", ctypes.c_int), ("flags", ctypes.c_uint32), ("scale", ctypes.c_float)]
 
 
 class kmoe_stage_events(ctypes.Structure):
@@ -96,6 +103,19 @@ def load_library(path: str = LIB_PATH):
     lib.kmoe_router.argtypes = [P, P, P, I, I, I, I, P, P, P, P, S, V]
     lib.kmoe_forward_router.argtypes = [pp, P, P, P, P, P, P, P, S, V, ctypes.POINTER(kmoe_stage_events)]
     lib.kmoe_selftest_activation.argtypes = [pp, P, P, I, P, V]
+    F, U = ctypes.c_float, ctypes.c_uint32
+    rp = ctypes.POINTER(kmoe_route_params)
+    lib.kmoe_rmsnorm.argtypes = [P, P, P, I, I, F, U, P, P, P, P, V]
+    lib.kmoe_rmsnorm_workspace_size.restype = S
+    lib.kmoe_rmsnorm_workspace_size.argtypes = [I, I]
+    lib.kmoe_rmsnorm_backward.argtypes = [P, P, P, P, I, I, F, U, P, P, P, S, V]
+    lib.kmoe_route_grouped.argtypes = [rp, P, P, P, P, V]
+    lib.kmoe_route_backward.argtypes = [rp, P, P, P, P, V]
+    lib.kmoe_combine_backward.argtypes = [P, P, P, I, I, I, I, F, P, V]
+    lib.kmoe_forward_mx.argtypes = [pp, P, P, P, P, P, P, P, P, S, V]
+    for n in ("kmoe_rmsnorm", "kmoe_rmsnorm_backward", "kmoe_route_grouped", "kmoe_route_backward",
+              "kmoe_combine_backward", "kmoe_forward_mx"):
+        getattr(lib, n).restype = ctypes.c_int
     for n in ("kmoe_check_device", "kmoe_workspace_layout", "kmoe_route", "kmoe_quantize_mx",
               "kmoe_prepare_weights", "kmoe_forward", "kmoe_forward_ex", "kmoe_device_error",
               "kmoe_selftest_wait_timeout", "kmoe_router", "kmoe_forward_router", "kmoe_selftest_activation"):
@@ -349,6 +369,207 @@ def kmoe_forward_noalloc(p, x, logits, bias, w13_k, w2_k, topk_ids=None, topk_w=
         ctypes.byref(p), _ptr(x), _ptr(logits), _ptr(bias), _ptr(w13_k), _ptr(w2_k), _ptr(topk_ids), _ptr(topk_w),
         _ptr(out), _ptr(device_error), _stream(stream)))
     return out
+
+
+def kmoe_forward_mx(p, x_codes, x_scales, topk_ids, topk_w, w13_k, w2_k, out=None, workspace=None, stream=None):
+    """kmoe_forward on rows quantised before (kmoe_rmsnorm's or
+    kmoe_quantize_mx's codes [T, H] and scales [T, H/32]), routing given."""
+    dev = _args(stream, ("x_codes", x_codes, torch.uint8, (p.T, p.H)), ("x_scales", x_scales, torch.uint8, (p.T, p.H // 32)),
+                ("topk_ids", topk_ids, torch.int32, (p.T, p.k)), ("topk_w", topk_w, torch.float32, (p.T, p.k)),
+                ("out", out, torch.bfloat16, (p.T, p.H)))
+    _arg(w13_k, "w13_k", torch.uint8, min_bytes=kmoe_prepared_weight_bytes(p, 0))
+    _arg(w2_k, "w2_k", torch.uint8, min_bytes=kmoe_prepared_weight_bytes(p, 1))
+    _arg(workspace, "workspace", torch.uint8, min_bytes=kmoe_workspace_size(p))
+    _gpu(w13_k=w13_k, w2_k=w2_k, workspace=workspace)
+    if out is None:
+        out = _new((p.T, p.H), torch.bfloat16, dev, stream)
+    if workspace is None:
+        workspace = _new(kmoe_workspace_size(p), torch.uint8, dev, stream)
+    _check("kmoe_forward_mx", _lib.kmoe_forward_mx(
+        ctypes.byref(p), _ptr(x_codes), _ptr(x_scales), _ptr(topk_ids), _ptr(topk_w), _ptr(w13_k), _ptr(w2_k),
+        _ptr(out), _ptr(workspace), _nbytes(workspace), _raw_stream(dev, stream)))
+    return out, workspace
+
+
+# ---- the operators around the experts.  Decode calls are a few microseconds
+# on the GPU, so their argument checks are one pass over the tensors.
+
+def _args(stream, *named):
+    """Checks (name, tensor, dtype, shape) of each argument, None passing, and
+    returns the device.  The errors are _arg's and _gpu's.  A tensor that a
+    given stream uses is kept from reuse until that stream is through."""
+    dev = None
+    for name, t, dtype, shape in named:
+        if t is None:
+            continue
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            _arg(t, name, dtype, shape)
+        if not t.is_cuda:
+            for n, u, d, s in named:
+                _arg(u, n, d, s)
+            _gpu(**{name: t})
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    if stream is not None:
+        for _, t, _, _ in named:
+            if t is not None:
+                t.record_stream(stream)
+    return dev
+
+
+def _raw_stream(dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _new(shape, dtype, dev, stream):
+    """An output or workspace of a call on `stream`: the allocator keeps its
+    memory from reuse until that stream is through with it."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+KMOE_NORM_STREAM_F32 = 1
+KMOE_NORM_WEIGHT_F32 = 2
+_F32_OR_BF16 = (torch.bfloat16, torch.float32)
+
+
+def _type_of(t, name, default):
+    if t is None:
+        return default
+    if t.dtype not in _F32_OR_BF16:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return t.dtype
+
+
+def kmoe_rmsnorm(x, weight, residual=None, eps=1e-6, mx=False, h=None, y=None, codes=None, scales=None, stream=None):
+    """h = x + residual, y = rmsnorm(h) * weight and, with `mx`, the MXFP8 codes
+    and scales of y, in one kernel.  Returns (h, y, codes, scales); h is None
+    without a residual, codes and scales without `mx`.  residual and h are
+    bf16 or fp32 (h may be residual itself), weight bf16 or fp32."""
+    T, H = _rows(x, "x", "H")
+    st = _type_of(residual, "residual", torch.bfloat16)
+    wt = _type_of(weight, "weight", None)
+    if h is not None and residual is None:
+        raise ValueError("h needs a residual")
+    if not mx and (codes is not None or scales is not None):
+        raise ValueError("codes and scales need mx=True")
+    dev = _args(stream, ("x", x, torch.bfloat16, (T, H)), ("weight", weight, wt, (H,)), ("residual", residual, st, (T, H)),
+                ("h", h, st, (T, H)), ("y", y, torch.bfloat16, (T, H)), ("codes", codes, torch.uint8, (T, H)),
+                ("scales", scales, torch.uint8, (T, H // 32)))
+    if h is None and residual is not None:
+        h = _new((T, H), st, dev, stream)
+    if y is None:
+        y = _new((T, H), torch.bfloat16, dev, stream)
+    if mx:
+        if codes is None:
+            codes = _new((T, H), torch.uint8, dev, stream)
+        if scales is None:
+            scales = _new((T, H // 32), torch.uint8, dev, stream)
+    flags = (KMOE_NORM_STREAM_F32 if st is torch.float32 else 0) | (KMOE_NORM_WEIGHT_F32 if wt is torch.float32 else 0)
+    _check("kmoe_rmsnorm", _lib.kmoe_rmsnorm(_at(x), _at(residual), _at(weight), T, H, eps, flags, _at(h),
+                                             _at(y), _at(codes), _at(scales), _raw_stream(dev, stream)))
+    return h, y, codes, scales
+
+
+def kmoe_rmsnorm_workspace_size(T: int, H: int) -> int:
+    return _lib.kmoe_rmsnorm_workspace_size(T, H)
+
+
+def kmoe_rmsnorm_backward(dy, h, weight, dh_in=None, eps=1e-6, dh=None, dweight=None, workspace=None, stream=None):
+    """Gradient of kmoe_rmsnorm at the stored h: (dh, dweight), dh of h's type
+    (the gradient of x and of residual alike, with dh_in added), dweight fp32.
+    dh may be dh_in itself."""
+    T, H = _rows(h, "h", "H")
+    st = _type_of(h, "h", None)
+    wt = _type_of(weight, "weight", None)
+    dev = _args(stream, ("dy", dy, torch.bfloat16, (T, H)), ("h", h, st, (T, H)), ("weight", weight, wt, (H,)),
+                ("dh_in", dh_in, st, (T, H)), ("dh", dh, st, (T, H)), ("dweight", dweight, torch.float32, (H,)))
+    n = _lib.kmoe_rmsnorm_workspace_size(T, H)
+    if workspace is None:
+        workspace = _new(max(n, 1), torch.uint8, dev, stream)
+    else:
+        _arg(workspace, "workspace", torch.uint8, min_bytes=n)
+        _gpu(workspace=workspace)
+    if dh is None:
+        dh = _new((T, H), st, dev, stream)
+    if dweight is None:
+        dweight = _new((H,), torch.float32, dev, stream)
+    flags = (KMOE_NORM_STREAM_F32 if st is torch.float32 else 0) | (KMOE_NORM_WEIGHT_F32 if wt is torch.float32 else 0)
+    _check("kmoe_rmsnorm_backward", _lib.kmoe_rmsnorm_backward(
+        _at(dy), _at(h), _at(weight), _at(dh_in), T, H, eps, flags, _at(dh),
+        _at(dweight), _at(workspace), workspace.numel(), _raw_stream(dev, stream)))
+    return dh, dweight
+
+
+KMOE_ROUTE_SOFTMAX = 1
+KMOE_ROUTE_RENORMALIZE = 2
+_SCORES = {"sigmoid": 0, "softmax": KMOE_ROUTE_SOFTMAX}
+
+
+def _route_params(T, E, k, n_group, topk_group, score, renormalize, scale):
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'sigmoid' or 'softmax', got {score!r}")
+    return kmoe_route_params(T, E, k, n_group, topk_group,
+                             _SCORES[score] | (KMOE_ROUTE_RENORMALIZE if renormalize else 0), scale)
+
+
+def kmoe_route_grouped(logits, bias, k, score="sigmoid", n_group=1, topk_group=1, renormalize=True, scale=1.0,
+                       topk_ids=None, topk_w=None, stream=None):
+    """Top-k routing with sigmoid or softmax scores, an optional balance bias
+    (None: the logits choose), `topk_group` of `n_group` expert groups and
+    optionally renormalised weights.  Returns (topk_ids, topk_w); slots no
+    expert could fill hold id -1 and weight 0."""
+    T, E = _rows(logits, "logits", "E")
+    dev = _args(stream, ("logits", logits, torch.float32, (T, E)), ("bias", bias, torch.float32, (E,)),
+                ("topk_ids", topk_ids, torch.int32, (T, k)), ("topk_w", topk_w, torch.float32, (T, k)))
+    p = _route_params(T, E, k, n_group, topk_group, score, renormalize, scale)
+    if topk_ids is None:
+        topk_ids = _new((T, k), torch.int32, dev, stream)
+    if topk_w is None:
+        topk_w = _new((T, k), torch.float32, dev, stream)
+    _check("kmoe_route_grouped", _lib.kmoe_route_grouped(p, _at(logits), _at(bias), _at(topk_ids),
+                                                         _at(topk_w), _raw_stream(dev, stream)))
+    return topk_ids, topk_w
+
+
+def kmoe_route_backward(d_w, logits, topk_ids, score="sigmoid", renormalize=True, scale=1.0, d_logits=None,
+                        stream=None):
+    """Gradient of the routing weights with respect to the logits: d_logits
+    fp32 [T, E], dense, for the ids that were chosen."""
+    T, E = _rows(logits, "logits", "E")
+    k = _rows(topk_ids, "topk_ids", "k")[1]
+    dev = _args(stream, ("logits", logits, torch.float32, (T, E)), ("d_w", d_w, torch.float32, (T, k)),
+                ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_logits", d_logits, torch.float32, (T, E)))
+    p = _route_params(T, E, k, 1, 1, score, renormalize, scale)
+    if d_logits is None:
+        d_logits = _new((T, E), torch.float32, dev, stream)
+    _check("kmoe_route_backward", _lib.kmoe_route_backward(p, _at(d_w), _at(logits), _at(topk_ids),
+                                                           _at(d_logits), _raw_stream(dev, stream)))
+    return d_logits
+
+
+def kmoe_combine_backward(d_out, y, topk_ids, E, routed_scaling_factor=1.0, d_w=None, stream=None):
+    """Gradient of the combine with respect to the routing weights: fp32
+    [T, k] from d_out bf16 [T, H] and the per-slot outputs y fp32 [T*k, H]
+    that a forward leaves in its workspace (stage_views(p, ws)["y"])."""
+    T, H = _rows(d_out, "d_out", "H")
+    k = _rows(topk_ids, "topk_ids", "k")[1]
+    dev = _args(stream, ("d_out", d_out, torch.bfloat16, (T, H)), ("y", y, torch.float32, (T * k, H)),
+                ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_w", d_w, torch.float32, (T, k)))
+    if d_w is None:
+        d_w = _new((T, k), torch.float32, dev, stream)
+    _check("kmoe_combine_backward", _lib.kmoe_combine_backward(
+        _at(d_out), _at(y), _at(topk_ids), T, H, k, E, routed_scaling_factor, _at(d_w),
+        _raw_stream(dev, stream)))
+    return d_w
 
 
 def kmoe_selftest_activation(p, gate, up, out=None, stream=None):

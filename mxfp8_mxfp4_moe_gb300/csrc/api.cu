@@ -9,6 +9,8 @@
 #include <mutex>
 
 #include "gemm.cuh"
+#include "norm.cuh"
+#include "route_group.cuh"
 #include "router.cuh"
 
 namespace kmoe {
@@ -19,6 +21,11 @@ cudaError_t launch_quant_rows(const void*, int, int, int, uint8_t*, uint8_t*, cu
 cudaError_t launch_quant_scatter(const void*, int, int, int, int, int, int, const int32_t*, const int32_t*,
                                  const int32_t*, const int32_t*, const int32_t*, const int32_t*, const int32_t*,
                                  int32_t*, int32_t*, uint8_t*, uint8_t*, uint8_t*, cudaStream_t, bool);
+cudaError_t launch_mx_scatter(const uint8_t*, const uint8_t*, int, int, int, int, int, int, const int32_t*,
+                              const int32_t*, const int32_t*, const int32_t*, const int32_t*, const int32_t*,
+                              const int32_t*, int32_t*, int32_t*, uint8_t*, uint8_t*, uint8_t*, cudaStream_t, bool);
+cudaError_t launch_combine_backward(const void*, const float*, const int32_t*, int, int, int, int, float, float*,
+                                    cudaStream_t);
 cudaError_t launch_combine(const float*, const int32_t*, const float*, int, int, int, int, float, void*,
                            cudaStream_t, bool);
 cudaError_t launch_wait_selftest(uint32_t* err, uint64_t budget_ns, cudaStream_t st);
@@ -282,11 +289,13 @@ int kmoe_forward(const kmoe_params* p, const void* x_bf16, const float* logits, 
 }
 
 // The forward; routing from given ids/weights, from logits, or (w_gate set)
-// by the fused router from x and the gate weight.
+// by the fused router from x and the gate weight.  The rows are x, or
+// (x_codes set) codes and scales quantised before.
 static int forward_impl(const kmoe_params* p, const void* x_bf16, const float* logits, const void* w_gate,
                         const float* bias, const uint8_t* w13_k, const uint8_t* w2_k, const int32_t* topk_ids,
                         const float* topk_w, void* out_bf16, void* workspace, size_t ws_bytes, cudaStream_t stream,
-                        const kmoe_stage_events* ev) {
+                        const kmoe_stage_events* ev, const uint8_t* x_codes = nullptr,
+                        const uint8_t* x_scales = nullptr) {
   int st = check_params(p);
   if (st != KMOE_OK) return st;
   Layout L;
@@ -300,7 +309,8 @@ static int forward_impl(const kmoe_params* p, const void* x_bf16, const float* l
   if (p->T == 0) return KMOE_OK;
   const bool given = topk_ids != nullptr;
   if ((topk_ids == nullptr) != (topk_w == nullptr)) return KMOE_ERR_ARG;
-  if (!x_bf16 || !w13_k || !w2_k || !out_bf16) return KMOE_ERR_ARG;
+  const bool mx = x_codes != nullptr;
+  if ((!x_bf16 && !mx) || !w13_k || !w2_k || !out_bf16) return KMOE_ERR_ARG;
   if (!given && !w_gate && (!logits || !bias)) return KMOE_ERR_ARG;
   if (!aligned(x_bf16, 16) || !aligned(out_bf16, 16) || !aligned(w13_k, 256) || !aligned(w2_k, 256))
     return KMOE_ERR_ALIGN;
@@ -385,8 +395,12 @@ static int forward_impl(const kmoe_params* p, const void* x_bf16, const float* l
   KMOE_CK(launch_permute(ids, R, E, L.BN, thr, rank, chunk_prefix, counts, seg_start, tile_start, tile_start_big, err,
                          stream, pdl && !given));
   KMOE_CK(mark(ev ? ev->permuted : nullptr));
-  KMOE_CK(launch_quant_scatter(x_bf16, T, H, k, E, L.BN, thr, ids, rank, chunk_prefix, counts, seg_start, tile_start,
-                               tile_start_big, row_of_slot, slot_of_row, xq, xsf, xsf_big, stream, pdl));
+  if (mx)
+    KMOE_CK(launch_mx_scatter(x_codes, x_scales, T, H, k, E, L.BN, thr, ids, rank, chunk_prefix, counts, seg_start,
+                              tile_start, tile_start_big, row_of_slot, slot_of_row, xq, xsf, xsf_big, stream, pdl));
+  else
+    KMOE_CK(launch_quant_scatter(x_bf16, T, H, k, E, L.BN, thr, ids, rank, chunk_prefix, counts, seg_start,
+                                 tile_start, tile_start_big, row_of_slot, slot_of_row, xq, xsf, xsf_big, stream, pdl));
   KMOE_CK(mark(ev ? ev->quantized : nullptr));
   const int grid = num_sms();
   if (grid <= 0) return KMOE_ERR_CUDA;
@@ -441,6 +455,16 @@ int kmoe_forward_router(const kmoe_params* p, const void* x_bf16, const void* w_
                       ws_bytes, stream, ev);
 }
 
+int kmoe_forward_mx(const kmoe_params* p, const uint8_t* x_codes, const uint8_t* x_scales, const int32_t* topk_ids,
+                    const float* topk_w, const uint8_t* w13_k, const uint8_t* w2_k, void* out_bf16, void* workspace,
+                    size_t ws_bytes, cudaStream_t stream) {
+  if (!p) return KMOE_ERR_ARG;
+  if (p->T > 0 && (!x_codes || !x_scales || !topk_ids || !topk_w)) return KMOE_ERR_ARG;
+  if (p->T > 0 && (!aligned(x_codes, 16) || !aligned(x_scales, 4))) return KMOE_ERR_ALIGN;
+  return forward_impl(p, nullptr, nullptr, nullptr, nullptr, w13_k, w2_k, topk_ids, topk_w, out_bf16, workspace,
+                      ws_bytes, stream, nullptr, x_codes, x_scales);
+}
+
 size_t kmoe_router_workspace_size(int T, int H, int E) {
   if (T < 0 || H <= 0 || H % 64 != 0 || E <= 0 || E > kMaxE) return 0;
   const RouterPlan rp = plan_router(T, H, E);
@@ -464,6 +488,101 @@ int kmoe_router(const void* x_bf16, const void* w_gate_bf16, const float* bias, 
   float* part = reinterpret_cast<float*>(ws + 256 + align_up(router_sync_bytes(rp), 256));
   return run_router(x_bf16, w_gate_bf16, bias, T, H, E, k, logits, part, topk_ids, topk_w,
                     reinterpret_cast<int*>(ws + 256), err, stream);
+}
+
+// Type and alignment of the norm's arguments: flags, and element alignment of
+// the stream (residual, h and their gradients) and of the weight.
+static int check_norm(int T, int H, float eps, uint32_t flags) {
+  if (T < 0 || H <= 0 || !(eps >= 0.f) || !std::isfinite(eps)) return KMOE_ERR_ARG;
+  if ((flags & ~(KMOE_NORM_STREAM_F32 | KMOE_NORM_WEIGHT_F32)) != 0u) return KMOE_ERR_ARG;
+  if (H > kMaxNormH) return KMOE_ERR_SHAPE;
+  return KMOE_OK;
+}
+
+int kmoe_rmsnorm(const void* x_bf16, const void* residual, const void* weight, int T, int H, float eps, uint32_t flags,
+                 void* h, void* y_bf16, uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
+  const int st = check_norm(T, H, eps, flags);
+  if (st != KMOE_OK) return st;
+  if ((codes == nullptr) != (scales == nullptr) || (h && !residual)) return KMOE_ERR_ARG;
+  if (codes && H % 32 != 0) return KMOE_ERR_SHAPE;
+  if (T == 0) return KMOE_OK;
+  if (!x_bf16 || !weight || (!h && !y_bf16 && !codes)) return KMOE_ERR_ARG;
+  const bool sf = (flags & KMOE_NORM_STREAM_F32) != 0u, wf = (flags & KMOE_NORM_WEIGHT_F32) != 0u;
+  if (!aligned(x_bf16, 2) || !aligned(residual, sf ? 4 : 2) || !aligned(h, sf ? 4 : 2) || !aligned(y_bf16, 2) ||
+      !aligned(weight, wf ? 4 : 2) || (codes && !aligned(codes, 16)))
+    return KMOE_ERR_ALIGN;
+  KMOE_CK(launch_rmsnorm(x_bf16, residual, weight, T, H, eps, sf, wf, h, y_bf16, codes, scales, stream));
+  return KMOE_OK;
+}
+
+size_t kmoe_rmsnorm_workspace_size(int T, int H) {
+  if (T < 0 || H <= 0 || H > kMaxNormH) return 0;
+  return 256 + align_up(norm_part_bytes(T, H), 256);
+}
+
+int kmoe_rmsnorm_backward(const void* dy_bf16, const void* h, const void* weight, const void* dh_in, int T, int H,
+                          float eps, uint32_t flags, void* dh, float* dweight, void* workspace, size_t ws_bytes,
+                          cudaStream_t stream) {
+  const int st = check_norm(T, H, eps, flags);
+  if (st != KMOE_OK) return st;
+  if (!workspace || ws_bytes < kmoe_rmsnorm_workspace_size(T, H)) return KMOE_ERR_WORKSPACE;
+  if (!dweight || (T > 0 && (!dy_bf16 || !h || !weight || !dh))) return KMOE_ERR_ARG;
+  const bool sf = (flags & KMOE_NORM_STREAM_F32) != 0u, wf = (flags & KMOE_NORM_WEIGHT_F32) != 0u;
+  const uintptr_t sa = sf ? 4 : 2;
+  if (!aligned(workspace, 256) || !aligned(dweight, 4) || !aligned(dy_bf16, 2) || !aligned(h, sa) ||
+      !aligned(dh_in, sa) || !aligned(dh, sa) || !aligned(weight, wf ? 4 : 2))
+    return KMOE_ERR_ALIGN;
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  KMOE_CK(launch_rmsnorm_backward(dy_bf16, h, weight, dh_in, T, H, eps, sf, wf, dh, dweight, part, stream));
+  return KMOE_OK;
+}
+
+static int route_args(const kmoe_route_params* p, RouteGroupArgs* a) {
+  if (!p || p->T < 0 || p->E <= 0 || p->E > kMaxE || p->k <= 0 || p->k > p->E || p->k > kMaxK) return KMOE_ERR_ARG;
+  if (p->n_group <= 0 || p->n_group > kMaxGroups || p->topk_group <= 0 || p->topk_group > p->n_group)
+    return KMOE_ERR_ARG;
+  if ((p->flags & ~(KMOE_ROUTE_SOFTMAX | KMOE_ROUTE_RENORMALIZE)) != 0u || !std::isfinite(p->scale))
+    return KMOE_ERR_ARG;
+  if (p->E % p->n_group != 0 || p->topk_group * (p->E / p->n_group) < p->k) return KMOE_ERR_SHAPE;
+  if (static_cast<long long>(p->T) * p->k >= (1LL << 31)) return KMOE_ERR_SHAPE;
+  *a = RouteGroupArgs{p->T, p->E, p->k, p->n_group, p->topk_group, (p->flags & KMOE_ROUTE_SOFTMAX) != 0u,
+                      (p->flags & KMOE_ROUTE_RENORMALIZE) != 0u, p->scale};
+  return KMOE_OK;
+}
+
+int kmoe_route_grouped(const kmoe_route_params* p, const float* logits, const float* bias, int32_t* topk_ids,
+                       float* topk_w, cudaStream_t stream) {
+  RouteGroupArgs a;
+  const int st = route_args(p, &a);
+  if (st != KMOE_OK) return st;
+  if (a.T == 0) return KMOE_OK;
+  if (!logits || !topk_ids || !topk_w) return KMOE_ERR_ARG;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4)) return KMOE_ERR_ALIGN;
+  KMOE_CK(launch_route_grouped(logits, bias, a, topk_ids, topk_w, stream));
+  return KMOE_OK;
+}
+
+int kmoe_route_backward(const kmoe_route_params* p, const float* d_w, const float* logits, const int32_t* topk_ids,
+                        float* d_logits, cudaStream_t stream) {
+  RouteGroupArgs a;
+  const int st = route_args(p, &a);
+  if (st != KMOE_OK) return st;
+  if (a.T == 0) return KMOE_OK;
+  if (!d_w || !logits || !topk_ids || !d_logits) return KMOE_ERR_ARG;
+  if (!aligned(d_w, 4) || !aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(d_logits, 4)) return KMOE_ERR_ALIGN;
+  KMOE_CK(launch_route_backward(d_w, logits, topk_ids, a, d_logits, stream));
+  return KMOE_OK;
+}
+
+int kmoe_combine_backward(const void* d_out_bf16, const float* y, const int32_t* topk_ids, int T, int H, int k, int E,
+                          float routed_scaling_factor, float* d_w, cudaStream_t stream) {
+  if (T < 0 || H <= 0 || E <= 0 || E > kMaxE || k <= 0 || k > E || k > kMaxK) return KMOE_ERR_ARG;
+  if (H % 4 != 0 || static_cast<long long>(T) * k >= (1LL << 31)) return KMOE_ERR_SHAPE;
+  if (T == 0) return KMOE_OK;
+  if (!d_out_bf16 || !y || !topk_ids || !d_w) return KMOE_ERR_ARG;
+  if (!aligned(d_out_bf16, 8) || !aligned(y, 16) || !aligned(topk_ids, 4) || !aligned(d_w, 4)) return KMOE_ERR_ALIGN;
+  KMOE_CK(launch_combine_backward(d_out_bf16, y, topk_ids, T, H, k, E, routed_scaling_factor, d_w, stream));
+  return KMOE_OK;
 }
 
 int kmoe_device_error(void* workspace, uint32_t* word, cudaStream_t stream) {

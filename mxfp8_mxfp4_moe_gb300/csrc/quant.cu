@@ -9,11 +9,12 @@
 //   quant_scatter_kernel  forward path: codes of token t written to each of
 //                         its k expert-sorted rows, scales in the token-tile
 //                         layout the GEMM copies into TMEM
+//   mx_scatter_kernel     the same rows from codes and scales quantised
+//                         before (kmoe_forward_mx)
 #include <cuda_bf16.h>
 #include <cuda_fp4.h>
-#include <cuda_fp8.h>
 
-#include "common.cuh"
+#include "mx_dev.cuh"
 
 namespace kmoe {
 
@@ -36,11 +37,6 @@ __device__ __forceinline__ float group_amax(const float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) a = fmaxf(a, fabsf(v[i]));  // fmaxf drops NaN
   return a;
-}
-
-__device__ __forceinline__ uint8_t e4m3_code(float x, float inv_scale) {
-  if (isnan(x)) return 0;
-  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x * inv_scale, __NV_SATFINITE, __NV_E4M3));
 }
 
 // 32 E4M3 codes of a group, packed little-endian into 8 words
@@ -105,6 +101,46 @@ cudaError_t launch_quant_rows(const void* x, int rows, int cols, int fmt, uint8_
   return cudaGetLastError();
 }
 
+// Where the k routed copies of one token go: expert-sorted row, token tile,
+// row inside the tile and tile class of each slot.
+struct SlotRows {
+  int row[kMaxK], tile[kMaxK], local[kMaxK], big[kMaxK];
+};
+
+// Threads 0..k-1 resolve token t's slots into `s` and record the permutation;
+// the block is synchronised before it returns.
+__device__ __forceinline__ void resolve_slots(SlotRows& s, int t, int k, int E, int BN, int thr,
+                                              const int32_t* __restrict__ ids, const int32_t* __restrict__ rank,
+                                              const int32_t* __restrict__ chunk_prefix,
+                                              const int32_t* __restrict__ counts,
+                                              const int32_t* __restrict__ seg_start,
+                                              const int32_t* __restrict__ tile_start,
+                                              const int32_t* __restrict__ tile_start_big,
+                                              int32_t* __restrict__ row_of_slot, int32_t* __restrict__ slot_of_row) {
+  if (threadIdx.x < k) {
+    const int j = threadIdx.x;
+    const int sl = t * k + j;
+    const int id = ids[sl];
+    int row = -1, tile = -1, local = -1, big = 0;
+    if (id >= 0 && id < E) {
+      const int c = sl / kRankChunk;
+      const int in_seg = chunk_prefix[static_cast<size_t>(c) * E + id] + rank[sl];
+      row = seg_start[id] + in_seg;
+      big = counts[id] > thr;
+      const int bn = big ? kBigTileRows : BN;
+      tile = (big ? tile_start_big[id] : tile_start[id]) + in_seg / bn;
+      local = in_seg % bn;
+      slot_of_row[row] = sl;
+    }
+    row_of_slot[sl] = row;
+    s.row[j] = row;
+    s.tile[j] = tile;
+    s.local[j] = local;
+    s.big[j] = big;
+  }
+  __syncthreads();
+}
+
 // One block per token.  Threads 0..k-1 first resolve the token's k slots to
 // expert-sorted rows and token tiles (of the expert's tile class: BN rows for
 // experts with at most `thr` rows, kBigTileRows rows and the xsf_big scale
@@ -123,30 +159,10 @@ __global__ void __launch_bounds__(256) quant_scatter_kernel(
     const int32_t* __restrict__ tile_start_big, int32_t* __restrict__ row_of_slot, int32_t* __restrict__ slot_of_row,
     uint8_t* __restrict__ xq, uint8_t* __restrict__ xsf, uint8_t* __restrict__ xsf_big) {
   chain_wait();
-  __shared__ int s_row[kMaxK], s_tile[kMaxK], s_local[kMaxK], s_big[kMaxK];
+  __shared__ SlotRows s;
   const int t = blockIdx.x;
-  if (threadIdx.x < k) {
-    const int j = threadIdx.x;
-    const int s = t * k + j;
-    const int id = ids[s];
-    int row = -1, tile = -1, local = -1, big = 0;
-    if (id >= 0 && id < E) {
-      const int c = s / kRankChunk;
-      const int in_seg = chunk_prefix[static_cast<size_t>(c) * E + id] + rank[s];
-      row = seg_start[id] + in_seg;
-      big = counts[id] > thr;
-      const int bn = big ? kBigTileRows : BN;
-      tile = (big ? tile_start_big[id] : tile_start[id]) + in_seg / bn;
-      local = in_seg % bn;
-      slot_of_row[row] = s;
-    }
-    row_of_slot[s] = row;
-    s_row[j] = row;
-    s_tile[j] = tile;
-    s_local[j] = local;
-    s_big[j] = big;
-  }
-  __syncthreads();
+  resolve_slots(s, t, k, E, BN, thr, ids, rank, chunk_prefix, counts, seg_start, tile_start, tile_start_big,
+                row_of_slot, slot_of_row);
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int gpr = H / 32;  // a multiple of 4: quads are wholly in or out of range
   const int KB = H / 128;
@@ -182,15 +198,15 @@ __global__ void __launch_bounds__(256) quant_scatter_kernel(
     sc |= __shfl_xor_sync(0xffffffffu, sc, 1);
     sc |= __shfl_xor_sync(0xffffffffu, sc, 2);
     for (int j = 0; j < k; ++j) {
-      const int row = s_row[j];
+      const int row = s.row[j];
       if (row < 0) continue;
       uint4* run = reinterpret_cast<uint4*>(xq + static_cast<size_t>(row) * H + 32 * gw);
       if (st0) run[lane] = v0;
       if (st1) run[32 + lane] = v1;
       if (active && (g & 3) == 0) {
         // small tiles (at most 64 rows) hold one 128-row scale chunk, big tiles two
-        uint8_t* base = s_big[j] ? xsf_big : xsf;
-        *reinterpret_cast<uint32_t*>(base + tile_sf_offset(s_tile[j], s_local[j], g, s_big[j] ? 2 : 1, KB)) = sc;
+        uint8_t* base = s.big[j] ? xsf_big : xsf;
+        *reinterpret_cast<uint32_t*>(base + tile_sf_offset(s.tile[j], s.local[j], g, s.big[j] ? 2 : 1, KB)) = sc;
       }
     }
   }
@@ -205,6 +221,50 @@ cudaError_t launch_quant_scatter(const void* x, int T, int H, int k, int E, int 
   return launch_chained(quant_scatter_kernel, dim3(T), dim3(256), 0, st, pdl, static_cast<const __nv_bfloat16*>(x),
                         H, k, E, BN, thr, ids, rank, chunk_prefix, counts, seg_start, tile_start, tile_start_big,
                         row_of_slot, slot_of_row, xq, xsf, xsf_big);
+}
+
+// quant_scatter_kernel's writes from rows that are quantised already: codes
+// [T, H] and scales [T, H/32] token-major.  Moves bytes only: each thread
+// loads 16 codes once and stores them to every routed row; a 128-wide K
+// block's four scale bytes are one 32-bit word in both layouts.
+__global__ void __launch_bounds__(256) mx_scatter_kernel(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int H, int k, int E, int BN, int thr,
+    const int32_t* __restrict__ ids, const int32_t* __restrict__ rank, const int32_t* __restrict__ chunk_prefix,
+    const int32_t* __restrict__ counts, const int32_t* __restrict__ seg_start, const int32_t* __restrict__ tile_start,
+    const int32_t* __restrict__ tile_start_big, int32_t* __restrict__ row_of_slot, int32_t* __restrict__ slot_of_row,
+    uint8_t* __restrict__ xq, uint8_t* __restrict__ xsf, uint8_t* __restrict__ xsf_big) {
+  chain_wait();
+  __shared__ SlotRows s;
+  const int t = blockIdx.x;
+  resolve_slots(s, t, k, E, BN, thr, ids, rank, chunk_prefix, counts, seg_start, tile_start, tile_start_big,
+                row_of_slot, slot_of_row);
+  const uint4* src = reinterpret_cast<const uint4*>(codes + static_cast<size_t>(t) * H);
+  for (int i = threadIdx.x; i < H / 16; i += blockDim.x) {
+    const uint4 v = __ldg(src + i);
+    for (int j = 0; j < k; ++j)
+      if (s.row[j] >= 0) reinterpret_cast<uint4*>(xq + static_cast<size_t>(s.row[j]) * H)[i] = v;
+  }
+  const int KB = H / 128;
+  const uint32_t* sf = reinterpret_cast<const uint32_t*>(scales + static_cast<size_t>(t) * (H / 32));
+  for (int kb = threadIdx.x; kb < KB; kb += blockDim.x) {
+    const uint32_t v = __ldg(sf + kb);
+    for (int j = 0; j < k; ++j) {
+      if (s.row[j] < 0) continue;
+      uint8_t* base = s.big[j] ? xsf_big : xsf;
+      *reinterpret_cast<uint32_t*>(base + tile_sf_offset(s.tile[j], s.local[j], 4 * kb, s.big[j] ? 2 : 1, KB)) = v;
+    }
+  }
+}
+
+cudaError_t launch_mx_scatter(const uint8_t* codes, const uint8_t* scales, int T, int H, int k, int E, int BN, int thr,
+                              const int32_t* ids, const int32_t* rank, const int32_t* chunk_prefix,
+                              const int32_t* counts, const int32_t* seg_start, const int32_t* tile_start,
+                              const int32_t* tile_start_big, int32_t* row_of_slot, int32_t* slot_of_row, uint8_t* xq,
+                              uint8_t* xsf, uint8_t* xsf_big, cudaStream_t st, bool pdl) {
+  if (T == 0) return cudaSuccess;
+  return launch_chained(mx_scatter_kernel, dim3(T), dim3(256), 0, st, pdl, codes, scales, H, k, E, BN, thr, ids, rank,
+                        chunk_prefix, counts, seg_start, tile_start, tile_start_big, row_of_slot, slot_of_row, xq, xsf,
+                        xsf_big);
 }
 
 }  // namespace kmoe
