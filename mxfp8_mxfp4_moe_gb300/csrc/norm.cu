@@ -1,168 +1,204 @@
 // Root-mean-square norm of the rows that enter the expert layer, with the
-// residual's addition in front and the MXFP8 quantisation behind it, and its
-// gradient.
+// residual's addition in front and the MXFP8 quantisation behind it.
 //   h = x + r,  y = bf16(h * rstd * w),  rstd = (mean(h^2) + eps)^-1/2,
 // sums and products in fp32; y comes from the unrounded h, the stored h is
 // rounded once to the stream's type.  The codes are those of the bf16 row y
 // (not of the fp32 product), so that a layer fed with them gives what the
 // layer fed with y gives, bit for bit.
-#include <cuda_bf16.h>
-
-#include "mx_dev.cuh"
-#include "norm.cuh"
+#include "norm_dev.cuh"
 
 namespace kmoe {
 
-__device__ __forceinline__ float load_f(const float* p, size_t i) { return p[i]; }
-__device__ __forceinline__ float load_f(const __nv_bfloat16* p, size_t i) { return __bfloat162float(p[i]); }
-__device__ __forceinline__ void store_f(float* p, size_t i, float v) { p[i] = v; }
-__device__ __forceinline__ void store_f(__nv_bfloat16* p, size_t i, float v) { p[i] = __float2bfloat16_rn(v); }
+struct NormArgs {
+  const __nv_bfloat16* x;
+  const void* residual;  // of the stream's type, may be h
+  const void* weight;
+  bool weight_f32;
+  int T, H, stages;
+  float eps;
+  void* h;
+  __nv_bfloat16* y;
+  uint8_t* codes;
+  uint8_t* scales;
+};
 
-// Sum over the block, the same value on every thread.  Warps in order.
-__device__ __forceinline__ float block_sum(float v, float* s_part) {
+// A quad of lanes holds a scale group of 32 columns.  The stored h, the sum of
+// squares and y all come from one read of the row: its fp32 values stay in
+// registers across the row's one barrier, and their ring slot is filled again
+// before it.
+template <class S, int NC, bool WARP, bool RAGGED>
+__global__ void __launch_bounds__(512, NC == 4 ? 1 : 2) rmsnorm_kernel(const NormArgs a) {
+  extern __shared__ uint4 s_ring[];
+  __shared__ float s_part[2 * 32];
+  const int lane = threadIdx.x & 31;
+  const int TS = WARP ? 32 : blockDim.x;
+  const int rank = WARP ? lane : threadIdx.x;
+  const int per_block = WARP ? blockDim.x >> 5 : 1;
+  const int team = blockIdx.x * per_block + (WARP ? threadIdx.x >> 5 : 0);
+  const int teams = gridDim.x * per_block;
+  const int T = a.T, H = a.H, stages = a.stages;
+  const int slots = TS * NC;
+  constexpr int kPlanes = 1 + sizeof(S) / 2;
+  uint4* ring = s_ring + (WARP ? (threadIdx.x >> 5) * stages * slots * kPlanes : 0);
+  const int lead = RAGGED ? ((team & 7) * (H & 7)) & 7 : 0;
+  const int nchunk = (lead + H + 7) >> 3;
+  const size_t total = static_cast<size_t>(T) * H;
+  const S* residual = static_cast<const S*>(a.residual);
+
+  auto issue = [&](int t, int s) {
+    if (t < T) {
+      const size_t first = static_cast<size_t>(t) * H - lead;
+      uint4* slot = ring + s * slots * kPlanes;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += s_part[w];
-  return s;
+      for (int i = 0; i < NC; ++i) {
+        const int c = i * TS + rank;
+        if (c >= nchunk) break;
+        load_chunk<__nv_bfloat16, RAGGED>(slot + c, slots, a.x, first + 8 * c, total);
+        if (residual) load_chunk<S, RAGGED>(slot + slots + c, slots, residual, first + 8 * c, total);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int s = 0; s < stages; ++s) issue(team + s * teams, s);
+  float w[NC][8];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = i * TS + rank;
+    if (c < nchunk) load_weight<RAGGED>(a.weight, a.weight_f32, 8 * c - lead, H, w[i]);
+  }
+
+  int s = 0, odd = 0;
+  for (int t = team; t < T; t += teams) {
+    const size_t base = static_cast<size_t>(t) * H;
+    cp_async_wait(stages - 1);
+    const uint4* slot = ring + s * slots * kPlanes;
+    float v[NC][8], sum[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = i * TS + rank;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      if (c >= nchunk) continue;
+      read_chunk<__nv_bfloat16>(slot + c, slots, v[i]);
+      if (residual) {
+        float r[8];
+        read_chunk<S>(slot + slots + c, slots, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+      }
+      const int j0 = 8 * c - lead;
+      if (RAGGED && (j0 < 0 || j0 + 8 > H)) {  // a neighbour's elements
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j0 + j < 0 || j0 + j >= H) v[i][j] = 0.f;
+      }
+      if (a.h) store_chunk<S, RAGGED>(static_cast<S*>(a.h) + base, j0, H, v[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
+    }
+    issue(t + stages * teams, s);
+    team_sum<1, WARP>(sum, s_part, odd);
+    const float rstd = rsqrtf(sum[0] / static_cast<float>(H) + a.eps);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = i * TS + rank;
+      const bool active = c < nchunk;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = active ? v[i][j] * rstd * w[i][j] : 0.f;
+      if (active && a.y) store_chunk<__nv_bfloat16, RAGGED>(a.y + base, 8 * c - lead, H, v[i]);
+      if (!RAGGED && a.codes) {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] = __bfloat162float(__float2bfloat16_rn(v[i][j]));
+          amax = fmaxf(amax, fabsf(v[i][j]));  // fmaxf drops NaN
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int e = e4m3_scale_exp(amax);
+        if (active) {
+          reinterpret_cast<uint2*>(a.codes + base)[c] = e4m3_chunk(v[i], exp2i(-e));
+          if ((c & 3) == 0) a.scales[(base >> 5) + (c >> 2)] = static_cast<uint8_t>(e + 127);
+        }
+      }
+    }
+    s = s + 1 == stages ? 0 : s + 1;
+    odd ^= 1;
+  }
 }
 
 // One block per row.
-template <class S, class W>
-__global__ void __launch_bounds__(256) rmsnorm_kernel(const __nv_bfloat16* __restrict__ x, const S* residual,
-                                                      const W* __restrict__ weight, int H, float eps, S* h,
-                                                      __nv_bfloat16* __restrict__ y, uint8_t* __restrict__ codes,
-                                                      uint8_t* __restrict__ scales) {
+template <class S>
+__global__ void __launch_bounds__(256) rmsnorm_elems_kernel(const NormArgs a) {
   extern __shared__ float s_h[];  // [H]
   __shared__ float s_part[8];
+  const int H = a.H;
   const size_t base = static_cast<size_t>(blockIdx.x) * H;
+  const S* residual = static_cast<const S*>(a.residual);
   float sum = 0.f;
   for (int i = threadIdx.x; i < H; i += blockDim.x) {
-    float v = load_f(x, base + i);
-    if (residual) {
-      v += load_f(residual, base + i);
-      if (h) store_f(h, base + i, v);
-    }
+    float v = load_f(a.x, base + i);
+    if (residual) v += load_f(residual, base + i);
+    if (a.h) store_f(static_cast<S*>(a.h), base + i, v);
     s_h[i] = v;
     sum = fmaf(v, v, sum);
   }
-  const float rstd = rsqrtf(block_sum(sum, s_part) / static_cast<float>(H) + eps);
-  // 32 consecutive columns a warp: one scale group
+  const float rstd = rsqrtf(block_sum(sum, s_part) / static_cast<float>(H) + a.eps);
   for (int i = threadIdx.x; i < H; i += blockDim.x) {
-    const __nv_bfloat16 yb = __float2bfloat16_rn(s_h[i] * rstd * load_f(weight, i));
-    if (y) y[base + i] = yb;
-    if (codes) {
+    const float w = a.weight_f32 ? load_f(static_cast<const float*>(a.weight), i)
+                                 : load_f(static_cast<const __nv_bfloat16*>(a.weight), i);
+    const __nv_bfloat16 yb = __float2bfloat16_rn(s_h[i] * rstd * w);
+    if (a.y) a.y[base + i] = yb;
+    if (a.codes) {  // 32 consecutive columns a warp: one scale group (H is a multiple of 32)
       const float v = __bfloat162float(yb);
-      float a = isnan(v) ? 0.f : fabsf(v);
+      float amax = isnan(v) ? 0.f : fabsf(v);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-      const int e = e4m3_scale_exp(a);
-      codes[base + i] = e4m3_code(v, exp2i(-e));
-      if ((i & 31) == 0) scales[(base + i) >> 5] = static_cast<uint8_t>(e + 127);
+      for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      const int e = e4m3_scale_exp(amax);
+      a.codes[base + i] = e4m3_code(v, exp2i(-e));
+      if ((i & 31) == 0) a.scales[(base + i) >> 5] = static_cast<uint8_t>(e + 127);
     }
   }
 }
 
-template <class S, class W>
-cudaError_t rmsnorm_typed(const void* x, const void* residual, const void* weight, int T, int H, float eps, void* h,
-                          void* y, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(H) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(rmsnorm_kernel<S, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+template <class S, int NC, bool WARP, bool RAGGED>
+cudaError_t launch_rows(const NormArgs& a, const NormPlan& p, cudaStream_t st) {
+  static int ready[kMaxDevices] = {};
+  const cudaError_t e = allow_smem(rmsnorm_kernel<S, NC, WARP, RAGGED>, ready);
   if (e != cudaSuccess) return e;
-  rmsnorm_kernel<S, W><<<T, 256, smem, st>>>(static_cast<const __nv_bfloat16*>(x), static_cast<const S*>(residual),
-                                             static_cast<const W*>(weight), H, eps, static_cast<S*>(h),
-                                             static_cast<__nv_bfloat16*>(y), codes, scales);
+  rmsnorm_kernel<S, NC, WARP, RAGGED><<<p.blocks, p.threads, p.smem, st>>>(a);
+  return cudaGetLastError();
+}
+template <class S, int NC>
+cudaError_t launch_nc(const NormArgs& a, const NormPlan& p, cudaStream_t st) {
+  if (a.H % 8 == 0)
+    return p.warp ? launch_rows<S, NC, true, false>(a, p, st) : launch_rows<S, NC, false, false>(a, p, st);
+  return p.warp ? launch_rows<S, NC, true, true>(a, p, st) : launch_rows<S, NC, false, true>(a, p, st);
+}
+template <class S>
+cudaError_t launch_stream(NormArgs a, cudaStream_t st) {
+  constexpr uintptr_t kVec = 15;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
+                        reinterpret_cast<uintptr_t>(a.h) | reinterpret_cast<uintptr_t>(a.y) |
+                        reinterpret_cast<uintptr_t>(a.weight);
+  const NormPlan p = (all & kVec) == 0 ? plan_norm(a.T, a.H, 16 * (1 + sizeof(S) / 2), 8) : NormPlan{};
+  a.stages = p.stages;
+  if (p.nc == 1) return launch_nc<S, 1>(a, p, st);
+  if (p.nc == 2) return launch_nc<S, 2>(a, p, st);
+  if (p.nc == 4) return launch_nc<S, 4>(a, p, st);
+  static int ready[kMaxDevices] = {};
+  const cudaError_t e = allow_smem(rmsnorm_elems_kernel<S>, ready);
+  if (e != cudaSuccess) return e;
+  rmsnorm_elems_kernel<S><<<a.T, 256, static_cast<size_t>(a.H) * 4, st>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_rmsnorm(const void* x, const void* residual, const void* weight, int T, int H, float eps,
                            bool stream_f32, bool weight_f32, void* h, void* y, uint8_t* codes, uint8_t* scales,
                            cudaStream_t st) {
-  if (stream_f32)
-    return weight_f32 ? rmsnorm_typed<float, float>(x, residual, weight, T, H, eps, h, y, codes, scales, st)
-                      : rmsnorm_typed<float, __nv_bfloat16>(x, residual, weight, T, H, eps, h, y, codes, scales, st);
-  return weight_f32
-             ? rmsnorm_typed<__nv_bfloat16, float>(x, residual, weight, T, H, eps, h, y, codes, scales, st)
-             : rmsnorm_typed<__nv_bfloat16, __nv_bfloat16>(x, residual, weight, T, H, eps, h, y, codes, scales, st);
-}
-
-// ---------------------------------------------------------------- gradient
-// With n = h * rstd, g = dy * w:
-//   dh = dh_in + rstd * (g - n * mean(g * n)),  dw = sum over rows of dy * n.
-// rstd is recomputed from h in the pass that reads it anyway.  Block b takes
-// rows b, b + parts, ... and writes its own row of dw partial sums; a second
-// kernel adds the parts in order, so dw does not depend on timing.
-template <class S, class W>
-__global__ void __launch_bounds__(256) rmsnorm_backward_kernel(const __nv_bfloat16* __restrict__ dy,
-                                                               const S* __restrict__ h, const W* __restrict__ weight,
-                                                               const S* dh_in, int T, int H, float eps, S* dh,
-                                                               float* __restrict__ part) {
-  extern __shared__ float s_dw[];  // [H]
-  __shared__ float s_part[8];
-  for (int i = threadIdx.x; i < H; i += blockDim.x) s_dw[i] = 0.f;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const size_t base = static_cast<size_t>(t) * H;
-    float ss = 0.f, gh = 0.f;
-    for (int i = threadIdx.x; i < H; i += blockDim.x) {
-      const float hv = load_f(h, base + i);
-      ss = fmaf(hv, hv, ss);
-      gh = fmaf(load_f(dy, base + i) * load_f(weight, i), hv, gh);
-    }
-    ss = block_sum(ss, s_part);
-    gh = block_sum(gh, s_part);
-    const float rstd = rsqrtf(ss / static_cast<float>(H) + eps);
-    const float c = gh * rstd / static_cast<float>(H);
-    for (int i = threadIdx.x; i < H; i += blockDim.x) {
-      const float n = load_f(h, base + i) * rstd;
-      const float d = load_f(dy, base + i);
-      s_dw[i] = fmaf(d, n, s_dw[i]);
-      const float v = rstd * (d * load_f(weight, i) - n * c);
-      store_f(dh, base + i, dh_in ? load_f(dh_in, base + i) + v : v);
-    }
-  }
-  for (int i = threadIdx.x; i < H; i += blockDim.x) part[static_cast<size_t>(blockIdx.x) * H + i] = s_dw[i];
-}
-
-__global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* __restrict__ part, int parts, int H,
-                                                              float* __restrict__ dweight) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= H) return;
-  float s = 0.f;
-  for (int p = 0; p < parts; ++p) s += part[static_cast<size_t>(p) * H + i];
-  dweight[i] = s;
-}
-
-template <class S, class W>
-cudaError_t rmsnorm_backward_typed(const void* dy, const void* h, const void* weight, const void* dh_in, int T, int H,
-                                   float eps, void* dh, float* dweight, float* part, cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(H) * 4;
-  const int parts = norm_parts(T);
-  const cudaError_t e = cudaFuncSetAttribute(rmsnorm_backward_kernel<S, W>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  rmsnorm_backward_kernel<S, W><<<parts, 256, smem, st>>>(
-      static_cast<const __nv_bfloat16*>(dy), static_cast<const S*>(h), static_cast<const W*>(weight),
-      static_cast<const S*>(dh_in), T, H, eps, static_cast<S*>(dh), part);
-  rmsnorm_dweight_kernel<<<(H + 255) / 256, 256, 0, st>>>(part, parts, H, dweight);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_rmsnorm_backward(const void* dy, const void* h, const void* weight, const void* dh_in, int T, int H,
-                                    float eps, bool stream_f32, bool weight_f32, void* dh, float* dweight, float* part,
-                                    cudaStream_t st) {
-  if (T == 0) return cudaMemsetAsync(dweight, 0, static_cast<size_t>(H) * 4, st);
-  if (stream_f32)
-    return weight_f32
-               ? rmsnorm_backward_typed<float, float>(dy, h, weight, dh_in, T, H, eps, dh, dweight, part, st)
-               : rmsnorm_backward_typed<float, __nv_bfloat16>(dy, h, weight, dh_in, T, H, eps, dh, dweight, part, st);
-  return weight_f32 ? rmsnorm_backward_typed<__nv_bfloat16, float>(dy, h, weight, dh_in, T, H, eps, dh, dweight, part,
-                                                                  st)
-                    : rmsnorm_backward_typed<__nv_bfloat16, __nv_bfloat16>(dy, h, weight, dh_in, T, H, eps, dh,
-                                                                          dweight, part, st);
+  const NormArgs a{static_cast<const __nv_bfloat16*>(x), residual, weight, weight_f32, T, H, 0, eps, h,
+                   static_cast<__nv_bfloat16*>(y), codes, scales};
+  return stream_f32 ? launch_stream<float>(a, st) : launch_stream<__nv_bfloat16>(a, st);
 }
 
 }  // namespace kmoe

@@ -1,15 +1,59 @@
-// Host interface of the norm kernels (norm.cu).
+// Host interface of the norm kernels (norm.cu, norm_backward.cu).
 #pragma once
 #include "common.cuh"
 
 namespace kmoe {
 
-constexpr int kMaxNormH = 32768;  // columns a block keeps on chip
+constexpr int kMaxNormH = 32768;       // columns of the element-wise path (a row of fp32 in shared memory)
+constexpr int kNormSmem = 224 * 1024;  // shared memory that a block may ask for
+constexpr int kNormSMs = 152;          // SMs the grids are laid out for
 
-// Partial rows of the weight gradient.  A function of the row count alone, so
-// that the summation order is the same on every GPU.
-__host__ inline int norm_parts(int T) { return T < 304 ? T : 304; }
-__host__ inline size_t norm_part_bytes(int T, int H) { return static_cast<size_t>(norm_parts(T)) * H * 4; }
+// Partial rows of the weight gradient: at most two blocks an SM.  A function
+// of the shape alone, so that the summation order is the same on every GPU.
+constexpr int kNormMaxParts = 2 * kNormSMs;
+__host__ inline size_t norm_part_bytes(int T, int H) {
+  return static_cast<size_t>(T < kNormMaxParts ? T : kNormMaxParts) * H * 4;
+}
+
+// Launch shape of a row kernel (norm_dev.cuh): chunks per thread, threads and
+// blocks, ring stages.  nc = 0: the row does not fit, take the element-wise path.
+struct NormPlan {
+  int nc, threads, blocks, stages;
+  bool warp;  // a warp, not a block, has a row
+  size_t smem;
+};
+
+// chunk_bytes: ring bytes of one chunk of one row (all its tensors).
+// max_per_sm: resident blocks an SM the grid is sized for.
+__host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, int max_per_sm) {
+  NormPlan p{};
+  const int C = H % 8 == 0 ? H / 8 : (H + 14) / 8;  // chunks a row can touch
+  int teams_per_block = 1, per_sm;
+  if (C <= 128) {
+    p.warp = true;
+    p.nc = C <= 32 ? 1 : (C <= 64 ? 2 : 4);
+    p.threads = 256;
+    teams_per_block = 8;
+    per_sm = 4;
+  } else {
+    p.nc = C <= 512 ? 1 : (C <= 1024 ? 2 : 4);
+    p.threads = ((C + p.nc - 1) / p.nc + 31) / 32 * 32;
+    if (p.threads > 512) return NormPlan{};
+    per_sm = 1024 / p.threads;
+  }
+  if (per_sm > max_per_sm) per_sm = max_per_sm;
+  const size_t stage = static_cast<size_t>(p.threads) * p.nc * chunk_bytes;
+  if (stage * per_sm > kNormSmem) per_sm = 1;
+  if (stage > kNormSmem) return NormPlan{};
+  const int want = (T + teams_per_block - 1) / teams_per_block;
+  p.blocks = want < kNormSMs * per_sm ? want : kNormSMs * per_sm;
+  const int rows = (T + p.blocks * teams_per_block - 1) / (p.blocks * teams_per_block);
+  p.stages = static_cast<int>(kNormSmem / per_sm / stage);
+  if (p.stages > 4) p.stages = 4;
+  if (p.stages > rows) p.stages = rows;
+  p.smem = stage * p.stages;
+  return p;
+}
 
 cudaError_t launch_rmsnorm(const void* x, const void* residual, const void* weight, int T, int H, float eps,
                            bool stream_f32, bool weight_f32, void* h, void* y, uint8_t* codes, uint8_t* scales,
