@@ -331,10 +331,11 @@ typedef struct kmoe_route_params {
  * j-th largest key.
  *   topk_w[t, j] = scale * s_j / sum_j' s_j' with KMOE_ROUTE_RENORMALIZE,
  *   scale * s_j without
- * (a few fp32 units in the last place; 0 where the sum is 0).  An expert whose
- * logit is -inf or NaN, or whose key is, cannot be chosen (and is no part of
- * the softmax); slots that stay empty get id -1 and weight 0, which the
- * forward skips.  A +inf logit takes the softmax's whole weight.
+ * (a few fp32 units in the last place; 0 where the sum is 0, a sigmoid below
+ * e^-700 counting as 0).  An expert whose logit is -inf or NaN, or whose key
+ * is, cannot be chosen (and is no part of the softmax); slots that stay empty
+ * get id -1 and weight 0, which the forward skips.  A +inf logit takes the
+ * softmax's whole weight.
  *   logits [T, E] float; bias [E] float or null; topk_ids [T, k] int32 (out),
  *   topk_w [T, k] float (out). */
 int kmoe_route_grouped(const kmoe_route_params* p, const float* logits, const float* bias, int32_t* topk_ids,

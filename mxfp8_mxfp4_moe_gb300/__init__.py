@@ -374,13 +374,19 @@ def kmoe_forward_noalloc(p, x, logits, bias, w13_k, w2_k, topk_ids=None, topk_w=
 def kmoe_forward_mx(p, x_codes, x_scales, topk_ids, topk_w, w13_k, w2_k, out=None, workspace=None, stream=None):
     """kmoe_forward on rows quantised before (kmoe_rmsnorm's or
     kmoe_quantize_mx's codes [T, H] and scales [T, H/32]), routing given."""
-    dev = _args(stream, ("x_codes", x_codes, torch.uint8, (p.T, p.H)), ("x_scales", x_scales, torch.uint8, (p.T, p.H // 32)),
-                ("topk_ids", topk_ids, torch.int32, (p.T, p.k)), ("topk_w", topk_w, torch.float32, (p.T, p.k)),
-                ("out", out, torch.bfloat16, (p.T, p.H)))
+    dev = _rows_on(x_codes, "x_codes", "H")[2]
+    _args(stream, dev, (("x_codes", x_codes, torch.uint8, (p.T, p.H)),
+                        ("x_scales", x_scales, torch.uint8, (p.T, p.H // 32)),
+                        ("topk_ids", topk_ids, torch.int32, (p.T, p.k)),
+                        ("topk_w", topk_w, torch.float32, (p.T, p.k)), ("out", out, torch.bfloat16, (p.T, p.H))))
     _arg(w13_k, "w13_k", torch.uint8, min_bytes=kmoe_prepared_weight_bytes(p, 0))
     _arg(w2_k, "w2_k", torch.uint8, min_bytes=kmoe_prepared_weight_bytes(p, 1))
     _arg(workspace, "workspace", torch.uint8, min_bytes=kmoe_workspace_size(p))
     _gpu(w13_k=w13_k, w2_k=w2_k, workspace=workspace)
+    if stream is not None:
+        for t in (w13_k, w2_k, workspace):
+            if t is not None:
+                t.record_stream(stream)
     if out is None:
         out = _new((p.T, p.H), torch.bfloat16, dev, stream)
     if workspace is None:
@@ -394,39 +400,42 @@ def kmoe_forward_mx(p, x_codes, x_scales, topk_ids, topk_w, w13_k, w2_k, out=Non
 # ---- the operators around the experts.  Decode calls are a few microseconds
 # on the GPU, so their argument checks are one pass over the tensors.
 
-def _args(stream, *named):
-    """Checks (name, tensor, dtype, shape) of each argument, None passing, and
-    returns the device.  The errors are _arg's and _gpu's.  A tensor that a
+def _args(stream, dev, named):
+    """Checks (name, tensor, dtype, shape) of each argument, None passing, on
+    device ordinal `dev`.  The errors are _arg's and _gpu's.  A tensor that a
     given stream uses is kept from reuse until that stream is through."""
-    dev = None
     for name, t, dtype, shape in named:
-        if t is None:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous()):
             continue
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-            _arg(t, name, dtype, shape)
-        if not t.is_cuda:
-            for n, u, d, s in named:
-                _arg(u, n, d, s)
-            _gpu(**{name: t})
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+        for n, u, d, s in named:
+            _arg(u, n, d, s)
+        _gpu(**{n: u for n, u, _, _ in named})
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
     if stream is not None:
         for _, t, _, _ in named:
             if t is not None:
                 t.record_stream(stream)
-    return dev
+
+
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _raw_stream(dev, stream):
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    return _current_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _rows_on(t, name, ncols_name):
+    """(rows, cols, device ordinal) of a 2-D argument."""
+    if t is None or t.dim() != 2:
+        _rows(t, name, ncols_name)
+    rows, cols = t.shape
+    return rows, cols, t.get_device()
 
 
 def _new(shape, dtype, dev, stream):
     """An output or workspace of a call on `stream`: the allocator keeps its
     memory from reuse until that stream is through with it."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
+    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -454,16 +463,17 @@ def kmoe_rmsnorm(x, weight, residual=None, eps=1e-6, mx=False, h=None, y=None, c
     and scales of y, in one kernel.  Returns (h, y, codes, scales); h is None
     without a residual, codes and scales without `mx`.  residual and h are
     bf16 or fp32 (h may be residual itself), weight bf16 or fp32."""
-    T, H = _rows(x, "x", "H")
+    T, H, dev = _rows_on(x, "x", "H")
     st = _type_of(residual, "residual", torch.bfloat16)
     wt = _type_of(weight, "weight", None)
     if h is not None and residual is None:
         raise ValueError("h needs a residual")
     if not mx and (codes is not None or scales is not None):
         raise ValueError("codes and scales need mx=True")
-    dev = _args(stream, ("x", x, torch.bfloat16, (T, H)), ("weight", weight, wt, (H,)), ("residual", residual, st, (T, H)),
-                ("h", h, st, (T, H)), ("y", y, torch.bfloat16, (T, H)), ("codes", codes, torch.uint8, (T, H)),
-                ("scales", scales, torch.uint8, (T, H // 32)))
+    rows = (T, H)
+    _args(stream, dev, (("x", x, torch.bfloat16, rows), ("weight", weight, wt, (H,)), ("residual", residual, st, rows),
+                        ("h", h, st, rows), ("y", y, torch.bfloat16, rows), ("codes", codes, torch.uint8, rows),
+                        ("scales", scales, torch.uint8, (T, H // 32))))
     if h is None and residual is not None:
         h = _new((T, H), st, dev, stream)
     if y is None:
@@ -487,17 +497,21 @@ def kmoe_rmsnorm_backward(dy, h, weight, dh_in=None, eps=1e-6, dh=None, dweight=
     """Gradient of kmoe_rmsnorm at the stored h: (dh, dweight), dh of h's type
     (the gradient of x and of residual alike, with dh_in added), dweight fp32.
     dh may be dh_in itself."""
-    T, H = _rows(h, "h", "H")
+    T, H, dev = _rows_on(h, "h", "H")
     st = _type_of(h, "h", None)
     wt = _type_of(weight, "weight", None)
-    dev = _args(stream, ("dy", dy, torch.bfloat16, (T, H)), ("h", h, st, (T, H)), ("weight", weight, wt, (H,)),
-                ("dh_in", dh_in, st, (T, H)), ("dh", dh, st, (T, H)), ("dweight", dweight, torch.float32, (H,)))
+    rows = (T, H)
+    _args(stream, dev, (("dy", dy, torch.bfloat16, rows), ("h", h, st, rows), ("weight", weight, wt, (H,)),
+                        ("dh_in", dh_in, st, rows), ("dh", dh, st, rows),
+                        ("dweight", dweight, torch.float32, (H,))))
     n = _lib.kmoe_rmsnorm_workspace_size(T, H)
     if workspace is None:
         workspace = _new(max(n, 1), torch.uint8, dev, stream)
     else:
         _arg(workspace, "workspace", torch.uint8, min_bytes=n)
         _gpu(workspace=workspace)
+        if stream is not None:
+            workspace.record_stream(stream)
     if dh is None:
         dh = _new((T, H), st, dev, stream)
     if dweight is None:
@@ -527,9 +541,9 @@ def kmoe_route_grouped(logits, bias, k, score="sigmoid", n_group=1, topk_group=1
     (None: the logits choose), `topk_group` of `n_group` expert groups and
     optionally renormalised weights.  Returns (topk_ids, topk_w); slots no
     expert could fill hold id -1 and weight 0."""
-    T, E = _rows(logits, "logits", "E")
-    dev = _args(stream, ("logits", logits, torch.float32, (T, E)), ("bias", bias, torch.float32, (E,)),
-                ("topk_ids", topk_ids, torch.int32, (T, k)), ("topk_w", topk_w, torch.float32, (T, k)))
+    T, E, dev = _rows_on(logits, "logits", "E")
+    _args(stream, dev, (("logits", logits, torch.float32, (T, E)), ("bias", bias, torch.float32, (E,)),
+                        ("topk_ids", topk_ids, torch.int32, (T, k)), ("topk_w", topk_w, torch.float32, (T, k))))
     p = _route_params(T, E, k, n_group, topk_group, score, renormalize, scale)
     if topk_ids is None:
         topk_ids = _new((T, k), torch.int32, dev, stream)
@@ -544,10 +558,10 @@ def kmoe_route_backward(d_w, logits, topk_ids, score="sigmoid", renormalize=True
                         stream=None):
     """Gradient of the routing weights with respect to the logits: d_logits
     fp32 [T, E], dense, for the ids that were chosen."""
-    T, E = _rows(logits, "logits", "E")
+    T, E, dev = _rows_on(logits, "logits", "E")
     k = _rows(topk_ids, "topk_ids", "k")[1]
-    dev = _args(stream, ("logits", logits, torch.float32, (T, E)), ("d_w", d_w, torch.float32, (T, k)),
-                ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_logits", d_logits, torch.float32, (T, E)))
+    _args(stream, dev, (("logits", logits, torch.float32, (T, E)), ("d_w", d_w, torch.float32, (T, k)),
+                        ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_logits", d_logits, torch.float32, (T, E))))
     p = _route_params(T, E, k, 1, 1, score, renormalize, scale)
     if d_logits is None:
         d_logits = _new((T, E), torch.float32, dev, stream)
@@ -560,10 +574,10 @@ def kmoe_combine_backward(d_out, y, topk_ids, E, routed_scaling_factor=1.0, d_w=
     """Gradient of the combine with respect to the routing weights: fp32
     [T, k] from d_out bf16 [T, H] and the per-slot outputs y fp32 [T*k, H]
     that a forward leaves in its workspace (stage_views(p, ws)["y"])."""
-    T, H = _rows(d_out, "d_out", "H")
+    T, H, dev = _rows_on(d_out, "d_out", "H")
     k = _rows(topk_ids, "topk_ids", "k")[1]
-    dev = _args(stream, ("d_out", d_out, torch.bfloat16, (T, H)), ("y", y, torch.float32, (T * k, H)),
-                ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_w", d_w, torch.float32, (T, k)))
+    _args(stream, dev, (("d_out", d_out, torch.bfloat16, (T, H)), ("y", y, torch.float32, (T * k, H)),
+                        ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_w", d_w, torch.float32, (T, k))))
     if d_w is None:
         d_w = _new((T, k), torch.float32, dev, stream)
     _check("kmoe_combine_backward", _lib.kmoe_combine_backward(

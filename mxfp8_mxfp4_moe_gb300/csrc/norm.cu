@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(512, NC == 4 ? 1 : 2) rmsnorm_kernel(const Nor
     cp_async_commit();
   };
   for (int s = 0; s < stages; ++s) issue(team + s * teams, s);
-  float w[NC][8];
+  float2 w[NC][4];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = i * TS + rank;
@@ -72,53 +72,55 @@ __global__ void __launch_bounds__(512, NC == 4 ? 1 : 2) rmsnorm_kernel(const Nor
     const size_t base = static_cast<size_t>(t) * H;
     cp_async_wait(stages - 1);
     const uint4* slot = ring + s * slots * kPlanes;
-    float v[NC][8], sum[1] = {0.f};
+    float2 v[NC][4], sq = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = i * TS + rank;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      zero(v[i]);
       if (c >= nchunk) continue;
       read_chunk<__nv_bfloat16>(slot + c, slots, v[i]);
       if (residual) {
-        float r[8];
+        float2 r[4];
         read_chunk<S>(slot + slots + c, slots, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+        for (int p = 0; p < 4; ++p) v[i][p] = __fadd2_rn(v[i][p], r[p]);
       }
       const int j0 = 8 * c - lead;
-      if (RAGGED && (j0 < 0 || j0 + 8 > H)) {  // a neighbour's elements
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j0 + j < 0 || j0 + j >= H) v[i][j] = 0.f;
+      if (RAGGED && (j0 < 0 || j0 + 8 > H)) mask_edge(v[i], j0, H);
+      if (a.h) {
+        Vec8<S> o;
+        pack(v[i], o);
+        store_chunk<S, RAGGED>(static_cast<S*>(a.h) + base, j0, H, o);
       }
-      if (a.h) store_chunk<S, RAGGED>(static_cast<S*>(a.h) + base, j0, H, v[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[i][j], v[i][j], sum[0]);
+      for (int p = 0; p < 4; ++p) sq = __ffma2_rn(v[i][p], v[i][p], sq);
     }
     issue(t + stages * teams, s);
+    float sum[1] = {sq.x + sq.y};
     team_sum<1, WARP>(sum, s_part, odd);
     const float rstd = rsqrtf(sum[0] / static_cast<float>(H) + a.eps);
+    const float2 rstd2 = make_float2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = i * TS + rank;
       const bool active = c < nchunk;
+      Vec8<__nv_bfloat16> o;
+      o.q[0] = make_uint4(0u, 0u, 0u, 0u);
+      if (active) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = active ? v[i][j] * rstd * w[i][j] : 0.f;
-      if (active && a.y) store_chunk<__nv_bfloat16, RAGGED>(a.y + base, 8 * c - lead, H, v[i]);
+        for (int p = 0; p < 4; ++p) v[i][p] = __fmul2_rn(__fmul2_rn(v[i][p], rstd2), w[i][p]);
+        pack(v[i], o);
+        if (a.y) store_chunk<__nv_bfloat16, RAGGED>(a.y + base, 8 * c - lead, H, o);
+      }
       if (!RAGGED && a.codes) {
-        float amax = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[i][j] = __bfloat162float(__float2bfloat16_rn(v[i][j]));
-          amax = fmaxf(amax, fabsf(v[i][j]));  // fmaxf drops NaN
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = e4m3_scale_exp(amax);
+        // the quad's largest magnitude; H is a multiple of 32, so whole quads are active or not
+        uint32_t amax = bf16_amax(o.q[0]);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         if (active) {
-          reinterpret_cast<uint2*>(a.codes + base)[c] = e4m3_chunk(v[i], exp2i(-e));
-          if ((c & 3) == 0) a.scales[(base >> 5) + (c >> 2)] = static_cast<uint8_t>(e + 127);
+          const uint32_t scale = e4m3_scale_byte(amax);
+          reinterpret_cast<uint2*>(a.codes + base)[c] = e4m3_chunk(o.q[0], scale);
+          if ((c & 3) == 0) a.scales[(base >> 5) + (c >> 2)] = static_cast<uint8_t>(scale);
         }
       }
     }
@@ -181,7 +183,7 @@ cudaError_t launch_stream(NormArgs a, cudaStream_t st) {
   const uintptr_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
                         reinterpret_cast<uintptr_t>(a.h) | reinterpret_cast<uintptr_t>(a.y) |
                         reinterpret_cast<uintptr_t>(a.weight);
-  const NormPlan p = (all & kVec) == 0 ? plan_norm(a.T, a.H, 16 * (1 + sizeof(S) / 2), 8) : NormPlan{};
+  const NormPlan p = (all & kVec) == 0 ? plan_norm(a.T, a.H, 16 * (1 + sizeof(S) / 2), false) : NormPlan{};
   a.stages = p.stages;
   if (p.nc == 1) return launch_nc<S, 1>(a, p, st);
   if (p.nc == 2) return launch_nc<S, 2>(a, p, st);

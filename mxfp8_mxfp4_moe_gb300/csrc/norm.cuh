@@ -24,10 +24,16 @@ struct NormPlan {
 };
 
 // chunk_bytes: ring bytes of one chunk of one row (all its tensors).
-// max_per_sm: resident blocks an SM the grid is sized for.
-__host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, int max_per_sm) {
+// Blocks an SM: rows in flight help until the streams of many rows hurt HBM.
+// Measured per direction (1 / 2 blocks, us): the forward, 512 threads an SM:
+// H = 7168 with codes 85.5 / 97.0, H = 4096 86 / 98, H = 2048 (2 / 4 blocks)
+// 83 / 99; the gradient, 1024 chunks an SM: H = 7168 75.9 / 78.4, H = 3584
+// 90 / 77.8.  Ragged rows do more for each byte and want twice as many: H =
+// 7001, T = 4096, forward 45.5 / 42.7, gradient 59.6 / 51.6.
+__host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, bool backward) {
   NormPlan p{};
-  const int C = H % 8 == 0 ? H / 8 : (H + 14) / 8;  // chunks a row can touch
+  const bool ragged = H % 8 != 0;
+  const int C = ragged ? (H + 14) / 8 : H / 8;  // chunks a row can touch
   int teams_per_block = 1, per_sm;
   if (C <= 128) {
     p.warp = true;
@@ -39,9 +45,10 @@ __host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, int max_per_sm
     p.nc = C <= 512 ? 1 : (C <= 1024 ? 2 : 4);
     p.threads = ((C + p.nc - 1) / p.nc + 31) / 32 * 32;
     if (p.threads > 512) return NormPlan{};
-    per_sm = 1024 / p.threads;
+    per_sm = (backward ? 1024 / (p.threads * p.nc) : 512 / p.threads) * (ragged ? 2 : 1);
+    if (per_sm < 1) per_sm = 1;
   }
-  if (per_sm > max_per_sm) per_sm = max_per_sm;
+  if (backward && per_sm > 2) per_sm = 2;  // kNormMaxParts
   const size_t stage = static_cast<size_t>(p.threads) * p.nc * chunk_bytes;
   if (stage * per_sm > kNormSmem) per_sm = 1;
   if (stage > kNormSmem) return NormPlan{};

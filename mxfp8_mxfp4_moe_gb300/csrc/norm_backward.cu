@@ -59,12 +59,12 @@ __global__ void __launch_bounds__(512, NC == 4 ? 1 : 2) rmsnorm_backward_kernel(
     cp_async_commit();
   };
   for (int s = 0; s < stages; ++s) issue(team + s * teams, s);
-  float w[NC][8], dw[NC][8];
+  float2 w[NC][4], dw[NC][4];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = i * TS + rank;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.f;
+    zero(w[i]);
+    zero(dw[i]);
     if (c < nchunk) load_weight<RAGGED>(a.weight, a.weight_f32, 8 * c - lead, H, w[i]);
   }
 
@@ -74,43 +74,48 @@ __global__ void __launch_bounds__(512, NC == 4 ? 1 : 2) rmsnorm_backward_kernel(
     const size_t base = static_cast<size_t>(t) * H;
     cp_async_wait(stages - 1);
     const uint4* slot = ring + s * slots * kPlanes;
-    float sum[2] = {0.f, 0.f};
+    float2 ss = make_float2(0.f, 0.f), gh = ss;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = i * TS + rank;
       if (c >= nchunk) break;
-      float d[8], v[8];
+      float2 d[4], v[4];
       read_chunk<__nv_bfloat16>(slot + c, slots, d);
       read_chunk<S>(slot + slots + c, slots, v);
       const int j0 = 8 * c - lead;
-      const bool edge = RAGGED && (j0 < 0 || j0 + 8 > H);  // holds a neighbour's elements
+      if (RAGGED && (j0 < 0 || j0 + 8 > H)) {
+        mask_edge(v, j0, H);
+        mask_edge(d, j0, H);
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (edge && (j0 + j < 0 || j0 + j >= H)) continue;
-        sum[0] = fmaf(v[j], v[j], sum[0]);
-        sum[1] = fmaf(d[j] * w[i][j], v[j], sum[1]);
+      for (int p = 0; p < 4; ++p) {
+        ss = __ffma2_rn(v[p], v[p], ss);
+        gh = __ffma2_rn(__fmul2_rn(d[p], w[i][p]), v[p], gh);
       }
     }
+    float sum[2] = {ss.x + ss.y, gh.x + gh.y};
     team_sum<2, WARP>(sum, s_part, odd);
     const float rstd = rsqrtf(sum[0] * inv_h + a.eps);
-    const float c1 = sum[1] * rstd * inv_h;  // mean(g * n)
+    const float nc1 = -sum[1] * rstd * inv_h;  // -mean(g * n)
+    const float2 rstd2 = make_float2(rstd, rstd), nc2 = make_float2(nc1, nc1);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = i * TS + rank;
       if (c >= nchunk) break;
-      float d[8], v[8], o[8];
+      float2 d[4], v[4], o[4];
       read_chunk<__nv_bfloat16>(slot + c, slots, d);
       read_chunk<S>(slot + slots + c, slots, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = 0.f;
+      zero(o);
       if (dh_in) read_chunk<S>(slot + (1 + kS) * slots + c, slots, o);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = v[j] * rstd;
-        dw[i][j] = fmaf(d[j], n, dw[i][j]);
-        o[j] = fmaf(rstd, fmaf(d[j], w[i][j], -n * c1), o[j]);
+      for (int p = 0; p < 4; ++p) {
+        const float2 n = __fmul2_rn(v[p], rstd2);
+        dw[i][p] = __ffma2_rn(d[p], n, dw[i][p]);
+        o[p] = __ffma2_rn(rstd2, __ffma2_rn(d[p], w[i][p], __fmul2_rn(n, nc2)), o[p]);
       }
-      store_chunk<S, RAGGED>(static_cast<S*>(a.dh) + base, 8 * c - lead, H, o);
+      Vec8<S> q;
+      pack(o, q);
+      store_chunk<S, RAGGED>(static_cast<S*>(a.dh) + base, 8 * c - lead, H, q);
     }
     issue(t + stages * teams, s);
     s = s + 1 == stages ? 0 : s + 1;
@@ -121,8 +126,10 @@ __global__ void __launch_bounds__(512, NC == 4 ? 1 : 2) rmsnorm_backward_kernel(
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = i * TS + rank;
-      if (c < nchunk)
-        store_chunk<float, true>(a.part + static_cast<size_t>(blockIdx.x) * H, 8 * c - lead, H, dw[i]);
+      if (c >= nchunk) break;
+      Vec8<float> q;
+      pack(dw[i], q);
+      store_chunk<float, RAGGED>(a.part + static_cast<size_t>(blockIdx.x) * H, 8 * c - lead, H, q);
     }
     return;
   }
@@ -134,9 +141,11 @@ __global__ void __launch_bounds__(512, NC == 4 ? 1 : 2) rmsnorm_backward_kernel(
   for (int i = 0; i < NC; ++i) {
     const int c = i * TS + rank;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = 8 * c - lead + j;
-      if (col >= 0 && col < H) s_dw[(threadIdx.x >> 5) * H + col] = dw[i][j];
+    for (int p = 0; p < 4; ++p) {
+      const int col = 8 * c - lead + 2 * p;
+      float* row = s_dw + (threadIdx.x >> 5) * H;
+      if (col >= 0 && col < H) row[col] = dw[i][p].x;
+      if (col + 1 >= 0 && col + 1 < H) row[col + 1] = dw[i][p].y;
     }
   }
   __syncthreads();
@@ -228,7 +237,7 @@ cudaError_t launch_stream(NormGradArgs a, float* dweight, cudaStream_t st) {
   const uintptr_t all = reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.h) |
                         reinterpret_cast<uintptr_t>(a.dh_in) | reinterpret_cast<uintptr_t>(a.dh) |
                         reinterpret_cast<uintptr_t>(a.weight);
-  const NormPlan p = (all & kVec) == 0 ? plan_norm(a.T, a.H, 16 * (1 + sizeof(S)), 2) : NormPlan{};
+  const NormPlan p = (all & kVec) == 0 ? plan_norm(a.T, a.H, 16 * (1 + sizeof(S)), true) : NormPlan{};
   a.stages = p.stages;
   int parts = p.blocks;
   cudaError_t e;

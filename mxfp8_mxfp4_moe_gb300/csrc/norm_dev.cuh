@@ -24,33 +24,51 @@
 namespace kmoe {
 
 // ---------------------------------------------------------------- chunks of 8 elements
+// In fp32 a chunk is four float2: the additions and products below are the
+// two-wide fp32 instructions, half the issue slots of scalar ones.
 template <class T>
 struct Vec8 {
   uint4 q[sizeof(T) / 2];
 };
-__device__ __forceinline__ void unpack(const Vec8<__nv_bfloat16>& a, float (&v)[8]) {
-  const uint32_t w[4] = {a.q[0].x, a.q[0].y, a.q[0].z, a.q[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ void unpack(const Vec8<float>& a, float (&v)[8]) {
-  const uint32_t w[8] = {a.q[0].x, a.q[0].y, a.q[0].z, a.q[0].w, a.q[1].x, a.q[1].y, a.q[1].z, a.q[1].w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+__device__ __forceinline__ void unpack(const Vec8<__nv_bfloat16>& a, float2 (&v)[4]) {
+  v[0] = unpack2(a.q[0].x);
+  v[1] = unpack2(a.q[0].y);
+  v[2] = unpack2(a.q[0].z);
+  v[3] = unpack2(a.q[0].w);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ void unpack(const Vec8<float>& a, float2 (&v)[4]) {
+  v[0] = make_float2(__uint_as_float(a.q[0].x), __uint_as_float(a.q[0].y));
+  v[1] = make_float2(__uint_as_float(a.q[0].z), __uint_as_float(a.q[0].w));
+  v[2] = make_float2(__uint_as_float(a.q[1].x), __uint_as_float(a.q[1].y));
+  v[3] = make_float2(__uint_as_float(a.q[1].z), __uint_as_float(a.q[1].w));
+}
+__device__ __forceinline__ uint32_t pack2(float2 a) {
+  const __nv_bfloat162 p = __float22bfloat162_rn(a);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ void pack(const float (&v)[8], Vec8<__nv_bfloat16>& a) {
-  a.q[0] = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+__device__ __forceinline__ void pack(const float2 (&v)[4], Vec8<__nv_bfloat16>& a) {
+  a.q[0] = make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3]));
 }
-__device__ __forceinline__ void pack(const float (&v)[8], Vec8<float>& a) {
-  a.q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-  a.q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+__device__ __forceinline__ void pack(const float2 (&v)[4], Vec8<float>& a) {
+  a.q[0] = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                      __float_as_uint(v[1].y));
+  a.q[1] = make_uint4(__float_as_uint(v[2].x), __float_as_uint(v[2].y), __float_as_uint(v[3].x),
+                      __float_as_uint(v[3].y));
+}
+__device__ __forceinline__ void zero(float2 (&v)[4]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) v[p] = make_float2(0.f, 0.f);
+}
+// Zeroes what a chunk that starts at element j0 of a row holds of the row's neighbours.
+__device__ __forceinline__ void mask_edge(float2 (&v)[4], int j0, int H) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    if (j0 + 2 * p < 0 || j0 + 2 * p >= H) v[p].x = 0.f;
+    if (j0 + 2 * p + 1 < 0 || j0 + 2 * p + 1 >= H) v[p].y = 0.f;
+  }
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t bytes) {
@@ -88,7 +106,7 @@ __device__ __forceinline__ void load_chunk(uint4* dst, int slots, const T* src, 
   }
 }
 template <class T>
-__device__ __forceinline__ void read_chunk(const uint4* src, int slots, float (&v)[8]) {
+__device__ __forceinline__ void read_chunk(const uint4* src, int slots, float2 (&v)[4]) {
   Vec8<T> a;
 #pragma unroll
   for (int p = 0; p < static_cast<int>(sizeof(T)) / 2; ++p) a.q[p] = src[p * slots];
@@ -97,9 +115,7 @@ __device__ __forceinline__ void read_chunk(const uint4* src, int slots, float (&
 // Stores the chunk whose first element is element j0 (negative before the
 // row's start) of the row at `row`.
 template <class T, bool RAGGED>
-__device__ __forceinline__ void store_chunk(T* row, int j0, int H, const float (&v)[8]) {
-  Vec8<T> a;
-  pack(v, a);
+__device__ __forceinline__ void store_chunk(T* row, int j0, int H, const Vec8<T>& a) {
   if (!RAGGED || (j0 >= 0 && j0 + 8 <= H)) {
 #pragma unroll
     for (int p = 0; p < static_cast<int>(sizeof(T)) / 2; ++p) reinterpret_cast<uint4*>(row + j0)[p] = a.q[p];
@@ -112,8 +128,8 @@ __device__ __forceinline__ void store_chunk(T* row, int j0, int H, const float (
 }
 // The weights of a chunk as fp32, 0 outside the row.
 template <bool RAGGED>
-__device__ __forceinline__ void load_weight(const void* weight, bool f32, int j0, int H, float (&w)[8]) {
-  if (!RAGGED) {
+__device__ __forceinline__ void load_weight(const void* weight, bool f32, int j0, int H, float2 (&w)[4]) {
+  if constexpr (!RAGGED) {
     if (f32) {
       Vec8<float> a;
       a.q[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(weight) + j0));
@@ -124,15 +140,13 @@ __device__ __forceinline__ void load_weight(const void* weight, bool f32, int j0
       a.q[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(weight) + j0));
       unpack(a, w);
     }
-    return;
-  }
+  } else {
+    auto at = [&](int j) {
+      if (j < 0 || j >= H) return 0.f;
+      return f32 ? static_cast<const float*>(weight)[j] : __bfloat162float(static_cast<const __nv_bfloat16*>(weight)[j]);
+    };
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int j = j0 + i;
-    w[i] = 0.f;
-    if (j >= 0 && j < H)
-      w[i] = f32 ? static_cast<const float*>(weight)[j]
-                 : __bfloat162float(static_cast<const __nv_bfloat16*>(weight)[j]);
+    for (int p = 0; p < 4; ++p) w[p] = make_float2(at(j0 + 2 * p), at(j0 + 2 * p + 1));
   }
 }
 
