@@ -19,6 +19,18 @@ __device__ __forceinline__ float warp_max(float v) {
   return order_key_inverse(__reduce_max_sync(0xffffffffu, order_key(v)));
 }
 
+// exp(x) and 1 / x from the hardware's approximations, results below 2^-126 as 0
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // ---------------------------------------------------------------- weights of chosen experts
 // What a chosen expert's logit l gives (lane j: slot j; -inf: an empty slot).
 struct Share {
@@ -45,14 +57,14 @@ __device__ __forceinline__ Share chosen_share(float l, const RouteGroupArgs& a, 
     if (expo) {
       r.p = l == base ? 1.f : expf(l - base);
     } else {
-      const float q = expf(-fabsf(l)), s = 1.f / (1.f + q);  // of |l|
+      const float q = expf(-fabsf(l)), s = fast_rcp(1.f + q);  // of |l|
       r.p = l >= 0.f ? s : q * s;
       r.slope = l >= 0.f ? q * s : s;
     }
   }
   if (a.renormalize) {
     const float sum = warp_sum(r.p);
-    r.p = sum > 0.f ? r.p / sum : 0.f;
+    r.p = sum > 0.f ? __fdividef(r.p, sum) : 0.f;
   } else if (a.softmax) {
     r.p /= total;
   }
@@ -69,38 +81,76 @@ __device__ __forceinline__ Share chosen_share(float l, const RouteGroupArgs& a, 
 //      margin: the keys that can be among a group's two largest are evaluated
 //      exactly and the groups ranked again.
 //   2. the k-th largest of the 32 lane maxima bounds the k-th largest key from
-//      below; experts within the margin of it are the candidates, usually at
-//      most one a lane.  More than 32 (k near 32, or many equal keys): the
-//      bound is raised by bisection over the keys' integer images.
+//      below (k > 16: or the k/2-th largest of the lanes' second keys, where
+//      that is more); experts within the margin of it are the candidates, about
+//      22 for k = 16.  More than 64 (many equal keys, mostly): the bound is
+//      raised by bisection over the keys' integer images.
 //   3. the candidates are sorted by (key, lower index).  Neighbours in the
 //      chosen order, or at its end, closer than the margin: the candidates get
-//      exact keys, one a lane, and are sorted again.
-//   4. softmax scores in doubt, infinite keys, or still more than 32
+//      exact keys, one or two a lane, and are sorted again.
+//   4. softmax scores in doubt, infinite keys, or still more than 64
 //      candidates: all keys exactly, and the same steps without a margin; if
-//      equal keys leave more than 32 candidates even so, k rounds of arg-max.
+//      equal keys leave more than 64 candidates even so, k rounds of arg-max.
 // Without a bias the logits are the keys and nothing is in doubt.
 //
 // Margin.  Sigmoid: the fast exponential is off by 2 + 1.16 |x| units in the
 // last place, which the sigmoid damps to at most 0.62 units of 2^-23; the sum
-// and the fast quotient add 2.5 more, the exact key's own two roundings one:
+// and the fast reciprocal add 1.5 more, the exact key's own two roundings one:
 // 6e-7 * max(1, |key|).  Two keys: 1.2e-6; 2e-6 is used.  Softmax: the
 // denominator's fp32 sum over up to 37 steps adds up to 2.3e-6; 1e-5 is used.
+constexpr int kMaxCand = 64;  // two a lane
 constexpr float kMarginSigmoid = 2e-6f;
 constexpr float kMarginSoftmax = 1e-5f;
 
-// Bitonic sort across the warp, lane 0 the largest.
-template <class V>
-__device__ __forceinline__ V warp_sort_desc(V v, int lane) {
+// Ranks by counting: a lane compares its value with all 32, read back from
+// shared memory in 16-byte pieces: independent instructions, where a bitonic
+// sort across the warp is a chain of 15 shuffles.
+// Number of the 32 floats at s_val (no NaN) that are larger.
+__device__ __forceinline__ int count_larger(float v, const float* s_val) {
+  int r = 0;
 #pragma unroll
-  for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      const V o = __shfl_xor_sync(0xffffffffu, v, stride);
-      const bool larger = ((lane & stride) == 0) == ((lane & size) == 0);
-      v = larger == (v < o) ? o : v;
+  for (int q = 0; q < 8; ++q) {
+    const float4 o = reinterpret_cast<const float4*>(s_val)[q];
+    r += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+  }
+  return r;
+}
+// Sorts the n <= 64 candidates (key, expert) in place by (larger key, lower
+// expert): a lane ranks numbers lane and lane + 32.
+__device__ __forceinline__ void sort_candidates(float* s_ckey, int* s_ce, int n, int lane) {
+  const bool two = n > 32, h0 = lane < n, h1 = lane + 32 < n;
+  const float v0 = h0 ? s_ckey[lane] : neg_inf_f(), v1 = h1 ? s_ckey[lane + 32] : neg_inf_f();
+  const int e0 = h0 ? s_ce[lane] : 0, e1 = h1 ? s_ce[lane + 32] : 0;
+  if (!h0) s_ckey[lane] = v0;
+  if (two && !h1) s_ckey[lane + 32] = v1;
+  __syncwarp();
+  int r0 = count_larger(v0, s_ckey), r1 = 0;
+  if (two) {
+    r0 += count_larger(v0, s_ckey + 32);
+    r1 = count_larger(v1, s_ckey) + count_larger(v1, s_ckey + 32);
+  }
+  // equal keys have equal counts: then the index decides
+  const unsigned low = (h0 && r0 < 32 ? 1u << (r0 & 31) : 0u) | (h1 && r1 < 32 ? 1u << (r1 & 31) : 0u);
+  const unsigned high = (h0 && r0 >= 32 ? 1u << (r0 & 31) : 0u) | (h1 && r1 >= 32 ? 1u << (r1 & 31) : 0u);
+  int distinct = __popc(__reduce_or_sync(0xffffffffu, low));
+  if (two) distinct += __popc(__reduce_or_sync(0xffffffffu, high));
+  if (distinct != n) {
+#pragma unroll 1
+    for (int q = 0; q < n; ++q) {
+      r0 += s_ckey[q] == v0 && s_ce[q] < e0;
+      r1 += s_ckey[q] == v1 && s_ce[q] < e1;
     }
   }
-  return v;
+  __syncwarp();
+  if (h0) {
+    s_ckey[r0] = v0;
+    s_ce[r0] = e0;
+  }
+  if (h1) {
+    s_ckey[r1] = v1;
+    s_ce[r1] = e1;
+  }
+  __syncwarp();
 }
 
 // Groups in shared memory.  LPG lanes scan a group, VEC keys a lane and step;
@@ -136,8 +186,124 @@ struct Top2 {
 __device__ __forceinline__ unsigned long long ranked(float key, int e) {
   return (static_cast<unsigned long long>(order_key(key)) << 32) | (0xffffffffu - static_cast<unsigned>(e));
 }
-__device__ __forceinline__ int expert_of(unsigned long long v) {
-  return static_cast<int>(0xffffffffu - static_cast<uint32_t>(v));
+// Keys below this are below `v` beyond doubt.
+__device__ __forceinline__ float margin_cut(float v, float margin) {
+  return fmaxf(v - margin * fmaxf(1.f, fabsf(v)), -3.402823466e38f);
+}
+// ---- rare paths, kept out of the kernel's instruction stream: over the keys
+// of a row in shared memory in expert order, -inf where nothing can be chosen.
+
+// Candidates of the largest value that kk keys reach, less the margin, written
+// to s_ckey and s_ce; returns their number, which is above 64 (and nothing
+// written) where equal or close keys leave more.
+__device__ __noinline__ int cold_candidates(const float* s_key, int E, int kk, float bound, float umax, float margin,
+                                            float* s_ckey, int* s_ce) {
+  const unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  auto count = [&](float cut) {
+    unsigned c = 0;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32) c += s_key[e] >= cut;
+    return static_cast<int>(__reduce_add_sync(kAll, c));
+  };
+  uint32_t lo = order_key(bound), hi = order_key(umax) + 1;  // kk keys reach lo; fewer reach hi, or none
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const float v = order_key_inverse(mid);
+    const int c = count(v);
+    if (c >= kk) {
+      lo = mid;
+      if (c <= kMaxCand && count(margin_cut(v, margin)) <= kMaxCand) break;
+    } else {
+      hi = mid;
+    }
+  }
+  const float cut = margin_cut(order_key_inverse(lo), margin);
+  const int n = count(cut);
+  if (n > kMaxCand) return n;
+  int base = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    const float k = e < E ? s_key[e] : neg_inf_f();
+    const unsigned m = __ballot_sync(kAll, k >= cut);
+    if (k >= cut) {
+      const int at = base + __popc(m & ((1u << lane) - 1u));
+      s_ckey[at] = k;
+      s_ce[at] = e;
+    }
+    base += __popc(m);
+  }
+  __syncwarp();
+  return n;
+}
+
+// kk rounds of arg-max: more equal keys than lanes.  Lane j gets slot j.
+__device__ __noinline__ int cold_argmax(float* s_key, int E, int kk) {
+  const unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  int best = -1;
+  for (int j = 0; j < kk; ++j) {
+    unsigned long long v = 0;
+    for (int e = lane; e < E; e += 32) {
+      const unsigned long long o = s_key[e] > neg_inf_f() ? ranked(s_key[e], e) : 0ull;
+      v = o > v ? o : v;
+    }
+    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32));
+    const uint32_t low =
+        __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+    const unsigned long long won = (static_cast<unsigned long long>(hi) << 32) | low;
+    const int e = static_cast<int>(0xffffffffu - low);
+    if (lane == j) best = e;
+    if (v == won) s_key[e] = neg_inf_f();
+    __syncwarp();
+  }
+  return best;
+}
+
+// All keys exactly.
+__device__ __noinline__ void cold_exact_keys(float* s_key, const float* lg, const float* bias, int E, bool softmax,
+                                             float top) {
+  const int lane = threadIdx.x & 31;
+  double sum = 0.0;
+  if (softmax) {
+    for (int e = lane; e < E; e += 32) {
+      const float l = lg[e];
+      if (l > neg_inf_f()) sum += l == top ? 1.0 : exp(static_cast<double>(l) - top);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  }
+  for (int e = lane; e < E; e += 32) {
+    const float l = lg[e];
+    float k = neg_inf_f();
+    if (l > neg_inf_f()) {
+      const float s = softmax ? static_cast<float>((l == top ? 1.0 : exp(static_cast<double>(l) - top)) / sum)
+                              : sigmoid_exact_f32(l);
+      k = fmaxf(s + bias[e], neg_inf_f());
+    }
+    s_key[e] = k;
+  }
+  __syncwarp();
+}
+
+// The two largest exact keys among a lane's share of a group (keys j = sub,
+// sub + lpg, ... of `row`, experts from e0): those whose cheap key reaches
+// `reach`.
+__device__ __noinline__ Top2 cold_group_top2(const float* row, const float* lg, const float* bias, int e0, int sub,
+                                             int lpg, int per, float reach) {
+  Top2 two{neg_inf_f(), neg_inf_f()};
+  for (int j0 = sub; j0 < per; j0 += 32 * lpg) {
+    unsigned todo = 0;
+    for (int i = 0; i < 32 && j0 + i * lpg < per; ++i) {
+      const float k = row[j0 + i * lpg];
+      todo |= static_cast<unsigned>(k > neg_inf_f() && k >= reach) << i;
+    }
+    for (; todo != 0; todo &= todo - 1) {
+      const int e = e0 + j0 + (__ffs(todo) - 1) * lpg;
+      two.add(fmaxf(sigmoid_exact_f32(lg[e]) + bias[e], neg_inf_f()));
+    }
+  }
+  return two;
 }
 
 // KPL keys a lane, VEC of them consecutive (one 16-byte load for VEC = 4).
@@ -147,17 +313,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
                                                                             const RouteGroupArgs a, GroupLayout gl,
                                                                             int warp_words, int32_t* __restrict__ ids,
                                                                             float* __restrict__ wts) {
-  extern __shared__ uint4 s_all[];  // per warp: candidates [32] (8 bytes each), keys
+  extern __shared__ uint4 s_all[];  // per warp: candidate keys [64] and experts [64], all keys
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
   if (t >= a.T) return;
-  unsigned long long* s_cand =
-      reinterpret_cast<unsigned long long*>(reinterpret_cast<float*>(s_all) + static_cast<size_t>(warp) * warp_words);
-  float* s_key = reinterpret_cast<float*>(s_cand + 32);
+  float* s_ckey = reinterpret_cast<float*>(s_all) + static_cast<size_t>(warp) * warp_words;
+  int* s_ce = reinterpret_cast<int*>(s_ckey + kMaxCand);
+  float* s_key = s_ckey + 2 * kMaxCand;
   const float* lg = logits + static_cast<size_t>(t) * a.E;
   const float NEG = neg_inf_f();
   const unsigned kAll = 0xffffffffu;
   constexpr int kChunks = KPL / VEC;
+  const int chunks = (a.E + 32 * VEC - 1) / (32 * VEC);  // chunks in use, the same for all lanes
   auto first_of = [&](int q) { return VEC * (lane + 32 * q); };  // first expert of this lane's chunk q
   // chunk q of a row of E floats, -inf behind its end
   auto load = [&](const float* row, int q, float (&v)[VEC]) {
@@ -178,7 +345,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
 #pragma unroll
   for (int q = 0; q < kChunks; ++q) {
     float v[VEC];
-    load(lg, q, v);
+    load(lg, q, v);  // without a branch: all loads are in flight together
 #pragma unroll
     for (int j = 0; j < VEC; ++j) key[q * VEC + j] = fmaxf(v[j], NEG);  // NaN to -inf
   }
@@ -190,55 +357,41 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
     total = 0.f;
 #pragma unroll
     for (int i = 0; i < KPL; ++i)
-      if (key[i] > NEG) total += key[i] == top ? 1.f : __expf(key[i] - top);
+      if (key[i] > NEG) total += key[i] == top ? 1.f : fast_exp(key[i] - top);
     total = warp_sum(total);
   }
-  const float margin = BIAS ? (a.softmax ? kMarginSoftmax : kMarginSigmoid) : 0.f;
+  float margin = BIAS ? (a.softmax ? kMarginSoftmax : kMarginSigmoid) : 0.f;
 
   if constexpr (BIAS) {  // the cheap keys
     const float inv_total = 1.f / total;
+    auto keys = [&](auto score) {
 #pragma unroll
-    for (int q = 0; q < kChunks; ++q) {
-      float b[VEC];
-      load(bias, q, b);
+      for (int q = 0; q < kChunks; ++q) {
+        float b[VEC];
+        load(bias, q, b);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float& k = key[q * VEC + j];
-        const float s = a.softmax ? (k == top ? 1.f : __expf(k - top)) * inv_total
-                                  : __fdividef(1.f, 1.f + __expf(-k));
-        k = k > NEG ? fmaxf(s + b[j], NEG) : NEG;
+        for (int j = 0; j < VEC; ++j) {
+          float& k = key[q * VEC + j];
+          k = k > NEG ? fmaxf(score(k) + b[j], NEG) : NEG;
+        }
       }
-    }
+    };
+    if (a.softmax)
+      keys([&](float l) { return (l == top ? 1.f : fast_exp(l - top)) * inv_total; });
+    else
+      keys([&](float l) { return fast_rcp(1.f + fast_exp(-l)); });
   }
-  unsigned long long best = 0;  // lane j: slot j
-  int kk = 0;                   // slots filled
+  int group_at[kChunks];  // this lane's chunks: their groups
+#pragma unroll
+  for (int q = 0; q < kChunks; ++q) group_at[q] = a.n_group > 1 && q < chunks ? gl.group(first_of(q)) : 0;
+  int id = -1;  // lane j: slot j
+  int kk = 0;   // slots filled
   bool exact = !BIAS, redo = false;
   for (;;) {
     if (BIAS && redo) {  // all keys exactly
       exact = true;
-      double sum = 0.0;
-      if (a.softmax) {
-#pragma unroll 1
-        for (int e = lane; e < a.E; e += 32) {
-          const float l = lg[e];
-          if (l > NEG) sum += l == top ? 1.0 : exp(static_cast<double>(l) - top);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-      }
-#pragma unroll 1
-      for (int e = lane; e < a.E; e += 32) {
-        const float l = lg[e];
-        float k = NEG;
-        if (l > NEG) {
-          const float s = a.softmax
-                              ? static_cast<float>((l == top ? 1.0 : exp(static_cast<double>(l) - top)) / sum)
-                              : sigmoid_exact_f32(l);
-          k = fmaxf(s + bias[e], NEG);
-        }
-        s_key[e] = k;
-      }
-      __syncwarp();
+      margin = 0.f;
+      cold_exact_keys(s_key, lg, bias, a.E, a.softmax, top);
 #pragma unroll
       for (int i = 0; i < KPL; ++i) {
         const int e = first_of(i / VEC) + i % VEC;
@@ -246,14 +399,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
       }
       __syncwarp();
     }
-    // ---- groups
-    if (a.n_group > 1) {
-      const int gap = gl.stride - gl.per;
+    // the keys into shared memory, groups apart
+    const int gap = gl.stride - gl.per;
+    auto to_smem = [&]() {
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) {
+        if (q >= chunks) break;
         const int e = first_of(q);
         if (e < a.E) {
-          float* at = s_key + e + gl.group(e) * gap;
+          float* at = s_key + e + group_at[q] * gap;
           if constexpr (VEC == 4)
             *reinterpret_cast<float4*>(at) = make_float4(key[4 * q], key[4 * q + 1], key[4 * q + 2], key[4 * q + 3]);
           else
@@ -261,6 +415,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
         }
       }
       __syncwarp();
+    };
+    bool in_smem = false;
+    // ---- groups
+    if (a.n_group > 1) {
+      to_smem();
+      in_smem = true;
       const int g = lane / gl.lpg, sub = lane - g * gl.lpg;
       const bool mine = g < a.n_group;
       const float* row = s_key + g * gl.stride;
@@ -281,24 +441,25 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
       }
       two.merge(gl.lpg);
       float gs;
-      bool keep;
+      int better;
       auto rank_groups = [&]() {
         gs = BIAS && two.k2 > NEG ? two.k1 + two.k2 : two.k1;
-        int better = 0;
+        better = 0;
+#pragma unroll 8
         for (int q = 0; q < a.n_group; ++q) {
           const float o = __shfl_sync(kAll, gs, q * gl.lpg);
           better += o > gs || (o == gs && q < g);
         }
-        keep = better < a.topk_group;
       };
       rank_groups();
-      if (BIAS && !exact) {
-        // the closest kept and dropped groups; a key's error grows with its size, so with the largest
-        const bool live = mine && two.k1 > NEG;
-        float size = live ? fmaxf(1.f, fabsf(two.k1)) : 1.f;
-        if (live && two.k2 > NEG) size = fmaxf(size, fabsf(two.k2));
-        size = warp_max(size);
-        const float in = -warp_max(live && keep ? -gs : NEG), out = warp_max(live && !keep ? gs : NEG);
+      if (BIAS && !exact && a.topk_group < a.n_group) {
+        // the last kept and the first dropped group
+        const float in = __shfl_sync(kAll, gs, __ffs(__ballot_sync(kAll, mine && better == a.topk_group - 1)) - 1);
+        const float out = __shfl_sync(kAll, gs, __ffs(__ballot_sync(kAll, mine && better == a.topk_group)) - 1);
+        // a key's error grows with its size: with the largest of all groups
+        float size = mine && two.k1 > NEG ? fabsf(two.k1) : 0.f;
+        if (mine && two.k2 > NEG) size = fmaxf(size, fabsf(two.k2));
+        size = fmaxf(1.f, __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size))));
         if (out > NEG && !(in - out > 2.f * margin * size)) {
           if (a.softmax || size > 1e30f) {
             redo = true;
@@ -306,35 +467,19 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
           }
           // exact keys of what can be among a group's two largest
           const float reach = (two.k2 > NEG ? two.k2 : two.k1) - margin * size;
-          two = Top2{NEG, NEG};
-          if (mine) {
-#pragma unroll 1
-            for (int j0 = sub; j0 < gl.per; j0 += 32 * gl.lpg) {
-              unsigned todo = 0;
-              for (int i = 0; i < 32 && j0 + i * gl.lpg < gl.per; ++i) {
-                const float k = row[j0 + i * gl.lpg];
-                todo |= static_cast<unsigned>(k > NEG && k >= reach) << i;
-              }
-#pragma unroll 1
-              for (; todo != 0; todo &= todo - 1) {
-                const int e = g * gl.per + j0 + (__ffs(todo) - 1) * gl.lpg;
-                two.add(fmaxf(sigmoid_exact_f32(lg[e]) + bias[e], NEG));
-              }
-            }
-          }
+          two = mine ? cold_group_top2(row, lg, bias, g * gl.per, sub, gl.lpg, gl.per, reach) : Top2{NEG, NEG};
           __syncwarp();
           two.merge(gl.lpg);
           rank_groups();
         }
       }
-      const unsigned kept = __ballot_sync(kAll, mine && keep);  // group q at bit q * lpg
+      const unsigned kept = __ballot_sync(kAll, mine && better < a.topk_group);  // group q at bit q * lpg
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) {
-        const int e = first_of(q);
-        if (e < a.E && !((kept >> (gl.group(e) * gl.lpg)) & 1u)) {
+        if (q >= chunks) break;
+        const float most = (kept >> (group_at[q] * gl.lpg)) & 1u ? -NEG : NEG;
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) key[q * VEC + j] = NEG;
-        }
+        for (int j = 0; j < VEC; ++j) key[q * VEC + j] = fminf(key[q * VEC + j], most);
       }
       __syncwarp();
     }
@@ -342,9 +487,24 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
     float lmax = NEG;
 #pragma unroll
     for (int i = 0; i < KPL; ++i) lmax = fmaxf(lmax, key[i]);
-    const float sorted = warp_sort_desc(lmax, lane);
-    float bound = __shfl_sync(kAll, sorted, a.k - 1);  // at least k keys reach it
-    const float umax = __shfl_sync(kAll, sorted, 0);
+    s_ckey[lane] = lmax;
+    __syncwarp();
+    const int larger = count_larger(lmax, s_ckey);
+    // the k-th largest lane maximum, which at least k keys reach, and the largest
+    float bound = order_key_inverse(__reduce_min_sync(kAll, larger < a.k ? order_key(lmax) : 0xffffffffu));
+    const float umax = __shfl_sync(kAll, lmax, __ffs(__ballot_sync(kAll, larger == 0)) - 1);
+    __syncwarp();
+    if (a.k > 16) {  // half as many lanes hold two keys that reach it
+      Top2 two{NEG, NEG};
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) two.add(key[i]);
+      s_ckey[lane] = two.k2;
+      __syncwarp();
+      const int l2 = count_larger(two.k2, s_ckey);
+      bound = fmaxf(bound, order_key_inverse(
+                               __reduce_min_sync(kAll, l2 < (a.k + 1) / 2 ? order_key(two.k2) : 0xffffffffu)));
+      __syncwarp();
+    }
     kk = a.k;
     if (!(bound > NEG)) {  // fewer lanes than slots have anything to choose from
       unsigned alive = 0;
@@ -358,59 +518,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
       redo = true;
       continue;
     }
-    auto cut_of = [&](float v) { return exact ? v : fmaxf(v - margin * fmaxf(1.f, fabsf(v)), -3.402823466e38f); };
-    auto candidates = [&](float cut, unsigned& mask) {
-      mask = 0;
+    const float cut = margin_cut(bound, margin);
+    unsigned mask = 0;
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) mask |= static_cast<unsigned>(key[i] >= cut) << i;
-      return static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(__popc(mask))));
-    };
-    unsigned mask;
-    int n = candidates(cut_of(bound), mask);
-    if (n > 32) {
-      uint32_t lo = order_key(bound), hi = order_key(umax) + 1;  // kk keys reach lo; fewer reach hi, or none
-      unsigned unused;
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const float v = order_key_inverse(mid);
-        const int c = candidates(v, unused);
-        if (c >= kk) {
-          lo = mid;
-          if (c <= 32 && candidates(cut_of(v), unused) <= 32) break;
-        } else {
-          hi = mid;
-        }
-      }
-      n = candidates(cut_of(order_key_inverse(lo)), mask);
-    }
-    if (n > 32) {
-      if (!exact) {
-        redo = true;
-        continue;
-      }
-      // more equal keys than lanes: one slot a round
-#pragma unroll 1
-      for (int j = 0; j < kk; ++j) {
-        unsigned long long v = 0;
-        int slot = 0;
-#pragma unroll
-        for (int i = 0; i < KPL; ++i) {
-          const unsigned long long o = ranked(key[i], first_of(i / VEC) + i % VEC);
-          if (((mask >> i) & 1u) && o > v) {
-            v = o;
-            slot = i;
-          }
-        }
-        const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32));
-        const uint32_t low =
-            __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
-        const unsigned long long won = (static_cast<unsigned long long>(hi) << 32) | low;
-        if (lane == j) best = won;
-        if (v == won) mask &= ~(1u << slot);
-      }
-      break;
-    }
-    // ---- one candidate a lane, sorted
+    for (int i = 0; i < KPL; ++i) mask |= static_cast<unsigned>(key[i] >= cut) << i;
     const int own = __popc(mask);
     int pos = own;
 #pragma unroll
@@ -418,41 +529,65 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
       const int o = __shfl_up_sync(kAll, pos, off);
       if (lane >= off) pos += o;
     }
-    pos -= own;
+    int n = __shfl_sync(kAll, pos, 31);
+    if (n <= kMaxCand) {
+      pos -= own;
+      // their keys are read where they lie: an index into registers is not possible
+      if (!in_smem) to_smem();
+#pragma unroll 1
+      for (; mask != 0; mask &= mask - 1, ++pos) {
+        const int i = __ffs(mask) - 1;
+        const int e = VEC * (lane + 32 * (i / VEC)) + i % VEC;
+        s_ckey[pos] = s_key[a.n_group > 1 ? e + gl.group(e) * gap : e];
+        s_ce[pos] = e;
+      }
+      __syncwarp();
+    } else {
+      __syncwarp();
 #pragma unroll
-    for (int i = 0; i < KPL; ++i)
-      if ((mask >> i) & 1u) s_cand[pos++] = ranked(key[i], first_of(i / VEC) + i % VEC);
-    __syncwarp();
-    best = lane < n ? s_cand[lane] : 0ull;
-    __syncwarp();
-    best = warp_sort_desc(best, lane);
-    if (exact) break;
-    const float self = order_key_inverse(static_cast<uint32_t>(best >> 32));
-    const unsigned long long nb = __shfl_down_sync(kAll, best, 1);
-    bool close = false;
-    if (lane < kk && lane + 1 < n) {
-      const float next = order_key_inverse(static_cast<uint32_t>(nb >> 32));
-      close = !(self - next > margin * fmaxf(1.f, fmaxf(fabsf(self), fabsf(next))));
-      if (close) {  // equal inputs have equal keys: their index decides, as it did
-        const int e = expert_of(best), f = expert_of(nb);
-        close = !(lg[e] == lg[f] && bias[e] == bias[f]);
+      for (int i = 0; i < KPL; ++i) {
+        const int e = first_of(i / VEC) + i % VEC;
+        if (e < a.E) s_key[e] = key[i];
+      }
+      __syncwarp();
+      n = cold_candidates(s_key, a.E, kk, bound, umax, margin, s_ckey, s_ce);
+      if (n > kMaxCand) {
+        if (!exact) {
+          redo = true;
+          continue;
+        }
+        id = cold_argmax(s_key, a.E, kk);
+        break;
       }
     }
-    if (!__any_sync(kAll, close)) break;
-    if (a.softmax) {
-      redo = true;
-      continue;
+    sort_candidates(s_ckey, s_ce, n, lane);
+    if (!exact) {
+      bool close = false;
+      if (lane < kk && lane + 1 < n) {
+        const float k0 = s_ckey[lane], k1 = s_ckey[lane + 1];
+        close = !(k0 - k1 > margin * fmaxf(1.f, fmaxf(fabsf(k0), fabsf(k1))));
+        if (close) {  // equal inputs have equal keys: their index decides, as it did
+          const int e = s_ce[lane], f = s_ce[lane + 1];
+          close = !(lg[e] == lg[f] && bias[e] == bias[f]);
+        }
+      }
+      if (__any_sync(kAll, close)) {
+        if (a.softmax) {
+          redo = true;
+          continue;
+        }
+#pragma unroll 1
+        for (int c = lane; c < n; c += 32) s_ckey[c] = sigmoid_exact_f32(lg[s_ce[c]]) + bias[s_ce[c]];
+        __syncwarp();
+        sort_candidates(s_ckey, s_ce, n, lane);
+      }
     }
-    if (lane < n) {
-      const int e = expert_of(best);
-      best = ranked(sigmoid_exact_f32(lg[e]) + bias[e], e);
-    }
-    best = warp_sort_desc(best, lane);
+    id = s_ce[lane];
     break;
   }
 
   // ---- weights
-  const int id = lane < kk ? expert_of(best) : -1;
+  if (lane >= kk) id = -1;
   const float p = chosen_share(id >= 0 ? lg[id] : NEG, a, top, total).p;
   if (lane < a.k) {
     ids[static_cast<size_t>(t) * a.k + lane] = id;
@@ -472,7 +607,7 @@ cudaError_t launch_route_vec(const float* logits, const float* bias, const Route
   gl.inv = 1.f / static_cast<float>(gl.per);
   gl.first = 0.5f * gl.inv - 0.5f;
   const int words = gl.stride * a.n_group > a.E ? gl.stride * a.n_group : a.E;
-  const int warp_words = 64 + (words + 3) / 4 * 4;
+  const int warp_words = 2 * kMaxCand + (words + 3) / 4 * 4;
   // few tokens: a warp a block, spread over the SMs
   const int warps = a.T <= 152 * kRouteWarps ? 1 : kRouteWarps;
   const size_t smem = static_cast<size_t>(warps) * warp_words * 4;
