@@ -435,7 +435,7 @@ def _rows_on(t, name, ncols_name):
 def _new(shape, dtype, dev, stream):
     """An output or workspace of a call on `stream`: the allocator keeps its
     memory from reuse until that stream is through with it."""
-    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    t = torch.empty(shape, dtype=dtype, device=dev)
     if stream is not None:
         t.record_stream(stream)
     return t

@@ -153,18 +153,15 @@ __device__ __forceinline__ void sort_candidates(float* s_ckey, int* s_ce, int n,
   __syncwarp();
 }
 
-// Groups in shared memory.  LPG lanes scan a group, VEC keys a lane and step;
-// groups start LPG * VEC banks apart (modulo 32), so that the warp's scan of
-// all groups has no bank conflicts.
-struct GroupLayout {
-  int per, lpg, stride;
-  float inv;    // 1 / per
-  float first;  // (0.5 - per / 2) / per
-  // Group of expert e: the nearest integer to (e + 0.5) / per - 0.5, which is never within
-  // 0.5 / per >= 2^-11 of half-way, read off the mantissa of its sum with 1.5 * 2^23.
-  __device__ __forceinline__ int group(int e) const {
-    return static_cast<int>(__float_as_uint(fmaf(static_cast<float>(e), inv, first) + 12582912.f) & 63u);
-  }
+// Keys in shared memory, group after group.  LPG lanes scan a group, VEC keys a
+// lane and step; groups start LPG * VEC banks apart (modulo 32), so that the
+// warp's scan of all groups has no bank conflicts.
+struct KeyLayout {
+  int E, per, gap;  // experts, experts a group, words between groups
+  int lpg, mul;     // lanes a group, ceil-like 2^20 / per
+  // floor(e / per): mul exceeds 2^20 / per by at most 1, times e < 1024 that is below 2^20 / per
+  __device__ __forceinline__ int group(int e) const { return (e * mul) >> 20; }
+  __device__ __forceinline__ int at(int e) const { return e + group(e) * gap; }
 };
 
 struct Top2 {
@@ -183,27 +180,28 @@ struct Top2 {
   }
 };
 
-__device__ __forceinline__ unsigned long long ranked(float key, int e) {
-  return (static_cast<unsigned long long>(order_key(key)) << 32) | (0xffffffffu - static_cast<unsigned>(e));
-}
 // Keys below this are below `v` beyond doubt.
 __device__ __forceinline__ float margin_cut(float v, float margin) {
   return fmaxf(v - margin * fmaxf(1.f, fabsf(v)), -3.402823466e38f);
 }
-// ---- rare paths, kept out of the kernel's instruction stream: over the keys
-// of a row in shared memory in expert order, -inf where nothing can be chosen.
+
+// ---- rare paths, kept out of the kernel's instruction stream.  `kept` has the
+// bits of the groups that experts are chosen from, group g at bit g * lpg.
 
 // Candidates of the largest value that kk keys reach, less the margin, written
 // to s_ckey and s_ce; returns their number, which is above 64 (and nothing
 // written) where equal or close keys leave more.
-__device__ __noinline__ int cold_candidates(const float* s_key, int E, int kk, float bound, float umax, float margin,
-                                            float* s_ckey, int* s_ce) {
+__device__ __noinline__ int cold_candidates(const float* s_key, const KeyLayout& kl, unsigned kept, int kk, float bound,
+                                            float umax, float margin, float* s_ckey, int* s_ce) {
   const unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
+  auto key = [&](int e) {
+    return e < kl.E && ((kept >> (kl.group(e) * kl.lpg)) & 1u) ? s_key[kl.at(e)] : neg_inf_f();
+  };
   auto count = [&](float cut) {
     unsigned c = 0;
 #pragma unroll 4
-    for (int e = lane; e < E; e += 32) c += s_key[e] >= cut;
+    for (int e = lane; e < kl.E; e += 32) c += key(e) >= cut;
     return static_cast<int>(__reduce_add_sync(kAll, c));
   };
   uint32_t lo = order_key(bound), hi = order_key(umax) + 1;  // kk keys reach lo; fewer reach hi, or none
@@ -222,14 +220,13 @@ __device__ __noinline__ int cold_candidates(const float* s_key, int E, int kk, f
   const int n = count(cut);
   if (n > kMaxCand) return n;
   int base = 0;
-  for (int e0 = 0; e0 < E; e0 += 32) {
-    const int e = e0 + lane;
-    const float k = e < E ? s_key[e] : neg_inf_f();
+  for (int e0 = 0; e0 < kl.E; e0 += 32) {
+    const float k = key(e0 + lane);
     const unsigned m = __ballot_sync(kAll, k >= cut);
     if (k >= cut) {
       const int at = base + __popc(m & ((1u << lane) - 1u));
       s_ckey[at] = k;
-      s_ce[at] = e;
+      s_ce[at] = e0 + lane;
     }
     base += __popc(m);
   }
@@ -237,43 +234,44 @@ __device__ __noinline__ int cold_candidates(const float* s_key, int E, int kk, f
   return n;
 }
 
-// kk rounds of arg-max: more equal keys than lanes.  Lane j gets slot j.
-__device__ __noinline__ int cold_argmax(float* s_key, int E, int kk) {
+// kk rounds of arg-max: more equal keys than candidates fit.  Lane j gets slot j.
+__device__ __noinline__ int cold_argmax(float* s_key, const KeyLayout& kl, unsigned kept, int kk) {
   const unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   int best = -1;
   for (int j = 0; j < kk; ++j) {
-    unsigned long long v = 0;
-    for (int e = lane; e < E; e += 32) {
-      const unsigned long long o = s_key[e] > neg_inf_f() ? ranked(s_key[e], e) : 0ull;
-      v = o > v ? o : v;
+    uint32_t key = 0, low = 0;  // the lane's best: its key's image, ~expert
+    for (int e = lane; e < kl.E; e += 32) {
+      const float k = (kept >> (kl.group(e) * kl.lpg)) & 1u ? s_key[kl.at(e)] : neg_inf_f();
+      const uint32_t image = k > neg_inf_f() ? order_key(k) : 0u;
+      if (image > key) {
+        key = image;
+        low = 0xffffffffu - static_cast<unsigned>(e);
+      }
     }
-    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32));
-    const uint32_t low =
-        __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
-    const unsigned long long won = (static_cast<unsigned long long>(hi) << 32) | low;
-    const int e = static_cast<int>(0xffffffffu - low);
+    const uint32_t top = __reduce_max_sync(kAll, key);
+    const int e = static_cast<int>(0xffffffffu - __reduce_max_sync(kAll, key == top ? low : 0u));
     if (lane == j) best = e;
-    if (v == won) s_key[e] = neg_inf_f();
+    if ((e & 31) == lane) s_key[kl.at(e)] = neg_inf_f();
     __syncwarp();
   }
   return best;
 }
 
 // All keys exactly.
-__device__ __noinline__ void cold_exact_keys(float* s_key, const float* lg, const float* bias, int E, bool softmax,
-                                             float top) {
+__device__ __noinline__ void cold_exact_keys(float* s_key, const KeyLayout& kl, const float* lg, const float* bias,
+                                             bool softmax, float top) {
   const int lane = threadIdx.x & 31;
   double sum = 0.0;
   if (softmax) {
-    for (int e = lane; e < E; e += 32) {
+    for (int e = lane; e < kl.E; e += 32) {
       const float l = lg[e];
       if (l > neg_inf_f()) sum += l == top ? 1.0 : exp(static_cast<double>(l) - top);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   }
-  for (int e = lane; e < E; e += 32) {
+  for (int e = lane; e < kl.E; e += 32) {
     const float l = lg[e];
     float k = neg_inf_f();
     if (l > neg_inf_f()) {
@@ -281,7 +279,7 @@ __device__ __noinline__ void cold_exact_keys(float* s_key, const float* lg, cons
                               : sigmoid_exact_f32(l);
       k = fmaxf(s + bias[e], neg_inf_f());
     }
-    s_key[e] = k;
+    s_key[kl.at(e)] = k;
   }
   __syncwarp();
 }
@@ -306,13 +304,18 @@ __device__ __noinline__ Top2 cold_group_top2(const float* row, const float* lg, 
   return two;
 }
 
-// KPL keys a lane, VEC of them consecutive (one 16-byte load for VEC = 4).
-template <int KPL, int VEC, bool BIAS>
-__global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(const float* __restrict__ logits,
-                                                                            const float* __restrict__ bias,
-                                                                            const RouteGroupArgs a, GroupLayout gl,
-                                                                            int warp_words, int32_t* __restrict__ ids,
-                                                                            float* __restrict__ wts) {
+// The keys live in shared memory and every pass over them is a short loop: few
+// registers (so that many tokens share an SM) and little code, which matter
+// more here than the loads saved by keeping them in registers (28 keys a lane
+// in registers and unrolled passes: 20 warps an SM, a fifth of their cycles
+// without an instruction to issue; T = 8192, E = 896, k = 16, 8 groups: 23.4
+// us against 20.9).  VEC keys are consecutive on a lane (16-byte loads).
+template <int VEC, bool BIAS>
+__global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(const float* __restrict__ logits,
+                                                                             const float* __restrict__ bias,
+                                                                             const RouteGroupArgs a, const KeyLayout kl,
+                                                                             int warp_words, int32_t* __restrict__ ids,
+                                                                             float* __restrict__ wts) {
   extern __shared__ uint4 s_all[];  // per warp: candidate keys [64] and experts [64], all keys
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
@@ -323,131 +326,125 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
   const float* lg = logits + static_cast<size_t>(t) * a.E;
   const float NEG = neg_inf_f();
   const unsigned kAll = 0xffffffffu;
-  constexpr int kChunks = KPL / VEC;
-  const int chunks = (a.E + 32 * VEC - 1) / (32 * VEC);  // chunks in use, the same for all lanes
-  auto first_of = [&](int q) { return VEC * (lane + 32 * q); };  // first expert of this lane's chunk q
-  // chunk q of a row of E floats, -inf behind its end
-  auto load = [&](const float* row, int q, float (&v)[VEC]) {
-    const int e = first_of(q);
+  const int step = 32 * VEC;
+
+  auto load = [&](const float* row, int e, float (&v)[VEC]) {
     if constexpr (VEC == 4) {
-      const float4 f = e < a.E ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(NEG, NEG, NEG, NEG);
+      const float4 f = __ldg(reinterpret_cast<const float4*>(row + e));
       v[0] = f.x;
       v[1] = f.y;
       v[2] = f.z;
       v[3] = f.w;
     } else {
-      v[0] = e < a.E ? __ldg(row + e) : NEG;
+      v[0] = __ldg(row + e);
     }
   };
+  auto put = [&](int at, const float (&v)[VEC]) {
+    if constexpr (VEC == 4)
+      *reinterpret_cast<float4*>(s_key + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      s_key[at] = v[0];
+  };
+  auto get = [&](int at, float (&v)[VEC]) {
+    if constexpr (VEC == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(s_key + at);
+      v[0] = f.x;
+      v[1] = f.y;
+      v[2] = f.z;
+      v[3] = f.w;
+    } else {
+      v[0] = s_key[at];
+    }
+  };
+  auto sigmoid_keys = [&](float (&v)[VEC], const float (&b)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      v[j] = v[j] > NEG ? fmaxf(fast_rcp(1.f + fast_exp(-v[j])) + b[j], NEG) : NEG;
+  };
 
-  // the row's logits; what cannot be chosen is -inf
-  float key[KPL];
+  // ---- keys: cheap ones; what cannot be chosen is -inf
+  float lmax = NEG;  // of this lane's keys
+  const bool denominator = a.softmax && (BIAS || !a.renormalize);
+#pragma unroll 2
+  for (int e = VEC * lane; e < a.E; e += step) {
+    float v[VEC], b[VEC];
+    load(lg, e, v);
+    if (BIAS) load(bias, e, b);
 #pragma unroll
-  for (int q = 0; q < kChunks; ++q) {
-    float v[VEC];
-    load(lg, q, v);  // without a branch: all loads are in flight together
+    for (int j = 0; j < VEC; ++j) v[j] = fmaxf(v[j], NEG);  // NaN to -inf
+    if (BIAS && !a.softmax) sigmoid_keys(v, b);
+    put(kl.at(e), v);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) key[q * VEC + j] = fmaxf(v[j], NEG);  // NaN to -inf
+    for (int j = 0; j < VEC; ++j) lmax = fmaxf(lmax, v[j]);
   }
   float top = NEG, total = 1.f;
-  if (a.softmax && (BIAS || !a.renormalize)) {
-#pragma unroll
-    for (int i = 0; i < KPL; ++i) top = fmaxf(top, key[i]);
-    top = warp_max(top);
+  if (denominator) {  // what is stored are logits; a lane reads what it wrote
+    top = warp_max(lmax);
     total = 0.f;
+    for (int e = VEC * lane; e < a.E; e += step) {
+      float v[VEC];
+      get(kl.at(e), v);
 #pragma unroll
-    for (int i = 0; i < KPL; ++i)
-      if (key[i] > NEG) total += key[i] == top ? 1.f : fast_exp(key[i] - top);
+      for (int j = 0; j < VEC; ++j)
+        if (v[j] > NEG) total += v[j] == top ? 1.f : fast_exp(v[j] - top);
+    }
     total = warp_sum(total);
-  }
-  float margin = BIAS ? (a.softmax ? kMarginSoftmax : kMarginSigmoid) : 0.f;
-
-  if constexpr (BIAS) {  // the cheap keys
-    const float inv_total = 1.f / total;
-    auto keys = [&](auto score) {
-#pragma unroll
-      for (int q = 0; q < kChunks; ++q) {
-        float b[VEC];
-        load(bias, q, b);
+    if (BIAS) {
+      const float inv_total = 1.f / total;
+      lmax = NEG;
+      for (int e = VEC * lane; e < a.E; e += step) {
+        float v[VEC], b[VEC];
+        get(kl.at(e), v);
+        load(bias, e, b);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          float& k = key[q * VEC + j];
-          k = k > NEG ? fmaxf(score(k) + b[j], NEG) : NEG;
+          const float s = (v[j] == top ? 1.f : fast_exp(v[j] - top)) * inv_total;
+          v[j] = v[j] > NEG ? fmaxf(s + b[j], NEG) : NEG;
+          lmax = fmaxf(lmax, v[j]);
         }
+        put(kl.at(e), v);
       }
-    };
-    if (a.softmax)
-      keys([&](float l) { return (l == top ? 1.f : fast_exp(l - top)) * inv_total; });
-    else
-      keys([&](float l) { return fast_rcp(1.f + fast_exp(-l)); });
+    }
   }
-  int group_at[kChunks];  // this lane's chunks: their groups
-#pragma unroll
-  for (int q = 0; q < kChunks; ++q) group_at[q] = a.n_group > 1 && q < chunks ? gl.group(first_of(q)) : 0;
+  __syncwarp();
+
+  float margin = BIAS ? (a.softmax ? kMarginSoftmax : kMarginSigmoid) : 0.f;
   int id = -1;  // lane j: slot j
   int kk = 0;   // slots filled
   bool exact = !BIAS, redo = false;
   for (;;) {
-    if (BIAS && redo) {  // all keys exactly
+    if (BIAS && redo) {
       exact = true;
       margin = 0.f;
-      cold_exact_keys(s_key, lg, bias, a.E, a.softmax, top);
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) {
-        const int e = first_of(i / VEC) + i % VEC;
-        key[i] = e < a.E ? s_key[e] : NEG;
-      }
-      __syncwarp();
+      cold_exact_keys(s_key, kl, lg, bias, a.softmax, top);
     }
-    // the keys into shared memory, groups apart
-    const int gap = gl.stride - gl.per;
-    auto to_smem = [&]() {
-#pragma unroll
-      for (int q = 0; q < kChunks; ++q) {
-        if (q >= chunks) break;
-        const int e = first_of(q);
-        if (e < a.E) {
-          float* at = s_key + e + group_at[q] * gap;
-          if constexpr (VEC == 4)
-            *reinterpret_cast<float4*>(at) = make_float4(key[4 * q], key[4 * q + 1], key[4 * q + 2], key[4 * q + 3]);
-          else
-            *at = key[q];
-        }
-      }
-      __syncwarp();
-    };
-    bool in_smem = false;
-    // ---- groups
+    unsigned kept = kAll;
+    // a key of the row, -inf outside the kept groups
+    auto limit = [&](int g) { return (kept >> (g * kl.lpg)) & 1u ? -NEG : NEG; };
     if (a.n_group > 1) {
-      to_smem();
-      in_smem = true;
-      const int g = lane / gl.lpg, sub = lane - g * gl.lpg;
+      // ---- groups
+      const int g = lane / kl.lpg, sub = lane - g * kl.lpg;
       const bool mine = g < a.n_group;
-      const float* row = s_key + g * gl.stride;
+      const int row = g * (kl.per + kl.gap);
       Top2 two{NEG, NEG};
       if (mine) {
-#pragma unroll 4
-        for (int j = VEC * sub; j < gl.per; j += VEC * gl.lpg) {
-          if constexpr (VEC == 4) {
-            const float4 k = *reinterpret_cast<const float4*>(row + j);
-            two.add(k.x);
-            two.add(k.y);
-            two.add(k.z);
-            two.add(k.w);
-          } else {
-            two.add(row[j]);
-          }
+#pragma unroll 2
+        for (int j = VEC * sub; j < kl.per; j += VEC * kl.lpg) {
+          float v[VEC];
+          get(row + j, v);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) two.add(v[i]);
         }
       }
-      two.merge(gl.lpg);
+      two.merge(kl.lpg);
       float gs;
       int better;
       auto rank_groups = [&]() {
         gs = BIAS && two.k2 > NEG ? two.k1 + two.k2 : two.k1;
         better = 0;
-#pragma unroll 8
+#pragma unroll 4
         for (int q = 0; q < a.n_group; ++q) {
-          const float o = __shfl_sync(kAll, gs, q * gl.lpg);
+          const float o = __shfl_sync(kAll, gs, q * kl.lpg);
           better += o > gs || (o == gs && q < g);
         }
       };
@@ -467,26 +464,27 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
           }
           // exact keys of what can be among a group's two largest
           const float reach = (two.k2 > NEG ? two.k2 : two.k1) - margin * size;
-          two = mine ? cold_group_top2(row, lg, bias, g * gl.per, sub, gl.lpg, gl.per, reach) : Top2{NEG, NEG};
+          two = mine ? cold_group_top2(s_key + row, lg, bias, g * kl.per, sub, kl.lpg, kl.per, reach) : Top2{NEG, NEG};
           __syncwarp();
-          two.merge(gl.lpg);
+          two.merge(kl.lpg);
           rank_groups();
         }
       }
-      const unsigned kept = __ballot_sync(kAll, mine && better < a.topk_group);  // group q at bit q * lpg
+      kept = __ballot_sync(kAll, mine && better < a.topk_group);
+    }
+    if (a.n_group > 1 || (BIAS && redo)) {
+      lmax = NEG;
+      for (int e = VEC * lane; e < a.E; e += step) {
+        float v[VEC];
+        const int g = kl.group(e);
+        get(e + g * kl.gap, v);
+        float m = v[0];
 #pragma unroll
-      for (int q = 0; q < kChunks; ++q) {
-        if (q >= chunks) break;
-        const float most = (kept >> (group_at[q] * gl.lpg)) & 1u ? -NEG : NEG;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) key[q * VEC + j] = fminf(key[q * VEC + j], most);
+        for (int j = 1; j < VEC; ++j) m = fmaxf(m, v[j]);
+        lmax = fmaxf(lmax, fminf(m, limit(g)));
       }
-      __syncwarp();
     }
     // ---- candidates
-    float lmax = NEG;
-#pragma unroll
-    for (int i = 0; i < KPL; ++i) lmax = fmaxf(lmax, key[i]);
     s_ckey[lane] = lmax;
     __syncwarp();
     const int larger = count_larger(lmax, s_ckey);
@@ -496,8 +494,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
     __syncwarp();
     if (a.k > 16) {  // half as many lanes hold two keys that reach it
       Top2 two{NEG, NEG};
+      for (int e = VEC * lane; e < a.E; e += step) {
+        float v[VEC];
+        const int g = kl.group(e);
+        const float most = limit(g);
+        get(e + g * kl.gap, v);
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) two.add(key[i]);
+        for (int j = 0; j < VEC; ++j) two.add(fminf(v[j], most));
+      }
       s_ckey[lane] = two.k2;
       __syncwarp();
       const int l2 = count_larger(two.k2, s_ckey);
@@ -508,8 +512,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
     kk = a.k;
     if (!(bound > NEG)) {  // fewer lanes than slots have anything to choose from
       unsigned alive = 0;
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) alive += key[i] > NEG;
+      for (int e = lane; e < a.E; e += 32) alive += fminf(s_key[kl.at(e)], limit(kl.group(e))) > NEG;
       kk = min(a.k, static_cast<int>(__reduce_add_sync(kAll, alive)));
       if (kk == 0) break;
       bound = -3.402823466e38f;  // the lowest finite key
@@ -519,9 +522,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
       continue;
     }
     const float cut = margin_cut(bound, margin);
-    unsigned mask = 0;
+    unsigned mask = 0;  // this lane's keys that reach it
+    int bit = 0;
+    for (int e = VEC * lane; e < a.E; e += step, bit += VEC) {
+      float v[VEC];
+      const int g = kl.group(e);
+      const float least = (kept >> (g * kl.lpg)) & 1u ? cut : __int_as_float(0x7fc00000);  // NaN: no key reaches it
+      get(e + g * kl.gap, v);
+      unsigned m = 0;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) mask |= static_cast<unsigned>(key[i] >= cut) << i;
+      for (int j = 0; j < VEC; ++j) m |= v[j] >= least ? 1u << j : 0u;
+      mask |= m << bit;
+    }
     const int own = __popc(mask);
     int pos = own;
 #pragma unroll
@@ -532,31 +544,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
     int n = __shfl_sync(kAll, pos, 31);
     if (n <= kMaxCand) {
       pos -= own;
-      // their keys are read where they lie: an index into registers is not possible
-      if (!in_smem) to_smem();
-#pragma unroll 1
       for (; mask != 0; mask &= mask - 1, ++pos) {
         const int i = __ffs(mask) - 1;
         const int e = VEC * (lane + 32 * (i / VEC)) + i % VEC;
-        s_ckey[pos] = s_key[a.n_group > 1 ? e + gl.group(e) * gap : e];
+        s_ckey[pos] = s_key[kl.at(e)];
         s_ce[pos] = e;
       }
       __syncwarp();
     } else {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) {
-        const int e = first_of(i / VEC) + i % VEC;
-        if (e < a.E) s_key[e] = key[i];
-      }
-      __syncwarp();
-      n = cold_candidates(s_key, a.E, kk, bound, umax, margin, s_ckey, s_ce);
+      n = cold_candidates(s_key, kl, kept, kk, bound, umax, margin, s_ckey, s_ce);
       if (n > kMaxCand) {
         if (!exact) {
           redo = true;
           continue;
         }
-        id = cold_argmax(s_key, a.E, kk);
+        id = cold_argmax(s_key, kl, kept, kk);
         break;
       }
     }
@@ -598,32 +600,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 5) route_grouped_kernel(cons
 template <int VEC, bool BIAS>
 cudaError_t launch_route_vec(const float* logits, const float* bias, const RouteGroupArgs& a, int32_t* ids, float* wts,
                              cudaStream_t st) {
-  GroupLayout gl{};
-  gl.per = a.E / a.n_group;
-  int lpg = 32;
-  while (lpg * a.n_group > 32) lpg >>= 1;
-  gl.lpg = lpg;
-  gl.stride = gl.per + ((VEC * lpg - gl.per) % 32 + 32) % 32;
-  gl.inv = 1.f / static_cast<float>(gl.per);
-  gl.first = 0.5f * gl.inv - 0.5f;
-  const int words = gl.stride * a.n_group > a.E ? gl.stride * a.n_group : a.E;
+  KeyLayout kl{};
+  kl.E = a.E;
+  kl.per = a.E / a.n_group;
+  kl.lpg = 32;
+  while (kl.lpg * a.n_group > 32) kl.lpg >>= 1;
+  kl.gap = a.n_group > 1 ? ((VEC * kl.lpg - kl.per) % 32 + 32) % 32 : 0;
+  kl.mul = (1 << 20) / kl.per + 1;
+  const int words = (kl.per + kl.gap) * a.n_group;
   const int warp_words = 2 * kMaxCand + (words + 3) / 4 * 4;
   // few tokens: a warp a block, spread over the SMs
   const int warps = a.T <= 152 * kRouteWarps ? 1 : kRouteWarps;
   const size_t smem = static_cast<size_t>(warps) * warp_words * 4;
-  const int blocks = (a.T + warps - 1) / warps;
-  const int kpl = (a.E + 32 * VEC - 1) / (32 * VEC) * VEC;
-#define KMOE_ROUTE(N)                                                                                                \
-  if (kpl <= N) {                                                                                                    \
-    route_grouped_kernel<N, VEC, BIAS><<<blocks, 32 * warps, smem, st>>>(logits, bias, a, gl, warp_words, ids, wts); \
-    return cudaGetLastError();                                                                                       \
-  }
-  KMOE_ROUTE(4)
-  KMOE_ROUTE(8)
-  KMOE_ROUTE(16)
-  KMOE_ROUTE(32)
-#undef KMOE_ROUTE
-  return cudaErrorInvalidValue;
+  route_grouped_kernel<VEC, BIAS><<<(a.T + warps - 1) / warps, 32 * warps, smem, st>>>(logits, bias, a, kl, warp_words,
+                                                                                       ids, wts);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_route_grouped(const float* logits, const float* bias, const RouteGroupArgs& a, int32_t* ids,
@@ -637,62 +628,130 @@ cudaError_t launch_route_grouped(const float* logits, const float* bias, const R
               : launch_route_vec<1, false>(logits, bias, a, ids, wts, st);
 }
 
-// One warp per token; lane j holds slot j.
+// ---------------------------------------------------------------- gradient
+// One warp a token; lane j holds slot j.  With p the weights without `scale`
+// and g = scale * d_w:
+//   renormalised: d_logit = p (g - sum g p) * slope at the chosen experts, 0
+//                 elsewhere (the softmax's common term cancels);
+//   sigmoid:      d_logit = g s (1 - s) at the chosen experts;
+//   softmax:      d_logit = p (g - sum g p) for all experts, g = 0 where not
+//                 chosen: the one form that reads the whole row (FULL).
+// Memory bounds it: E floats are written a token.  The row goes out as 16-byte
+// zeros (or softmax terms), then the chosen elements over them; a slot whose
+// expert an earlier slot has too (routing gives none) is added there.
+template <int KPL, int VEC, bool FULL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const float* __restrict__ d_w,
                                                                           const float* __restrict__ logits,
                                                                           const int32_t* __restrict__ ids,
-                                                                          RouteGroupArgs a,
+                                                                          const RouteGroupArgs a,
                                                                           float* __restrict__ d_logits) {
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.T) return;
   const float NEG = neg_inf_f();
   const float* lg = logits + static_cast<size_t>(t) * a.E;
   float* out = d_logits + static_cast<size_t>(t) * a.E;
+  constexpr int kChunks = KPL / VEC;
+  float p_all[FULL ? KPL : 1];
+  auto store_row = [&](float factor) {  // p_all * factor, or zeros
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q) {
+      const int e = VEC * (lane + 32 * q);
+      if (e >= a.E) break;
+      if constexpr (VEC == 4) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (FULL)
+          f = make_float4(p_all[4 * q] * factor, p_all[4 * q + 1] * factor, p_all[4 * q + 2] * factor,
+                          p_all[4 * q + 3] * factor);
+        *reinterpret_cast<float4*>(out + e) = f;
+      } else {
+        out[e] = FULL ? p_all[FULL ? q : 0] * factor : 0.f;
+      }
+    }
+  };
   int id = lane < a.k ? ids[static_cast<size_t>(t) * a.k + lane] : -1;
+  const float given_w = lane < a.k ? d_w[static_cast<size_t>(t) * a.k + lane] : 0.f;
   if (id < 0 || id >= a.E) id = -1;
-  const float given = id >= 0 ? lg[id] : NEG;
+  const float given = id >= 0 ? __ldg(lg + id) : NEG;
   const float l = given > NEG ? given : NEG;  // NaN too
-  const float g = l > NEG ? a.scale * d_w[static_cast<size_t>(t) * a.k + lane] : 0.f;
+  const float g = l > NEG ? a.scale * given_w : 0.f;
+
   float top = NEG, total = 1.f;
-  if (a.softmax && !a.renormalize) {
-    for (int e = lane; e < a.E; e += 32) top = fmaxf(top, lg[e]);
+  if constexpr (FULL) {
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q) {
+      const int e = VEC * (lane + 32 * q);
+      if constexpr (VEC == 4) {
+        const float4 f = e < a.E ? __ldg(reinterpret_cast<const float4*>(lg + e)) : make_float4(NEG, NEG, NEG, NEG);
+        p_all[4 * q] = f.x;
+        p_all[4 * q + 1] = f.y;
+        p_all[4 * q + 2] = f.z;
+        p_all[4 * q + 3] = f.w;
+      } else {
+        p_all[q] = e < a.E ? __ldg(lg + e) : NEG;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) top = fmaxf(top, p_all[i]);  // fmaxf drops NaN
     top = warp_max(top);
     total = 0.f;
-    for (int e = lane; e < a.E; e += 32)
-      if (lg[e] > NEG) total += lg[e] == top ? 1.f : expf(lg[e] - top);
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      p_all[i] = p_all[i] > NEG ? (p_all[i] == top ? 1.f : expf(p_all[i] - top)) : 0.f;
+      total += p_all[i];
+    }
     total = warp_sum(total);
   }
   const Share sh = chosen_share(l, a, top, total);
   const float s = sh.p;
   const float d = a.renormalize ? s * (g - warp_sum(g * s)) * sh.slope : g * s * sh.slope;
-  // slots of one expert (routing gives none) are added in slot order
+  float common = 0.f, factor = 0.f;  // sum g p, and what turns p_all into its row's terms
+  if constexpr (FULL) {
+    common = warp_sum(d);
+    factor = total > 0.f ? -common / total : 0.f;
+  }
+  store_row(factor);
   const unsigned same = __match_any_sync(0xffffffffu, id);
-  float acc = 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    const float o = __shfl_sync(0xffffffffu, d, j);
-    if ((same >> j) & 1u) acc += o;
-  }
-  if (a.softmax && !a.renormalize) {
-    const float dot = warp_sum(d);
-    for (int e = lane; e < a.E; e += 32) {
-      const float v = lg[e];
-      out[e] = v > NEG ? -(v == top ? 1.f : expf(v - top)) / total * dot : 0.f;
+  float acc = d;
+  if (__any_sync(0xffffffffu, id >= 0 && (same & (same - 1)) != 0)) {  // in slot order
+    acc = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const float o = __shfl_sync(0xffffffffu, d, j);
+      if ((same >> j) & 1u) acc += o;
     }
-    __syncwarp();
-    if (id >= 0 && l > NEG && lane == __ffs(same) - 1) out[id] = acc - s * dot;
-  } else {
-    for (int e = lane; e < a.E; e += 32) out[e] = 0.f;
-    __syncwarp();
-    if (id >= 0 && lane == __ffs(same) - 1) out[id] = acc;
   }
+  __syncwarp();  // the row's stores come before these
+  if (id >= 0 && l > NEG && lane == __ffs(same) - 1) out[id] = FULL ? fmaf(-s, common, acc) : acc;
+}
+
+template <int VEC>
+cudaError_t launch_route_backward_vec(const float* d_w, const float* logits, const int32_t* ids,
+                                      const RouteGroupArgs& a, float* d_logits, cudaStream_t st) {
+  const bool full = a.softmax && !a.renormalize;
+  const int warps = a.T <= 152 * kRouteWarps ? 1 : kRouteWarps;
+  const int blocks = (a.T + warps - 1) / warps;
+  const int kpl = (a.E + 32 * VEC - 1) / (32 * VEC) * VEC;
+#define KMOE_ROUTE(N)                                                                                          \
+  if (kpl <= N) {                                                                                              \
+    if (full)                                                                                                  \
+      route_backward_kernel<N, VEC, true><<<blocks, 32 * warps, 0, st>>>(d_w, logits, ids, a, d_logits);       \
+    else                                                                                                       \
+      route_backward_kernel<N, VEC, false><<<blocks, 32 * warps, 0, st>>>(d_w, logits, ids, a, d_logits);      \
+    return cudaGetLastError();                                                                                 \
+  }
+  KMOE_ROUTE(4)
+  KMOE_ROUTE(8)
+  KMOE_ROUTE(16)
+  KMOE_ROUTE(32)
+#undef KMOE_ROUTE
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_route_backward(const float* d_w, const float* logits, const int32_t* ids, const RouteGroupArgs& a,
                                   float* d_logits, cudaStream_t st) {
-  route_backward_kernel<<<(a.T + kRouteWarps - 1) / kRouteWarps, 32 * kRouteWarps, 0, st>>>(d_w, logits, ids, a,
-                                                                                           d_logits);
-  return cudaGetLastError();
+  const uintptr_t both = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(d_logits);
+  return (both & 15) == 0 && a.E % 4 == 0 ? launch_route_backward_vec<4>(d_w, logits, ids, a, d_logits, st)
+                                          : launch_route_backward_vec<1>(d_w, logits, ids, a, d_logits, st);
 }
 
 }  // namespace kmoe
