@@ -52,9 +52,11 @@ __host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, bool backward)
   const size_t stage = static_cast<size_t>(p.threads) * p.nc * chunk_bytes;
   if (stage * per_sm > kNormSmem) per_sm = 1;
   if (stage > kNormSmem) return NormPlan{};
-  const int want = (T + teams_per_block - 1) / teams_per_block;
-  p.blocks = want < kNormSMs * per_sm ? want : kNormSMs * per_sm;
-  const int rows = (T + p.blocks * teams_per_block - 1) / (p.blocks * teams_per_block);
+  // no more blocks than the rows of the longest need: the gradient's partial rows are fewer
+  const int want = (T + teams_per_block - 1) / teams_per_block, most = kNormSMs * per_sm;
+  const int rows = (want + most - 1) / most;
+  p.blocks = (want + rows - 1) / rows;
+  if (ragged && rows > 1) p.blocks = (p.blocks + 7) / 8 * 8;  // most is a multiple of 8
   p.stages = static_cast<int>(kNormSmem / per_sm / stage);
   if (p.stages > 4) p.stages = 4;
   if (p.stages > rows) p.stages = rows;
