@@ -238,7 +238,7 @@ __host__ inline bool make_layout(const kmoe_params& p, Layout& L) {
 // ---------------------------------------------------------------- numerics
 // 2^n as a float for n in [-127, 127] (exact).
 __device__ __forceinline__ float exp2i(int n) {
-  return n >= -126 ? __int_as_float((n + 127) << 23) : __int_as_float(0x00200000);
+  return n >= -126 ? __int_as_float((n + 127) << 23) : __int_as_float(0x00400000);
 }
 
 // Scale exponent of the microscaling rule: smallest e with amax <= qmax*2^e,

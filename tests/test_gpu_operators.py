@@ -473,6 +473,49 @@ def test_block_from_stream_to_gradients(K):
                         1e-6)
 
 
+def test_example_learns(K):
+    """The example's block runs and its gate learns from the gradients."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses = mod.main(steps=20)
+    assert all(np.isfinite(losses)) and losses[-1] < losses[0]
+
+
+def test_norm_codes_of_infinite_and_huge_values(K):
+    """A bf16 row with infinities quantises as kmoe_quantize_mx has it: the
+    scale byte 254, finite neighbours scaled by 2^-127."""
+    H = 128
+    x = randn(1, 4, H).to(BF).cuda()
+    w = torch.ones(H)
+    w[3], w[4], w[40], w[41] = float("inf"), 3e38, 3e38, -2e38
+    _, y, codes, scales = K.kmoe_rmsnorm(x, w.cuda(), mx=True)
+    c, s = K.kmoe_quantize_mx(y)
+    assert torch.equal(codes, c) and torch.equal(scales, s) and (scales == 254).any()
+    cr, sr = F.quantize_mx(F.bf16_decode(y.cpu().view(torch.int16).numpy()))
+    assert np.array_equal(codes.cpu().numpy(), cr) and np.array_equal(scales.cpu().numpy(), sr)
+
+
+def test_route_unaligned_rows(K):
+    """Logits and bias that start inside a 16-byte word, and odd expert counts, take the scalar loads."""
+    T, E, k = 37, 96, 8
+    logits, bias = 1.7 * randn(1, T, E), 0.1 * randn(2, E)
+    ri, rw = P.route_grouped(logits.numpy(), bias.numpy(), k, False, 8, 4)
+    for o1, o2 in ((1, 0), (0, 2), (3, 5)):
+        ids, w = K.kmoe_route_grouped(at_offset(logits, o1), at_offset(bias, o2), k, n_group=8, topk_group=4)
+        assert np.array_equal(ids.cpu().numpy(), ri)
+    d_w = randn(3, T, k)
+    ref = K.kmoe_route_backward(d_w.cuda(), logits.cuda(), ids, score="softmax", renormalize=False)
+    got = K.kmoe_route_backward(d_w.cuda(), at_offset(logits, 1), ids, score="softmax", renormalize=False,
+                                d_logits=at_offset(torch.zeros(T, E), 3))
+    check_route_gradient(got, P.route_backward(d_w.double().numpy(), logits.numpy(), ri, True, False, 1.0),
+                         d_w.double().numpy(), logits, ri, True, False, 1.0)
+    assert torch.allclose(got, ref, rtol=1e-5, atol=1e-7)
+
+
 def test_streams_and_graphs(K):
     """On a stream of its own, outputs allocated by the calls; then captured
     once and replayed on new inputs."""
