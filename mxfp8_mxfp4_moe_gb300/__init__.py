@@ -10,6 +10,7 @@ in-tree libkmoe.so and raises if it is missing (build it with
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -402,19 +403,25 @@ def kmoe_forward_mx(p, x_codes, x_scales, topk_ids, topk_w, w13_k, w2_k, out=Non
 
 def _args(stream, dev, named):
     """Checks (name, tensor, dtype, shape) of each argument, None passing, on
-    device ordinal `dev`.  The errors are _arg's and _gpu's.  A tensor that a
-    given stream uses is kept from reuse until that stream is through."""
+    device ordinal `dev`, and returns their addresses.  The errors are _arg's
+    and _gpu's.  A tensor that a given stream uses is kept from reuse until
+    that stream is through."""
+    at = []
     for name, t, dtype, shape in named:
-        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous()):
-            continue
-        for n, u, d, s in named:
-            _arg(u, n, d, s)
-        _gpu(**{n: u for n, u, _, _ in named})
-        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
+        if t is None:
+            at.append(None)
+        elif t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous():
+            at.append(t.data_ptr())
+        else:
+            for n, u, d, s in named:
+                _arg(u, n, d, s)
+            _gpu(**{n: u for n, u, _, _ in named})
+            raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
     if stream is not None:
         for _, t, _, _ in named:
             if t is not None:
                 t.record_stream(stream)
+    return at
 
 
 _current_stream = torch._C._cuda_getCurrentRawStream
@@ -439,10 +446,6 @@ def _new(shape, dtype, dev, stream):
     if stream is not None:
         t.record_stream(stream)
     return t
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
 
 
 KMOE_NORM_STREAM_F32 = 1
@@ -471,21 +474,25 @@ def kmoe_rmsnorm(x, weight, residual=None, eps=1e-6, mx=False, h=None, y=None, c
     if not mx and (codes is not None or scales is not None):
         raise ValueError("codes and scales need mx=True")
     rows = (T, H)
-    _args(stream, dev, (("x", x, torch.bfloat16, rows), ("weight", weight, wt, (H,)), ("residual", residual, st, rows),
-                        ("h", h, st, rows), ("y", y, torch.bfloat16, rows), ("codes", codes, torch.uint8, rows),
-                        ("scales", scales, torch.uint8, (T, H // 32))))
+    at = _args(stream, dev, (("x", x, torch.bfloat16, rows), ("residual", residual, st, rows),
+                             ("weight", weight, wt, (H,)), ("h", h, st, rows), ("y", y, torch.bfloat16, rows),
+                             ("codes", codes, torch.uint8, rows), ("scales", scales, torch.uint8, (T, H // 32))))
     if h is None and residual is not None:
-        h = _new((T, H), st, dev, stream)
+        h = _new(rows, st, dev, stream)
+        at[3] = h.data_ptr()
     if y is None:
-        y = _new((T, H), torch.bfloat16, dev, stream)
+        y = _new(rows, torch.bfloat16, dev, stream)
+        at[4] = y.data_ptr()
     if mx:
         if codes is None:
-            codes = _new((T, H), torch.uint8, dev, stream)
+            codes = _new(rows, torch.uint8, dev, stream)
+            at[5] = codes.data_ptr()
         if scales is None:
             scales = _new((T, H // 32), torch.uint8, dev, stream)
+            at[6] = scales.data_ptr()
     flags = (KMOE_NORM_STREAM_F32 if st is torch.float32 else 0) | (KMOE_NORM_WEIGHT_F32 if wt is torch.float32 else 0)
-    _check("kmoe_rmsnorm", _lib.kmoe_rmsnorm(_at(x), _at(residual), _at(weight), T, H, eps, flags, _at(h),
-                                             _at(y), _at(codes), _at(scales), _raw_stream(dev, stream)))
+    _check("kmoe_rmsnorm", _lib.kmoe_rmsnorm(at[0], at[1], at[2], T, H, eps, flags, at[3], at[4], at[5], at[6],
+                                             _raw_stream(dev, stream)))
     return h, y, codes, scales
 
 
@@ -501,25 +508,28 @@ def kmoe_rmsnorm_backward(dy, h, weight, dh_in=None, eps=1e-6, dh=None, dweight=
     st = _type_of(h, "h", None)
     wt = _type_of(weight, "weight", None)
     rows = (T, H)
-    _args(stream, dev, (("dy", dy, torch.bfloat16, rows), ("h", h, st, rows), ("weight", weight, wt, (H,)),
-                        ("dh_in", dh_in, st, rows), ("dh", dh, st, rows),
-                        ("dweight", dweight, torch.float32, (H,))))
+    at = _args(stream, dev, (("dy", dy, torch.bfloat16, rows), ("h", h, st, rows), ("weight", weight, wt, (H,)),
+                             ("dh_in", dh_in, st, rows), ("dh", dh, st, rows),
+                             ("dweight", dweight, torch.float32, (H,))))
     n = _lib.kmoe_rmsnorm_workspace_size(T, H)
     if workspace is None:
-        workspace = _new(max(n, 1), torch.uint8, dev, stream)
+        workspace = _new(n, torch.uint8, dev, stream)
     else:
         _arg(workspace, "workspace", torch.uint8, min_bytes=n)
         _gpu(workspace=workspace)
         if stream is not None:
             workspace.record_stream(stream)
+        n = workspace.numel()
     if dh is None:
-        dh = _new((T, H), st, dev, stream)
+        dh = _new(rows, st, dev, stream)
+        at[4] = dh.data_ptr()
     if dweight is None:
         dweight = _new((H,), torch.float32, dev, stream)
+        at[5] = dweight.data_ptr()
     flags = (KMOE_NORM_STREAM_F32 if st is torch.float32 else 0) | (KMOE_NORM_WEIGHT_F32 if wt is torch.float32 else 0)
     _check("kmoe_rmsnorm_backward", _lib.kmoe_rmsnorm_backward(
-        _at(dy), _at(h), _at(weight), _at(dh_in), T, H, eps, flags, _at(dh),
-        _at(dweight), _at(workspace), workspace.numel(), _raw_stream(dev, stream)))
+        at[0], at[1], at[2], at[3], T, H, eps, flags, at[4], at[5], workspace.data_ptr(), n,
+        _raw_stream(dev, stream)))
     return dh, dweight
 
 
@@ -528,11 +538,13 @@ KMOE_ROUTE_RENORMALIZE = 2
 _SCORES = {"sigmoid": 0, "softmax": KMOE_ROUTE_SOFTMAX}
 
 
+@functools.lru_cache(maxsize=256)
 def _route_params(T, E, k, n_group, topk_group, score, renormalize, scale):
+    """The C struct of these parameters (read only, so calls can share it)."""
     if score not in _SCORES:
         raise ValueError(f"score must be 'sigmoid' or 'softmax', got {score!r}")
-    return kmoe_route_params(T, E, k, n_group, topk_group,
-                             _SCORES[score] | (KMOE_ROUTE_RENORMALIZE if renormalize else 0), scale)
+    return ctypes.byref(kmoe_route_params(T, E, k, n_group, topk_group,
+                                          _SCORES[score] | (KMOE_ROUTE_RENORMALIZE if renormalize else 0), scale))
 
 
 def kmoe_route_grouped(logits, bias, k, score="sigmoid", n_group=1, topk_group=1, renormalize=True, scale=1.0,
@@ -542,15 +554,16 @@ def kmoe_route_grouped(logits, bias, k, score="sigmoid", n_group=1, topk_group=1
     optionally renormalised weights.  Returns (topk_ids, topk_w); slots no
     expert could fill hold id -1 and weight 0."""
     T, E, dev = _rows_on(logits, "logits", "E")
-    _args(stream, dev, (("logits", logits, torch.float32, (T, E)), ("bias", bias, torch.float32, (E,)),
-                        ("topk_ids", topk_ids, torch.int32, (T, k)), ("topk_w", topk_w, torch.float32, (T, k))))
+    at = _args(stream, dev, (("logits", logits, torch.float32, (T, E)), ("bias", bias, torch.float32, (E,)),
+                             ("topk_ids", topk_ids, torch.int32, (T, k)), ("topk_w", topk_w, torch.float32, (T, k))))
     p = _route_params(T, E, k, n_group, topk_group, score, renormalize, scale)
     if topk_ids is None:
         topk_ids = _new((T, k), torch.int32, dev, stream)
+        at[2] = topk_ids.data_ptr()
     if topk_w is None:
         topk_w = _new((T, k), torch.float32, dev, stream)
-    _check("kmoe_route_grouped", _lib.kmoe_route_grouped(p, _at(logits), _at(bias), _at(topk_ids),
-                                                         _at(topk_w), _raw_stream(dev, stream)))
+        at[3] = topk_w.data_ptr()
+    _check("kmoe_route_grouped", _lib.kmoe_route_grouped(p, at[0], at[1], at[2], at[3], _raw_stream(dev, stream)))
     return topk_ids, topk_w
 
 
@@ -560,13 +573,14 @@ def kmoe_route_backward(d_w, logits, topk_ids, score="sigmoid", renormalize=True
     fp32 [T, E], dense, for the ids that were chosen."""
     T, E, dev = _rows_on(logits, "logits", "E")
     k = _rows(topk_ids, "topk_ids", "k")[1]
-    _args(stream, dev, (("logits", logits, torch.float32, (T, E)), ("d_w", d_w, torch.float32, (T, k)),
-                        ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_logits", d_logits, torch.float32, (T, E))))
+    at = _args(stream, dev, (("d_w", d_w, torch.float32, (T, k)), ("logits", logits, torch.float32, (T, E)),
+                             ("topk_ids", topk_ids, torch.int32, (T, k)),
+                             ("d_logits", d_logits, torch.float32, (T, E))))
     p = _route_params(T, E, k, 1, 1, score, renormalize, scale)
     if d_logits is None:
         d_logits = _new((T, E), torch.float32, dev, stream)
-    _check("kmoe_route_backward", _lib.kmoe_route_backward(p, _at(d_w), _at(logits), _at(topk_ids),
-                                                           _at(d_logits), _raw_stream(dev, stream)))
+        at[3] = d_logits.data_ptr()
+    _check("kmoe_route_backward", _lib.kmoe_route_backward(p, at[0], at[1], at[2], at[3], _raw_stream(dev, stream)))
     return d_logits
 
 
@@ -576,13 +590,13 @@ def kmoe_combine_backward(d_out, y, topk_ids, E, routed_scaling_factor=1.0, d_w=
     that a forward leaves in its workspace (stage_views(p, ws)["y"])."""
     T, H, dev = _rows_on(d_out, "d_out", "H")
     k = _rows(topk_ids, "topk_ids", "k")[1]
-    _args(stream, dev, (("d_out", d_out, torch.bfloat16, (T, H)), ("y", y, torch.float32, (T * k, H)),
-                        ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_w", d_w, torch.float32, (T, k))))
+    at = _args(stream, dev, (("d_out", d_out, torch.bfloat16, (T, H)), ("y", y, torch.float32, (T * k, H)),
+                             ("topk_ids", topk_ids, torch.int32, (T, k)), ("d_w", d_w, torch.float32, (T, k))))
     if d_w is None:
         d_w = _new((T, k), torch.float32, dev, stream)
-    _check("kmoe_combine_backward", _lib.kmoe_combine_backward(
-        _at(d_out), _at(y), _at(topk_ids), T, H, k, E, routed_scaling_factor, _at(d_w),
-        _raw_stream(dev, stream)))
+        at[3] = d_w.data_ptr()
+    _check("kmoe_combine_backward", _lib.kmoe_combine_backward(at[0], at[1], at[2], T, H, k, E, routed_scaling_factor,
+                                                               at[3], _raw_stream(dev, stream)))
     return d_w
 
 
