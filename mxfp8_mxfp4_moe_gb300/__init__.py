@@ -425,6 +425,10 @@ def _args(stream, dev, named):
 
 
 _current_stream = torch._C._cuda_getCurrentRawStream
+# scratch of one call, from the caching allocator without a tensor around it (a
+# tensor costs about 5 us beside a launch)
+_scratch_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
+_scratch_free = torch._C._cuda_cudaCachingAllocator_raw_delete
 
 
 def _raw_stream(dev, stream):
@@ -512,14 +516,11 @@ def kmoe_rmsnorm_backward(dy, h, weight, dh_in=None, eps=1e-6, dh=None, dweight=
                              ("dh_in", dh_in, st, rows), ("dh", dh, st, rows),
                              ("dweight", dweight, torch.float32, (H,))))
     n = _lib.kmoe_rmsnorm_workspace_size(T, H)
-    if workspace is None:
-        workspace = _new(n, torch.uint8, dev, stream)
-    else:
+    if workspace is not None:
         _arg(workspace, "workspace", torch.uint8, min_bytes=n)
         _gpu(workspace=workspace)
         if stream is not None:
             workspace.record_stream(stream)
-        n = workspace.numel()
     if dh is None:
         dh = _new(rows, st, dev, stream)
         at[4] = dh.data_ptr()
@@ -527,9 +528,15 @@ def kmoe_rmsnorm_backward(dy, h, weight, dh_in=None, eps=1e-6, dh=None, dweight=
         dweight = _new((H,), torch.float32, dev, stream)
         at[5] = dweight.data_ptr()
     flags = (KMOE_NORM_STREAM_F32 if st is torch.float32 else 0) | (KMOE_NORM_WEIGHT_F32 if wt is torch.float32 else 0)
-    _check("kmoe_rmsnorm_backward", _lib.kmoe_rmsnorm_backward(
-        at[0], at[1], at[2], at[3], T, H, eps, flags, at[4], at[5], workspace.data_ptr(), n,
-        _raw_stream(dev, stream)))
+    raw = _raw_stream(dev, stream)
+    # freed when the launches are queued: the memory's next user on this stream comes after them
+    scratch = _scratch_alloc(max(n, 1), raw) if workspace is None else 0
+    try:
+        _check("kmoe_rmsnorm_backward", _lib.kmoe_rmsnorm_backward(
+            at[0], at[1], at[2], at[3], T, H, eps, flags, at[4], at[5], scratch or workspace.data_ptr(), n, raw))
+    finally:
+        if scratch:
+            _scratch_free(scratch)
     return dh, dweight
 
 

@@ -310,15 +310,18 @@ __device__ __noinline__ Top2 cold_group_top2(const float* row, const float* lg, 
 // in registers and unrolled passes: 20 warps an SM, a fifth of their cycles
 // without an instruction to issue; T = 8192, E = 896, k = 16, 8 groups: 23.4
 // us against 20.9).  VEC keys are consecutive on a lane (16-byte loads).
-template <int VEC, bool BIAS>
+// WPT warps load a token's row and make its keys; the first chooses.  One, four
+// tokens a block, where tokens are many; four where they are few and a token's
+// latency counts.
+template <int VEC, bool BIAS, int WPT>
 __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(const float* __restrict__ logits,
                                                                              const float* __restrict__ bias,
                                                                              const RouteGroupArgs a, const KeyLayout kl,
                                                                              int warp_words, int32_t* __restrict__ ids,
                                                                              float* __restrict__ wts) {
   extern __shared__ uint4 s_all[];  // per warp: candidate keys [64] and experts [64], all keys
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * (blockDim.x >> 5) + warp;
+  const int warp = WPT > 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = WPT > 1 ? blockIdx.x : blockIdx.x * kRouteWarps + warp;
   if (t >= a.T) return;
   float* s_ckey = reinterpret_cast<float*>(s_all) + static_cast<size_t>(warp) * warp_words;
   int* s_ce = reinterpret_cast<int*>(s_ckey + kMaxCand);
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
   float lmax = NEG;  // of this lane's keys
   const bool denominator = a.softmax && (BIAS || !a.renormalize);
 #pragma unroll 2
-  for (int e = VEC * lane; e < a.E; e += step) {
+  for (int e = VEC * (WPT > 1 ? threadIdx.x : lane); e < a.E; e += step * WPT) {
     float v[VEC], b[VEC];
     load(lg, e, v);
     if (BIAS) load(bias, e, b);
@@ -377,8 +380,25 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
 #pragma unroll
     for (int j = 0; j < VEC; ++j) lmax = fmaxf(lmax, v[j]);
   }
+  auto lane_max = [&](auto limit) {
+    lmax = NEG;
+    for (int e = VEC * lane; e < a.E; e += step) {
+      float v[VEC];
+      const int g = kl.group(e);
+      get(e + g * kl.gap, v);
+      float m = v[0];
+#pragma unroll
+      for (int j = 1; j < VEC; ++j) m = fmaxf(m, v[j]);
+      lmax = fmaxf(lmax, fminf(m, limit(g)));
+    }
+  };
+  if constexpr (WPT > 1) {
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    if (denominator || a.n_group == 1) lane_max([&](int) { return -NEG; });
+  }
   float top = NEG, total = 1.f;
-  if (denominator) {  // what is stored are logits; a lane reads what it wrote
+  if (denominator) {  // what is stored are logits
     top = warp_max(lmax);
     total = 0.f;
     for (int e = VEC * lane; e < a.E; e += step) {
@@ -472,18 +492,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
       }
       kept = __ballot_sync(kAll, mine && better < a.topk_group);
     }
-    if (a.n_group > 1 || (BIAS && redo)) {
-      lmax = NEG;
-      for (int e = VEC * lane; e < a.E; e += step) {
-        float v[VEC];
-        const int g = kl.group(e);
-        get(e + g * kl.gap, v);
-        float m = v[0];
-#pragma unroll
-        for (int j = 1; j < VEC; ++j) m = fmaxf(m, v[j]);
-        lmax = fmaxf(lmax, fminf(m, limit(g)));
-      }
-    }
+    if (a.n_group > 1 || (BIAS && redo)) lane_max(limit);
     // ---- candidates
     s_ckey[lane] = lmax;
     __syncwarp();
@@ -609,11 +618,13 @@ cudaError_t launch_route_vec(const float* logits, const float* bias, const Route
   kl.mul = (1 << 20) / kl.per + 1;
   const int words = (kl.per + kl.gap) * a.n_group;
   const int warp_words = 2 * kMaxCand + (words + 3) / 4 * 4;
-  // few tokens: a warp a block, spread over the SMs
-  const int warps = a.T <= 152 * kRouteWarps ? 1 : kRouteWarps;
-  const size_t smem = static_cast<size_t>(warps) * warp_words * 4;
-  route_grouped_kernel<VEC, BIAS><<<(a.T + warps - 1) / warps, 32 * warps, smem, st>>>(logits, bias, a, kl, warp_words,
-                                                                                       ids, wts);
+  if (a.T <= 152 * kRouteWarps)
+    route_grouped_kernel<VEC, BIAS, kRouteWarps>
+        <<<a.T, 32 * kRouteWarps, warp_words * 4, st>>>(logits, bias, a, kl, warp_words, ids, wts);
+  else
+    route_grouped_kernel<VEC, BIAS, 1><<<(a.T + kRouteWarps - 1) / kRouteWarps, 32 * kRouteWarps,
+                                         static_cast<size_t>(kRouteWarps) * warp_words * 4, st>>>(
+        logits, bias, a, kl, warp_words, ids, wts);
   return cudaGetLastError();
 }
 
