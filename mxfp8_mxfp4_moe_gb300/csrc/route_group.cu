@@ -1,5 +1,7 @@
 // Expert routing with score functions, groups and renormalised weights, and
 // its gradient with respect to the logits (definitions in include/kmoe.h).
+#include <cuda_bf16.h>
+
 #include "route_dev.cuh"
 #include "route_group.cuh"
 
@@ -49,9 +51,9 @@ __device__ __forceinline__ Share chosen_share(float l, const RouteGroupArgs& a, 
   const bool live = l > neg_inf_f();
   float base = top;
   bool expo = a.softmax;
-  if (a.renormalize) {
+  if (a.renormalize && (a.softmax || !__any_sync(0xffffffffu, l >= -40.f))) {
     base = warp_max(l);
-    expo = expo || (base < -40.f && base > -700.f);
+    expo = expo || base > -700.f;
   }
   if (live) {
     if (expo) {
@@ -115,31 +117,45 @@ __device__ __forceinline__ int count_larger(float v, const float* s_val) {
   }
   return r;
 }
+// A lower bound of the k-th largest of the lanes' values: the k-th largest of
+// them rounded down to bf16, compared and counted two at a time (counts up to
+// 32 are exact in bf16).  -inf where fewer than k lanes have more.
+__device__ __forceinline__ float kth_largest(float v, int k, float* s_val, int lane) {
+  // down: towards zero for positive values, away from it for negative ones
+  uint32_t u = __float_as_uint(v);
+  if (v < 0.f && v > neg_inf_f()) u += 0xFFFFu;
+  const uint16_t h = static_cast<uint16_t>(u >> 16);
+  reinterpret_cast<uint16_t*>(s_val)[lane] = h;
+  __syncwarp();
+  const uint32_t twice = h | (static_cast<uint32_t>(h) << 16);
+  const __nv_bfloat162 mine = *reinterpret_cast<const __nv_bfloat162*>(&twice);
+  __nv_bfloat162 r = __float2bfloat162_rn(0.f);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 o = reinterpret_cast<const uint4*>(s_val)[q];
+    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r = __hadd2(r, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), mine));
+  }
+  __syncwarp();
+  const float larger = __low2float(r) + __high2float(r);
+  const float down = __uint_as_float(static_cast<uint32_t>(h) << 16);
+  return order_key_inverse(
+      __reduce_min_sync(0xffffffffu, larger < static_cast<float>(k) ? order_key(down) : 0xffffffffu));
+}
 // Sorts the n <= 64 candidates (key, expert) in place by (larger key, lower
 // expert): a lane ranks numbers lane and lane + 32.
-__device__ __forceinline__ void sort_candidates(float* s_ckey, int* s_ce, int n, int lane) {
-  const bool two = n > 32, h0 = lane < n, h1 = lane + 32 < n;
-  const float v0 = h0 ? s_ckey[lane] : neg_inf_f(), v1 = h1 ? s_ckey[lane + 32] : neg_inf_f();
+__device__ __noinline__ void cold_sort(float* s_ckey, int* s_ce, int n, int lane) {
+  const bool h0 = lane < n, h1 = lane + 32 < n;
+  const float v0 = h0 ? s_ckey[lane] : 0.f, v1 = h1 ? s_ckey[lane + 32] : 0.f;
   const int e0 = h0 ? s_ce[lane] : 0, e1 = h1 ? s_ce[lane + 32] : 0;
-  if (!h0) s_ckey[lane] = v0;
-  if (two && !h1) s_ckey[lane + 32] = v1;
-  __syncwarp();
-  int r0 = count_larger(v0, s_ckey), r1 = 0;
-  if (two) {
-    r0 += count_larger(v0, s_ckey + 32);
-    r1 = count_larger(v1, s_ckey) + count_larger(v1, s_ckey + 32);
-  }
-  // equal keys have equal counts: then the index decides
-  const unsigned low = (h0 && r0 < 32 ? 1u << (r0 & 31) : 0u) | (h1 && r1 < 32 ? 1u << (r1 & 31) : 0u);
-  const unsigned high = (h0 && r0 >= 32 ? 1u << (r0 & 31) : 0u) | (h1 && r1 >= 32 ? 1u << (r1 & 31) : 0u);
-  int distinct = __popc(__reduce_or_sync(0xffffffffu, low));
-  if (two) distinct += __popc(__reduce_or_sync(0xffffffffu, high));
-  if (distinct != n) {
-#pragma unroll 1
-    for (int q = 0; q < n; ++q) {
-      r0 += s_ckey[q] == v0 && s_ce[q] < e0;
-      r1 += s_ckey[q] == v1 && s_ce[q] < e1;
-    }
+  int r0 = 0, r1 = 0;
+#pragma unroll 4
+  for (int q = 0; q < n; ++q) {
+    const float o = s_ckey[q];
+    const int f = s_ce[q];
+    r0 += o > v0 || (o == v0 && f < e0);
+    r1 += o > v1 || (o == v1 && f < e1);
   }
   __syncwarp();
   if (h0) {
@@ -152,16 +168,35 @@ __device__ __forceinline__ void sort_candidates(float* s_ckey, int* s_ce, int n,
   }
   __syncwarp();
 }
+__device__ __forceinline__ void sort_candidates(float* s_ckey, int* s_ce, int n, int lane) {
+  if (n <= 32) {
+    const bool have = lane < n;
+    const float v = have ? s_ckey[lane] : neg_inf_f();
+    const int e = s_ce[lane];
+    s_ckey[lane] = v;
+    __syncwarp();
+    const int r = count_larger(v, s_ckey);
+    // equal keys have equal counts: then the index has to decide
+    if (__popc(__reduce_or_sync(0xffffffffu, have ? 1u << r : 0u)) == n) {
+      __syncwarp();
+      if (have) {
+        s_ckey[r] = v;
+        s_ce[r] = e;
+      }
+      __syncwarp();
+      return;
+    }
+  }
+  cold_sort(s_ckey, s_ce, n, lane);
+}
 
-// Keys in shared memory, group after group.  LPG lanes scan a group, VEC keys a
-// lane and step; groups start LPG * VEC banks apart (modulo 32), so that the
-// warp's scan of all groups has no bank conflicts.
+// The row's keys in shared memory, and its groups: LPG lanes scan a group, VEC
+// keys a lane and step.
 struct KeyLayout {
-  int E, per, gap;  // experts, experts a group, words between groups
-  int lpg, mul;     // lanes a group, ceil-like 2^20 / per
+  int E, per;    // experts, experts a group
+  int lpg, mul;  // lanes a group, 2^20 / per (rounded down) + 1
   // floor(e / per): mul exceeds 2^20 / per by at most 1, times e < 1024 that is below 2^20 / per
   __device__ __forceinline__ int group(int e) const { return (e * mul) >> 20; }
-  __device__ __forceinline__ int at(int e) const { return e + group(e) * gap; }
 };
 
 struct Top2 {
@@ -186,7 +221,7 @@ __device__ __forceinline__ float margin_cut(float v, float margin) {
 }
 
 // ---- rare paths, kept out of the kernel's instruction stream.  `kept` has the
-// bits of the groups that experts are chosen from, group g at bit g * lpg.
+// groups that experts are chosen from, group g at bit g * lpg.
 
 // Candidates of the largest value that kk keys reach, less the margin, written
 // to s_ckey and s_ce; returns their number, which is above 64 (and nothing
@@ -196,7 +231,7 @@ __device__ __noinline__ int cold_candidates(const float* s_key, const KeyLayout&
   const unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   auto key = [&](int e) {
-    return e < kl.E && ((kept >> (kl.group(e) * kl.lpg)) & 1u) ? s_key[kl.at(e)] : neg_inf_f();
+    return e < kl.E && ((kept >> (kl.group(e) * kl.lpg)) & 1u) ? s_key[e] : neg_inf_f();
   };
   auto count = [&](float cut) {
     unsigned c = 0;
@@ -242,7 +277,7 @@ __device__ __noinline__ int cold_argmax(float* s_key, const KeyLayout& kl, unsig
   for (int j = 0; j < kk; ++j) {
     uint32_t key = 0, low = 0;  // the lane's best: its key's image, ~expert
     for (int e = lane; e < kl.E; e += 32) {
-      const float k = (kept >> (kl.group(e) * kl.lpg)) & 1u ? s_key[kl.at(e)] : neg_inf_f();
+      const float k = (kept >> (kl.group(e) * kl.lpg)) & 1u ? s_key[e] : neg_inf_f();
       const uint32_t image = k > neg_inf_f() ? order_key(k) : 0u;
       if (image > key) {
         key = image;
@@ -252,7 +287,7 @@ __device__ __noinline__ int cold_argmax(float* s_key, const KeyLayout& kl, unsig
     const uint32_t top = __reduce_max_sync(kAll, key);
     const int e = static_cast<int>(0xffffffffu - __reduce_max_sync(kAll, key == top ? low : 0u));
     if (lane == j) best = e;
-    if ((e & 31) == lane) s_key[kl.at(e)] = neg_inf_f();
+    if ((e & 31) == lane) s_key[e] = neg_inf_f();
     __syncwarp();
   }
   return best;
@@ -279,7 +314,7 @@ __device__ __noinline__ void cold_exact_keys(float* s_key, const KeyLayout& kl, 
                               : sigmoid_exact_f32(l);
       k = fmaxf(s + bias[e], neg_inf_f());
     }
-    s_key[kl.at(e)] = k;
+    s_key[e] = k;
   }
   __syncwarp();
 }
@@ -376,26 +411,30 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = fmaxf(v[j], NEG);  // NaN to -inf
     if (BIAS && !a.softmax) sigmoid_keys(v, b);
-    put(kl.at(e), v);
+    put(e, v);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) lmax = fmaxf(lmax, v[j]);
   }
-  auto lane_max = [&](auto limit) {
+  unsigned kept = kAll;  // groups that experts are chosen from, group g at bit g * lpg
+  unsigned open = kAll;  // this lane's chunks in them, chunk q at bit q
+  auto lane_max = [&]() {
     lmax = NEG;
-    for (int e = VEC * lane; e < a.E; e += step) {
+    open = 0;
+    unsigned bit = 1;
+    for (int e = VEC * lane; e < a.E; e += step, bit <<= 1) {
       float v[VEC];
-      const int g = kl.group(e);
-      get(e + g * kl.gap, v);
-      float m = v[0];
+      get(e, v);
+      if ((kept >> (kl.group(e) * kl.lpg)) & 1u) {
+        open |= bit;
 #pragma unroll
-      for (int j = 1; j < VEC; ++j) m = fmaxf(m, v[j]);
-      lmax = fmaxf(lmax, fminf(m, limit(g)));
+        for (int j = 0; j < VEC; ++j) lmax = fmaxf(lmax, v[j]);
+      }
     }
   };
   if constexpr (WPT > 1) {
     __syncthreads();
     if (threadIdx.x >= 32) return;
-    if (denominator || a.n_group == 1) lane_max([&](int) { return -NEG; });
+    if (denominator || a.n_group == 1) lane_max();
   }
   float top = NEG, total = 1.f;
   if (denominator) {  // what is stored are logits
@@ -403,7 +442,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
     total = 0.f;
     for (int e = VEC * lane; e < a.E; e += step) {
       float v[VEC];
-      get(kl.at(e), v);
+      get(e, v);
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
         if (v[j] > NEG) total += v[j] == top ? 1.f : fast_exp(v[j] - top);
@@ -414,7 +453,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
       lmax = NEG;
       for (int e = VEC * lane; e < a.E; e += step) {
         float v[VEC], b[VEC];
-        get(kl.at(e), v);
+        get(e, v);
         load(bias, e, b);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
@@ -422,7 +461,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
           v[j] = v[j] > NEG ? fmaxf(s + b[j], NEG) : NEG;
           lmax = fmaxf(lmax, v[j]);
         }
-        put(kl.at(e), v);
+        put(e, v);
       }
     }
   }
@@ -438,14 +477,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
       margin = 0.f;
       cold_exact_keys(s_key, kl, lg, bias, a.softmax, top);
     }
-    unsigned kept = kAll;
-    // a key of the row, -inf outside the kept groups
-    auto limit = [&](int g) { return (kept >> (g * kl.lpg)) & 1u ? -NEG : NEG; };
     if (a.n_group > 1) {
       // ---- groups
       const int g = lane / kl.lpg, sub = lane - g * kl.lpg;
       const bool mine = g < a.n_group;
-      const int row = g * (kl.per + kl.gap);
+      const int row = g * kl.per;
       Top2 two{NEG, NEG};
       if (mine) {
 #pragma unroll 2
@@ -492,52 +528,43 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
       }
       kept = __ballot_sync(kAll, mine && better < a.topk_group);
     }
-    if (a.n_group > 1 || (BIAS && redo)) lane_max(limit);
+    if (a.n_group > 1 || (BIAS && redo)) lane_max();
     // ---- candidates
-    s_ckey[lane] = lmax;
-    __syncwarp();
-    const int larger = count_larger(lmax, s_ckey);
-    // the k-th largest lane maximum, which at least k keys reach, and the largest
-    float bound = order_key_inverse(__reduce_min_sync(kAll, larger < a.k ? order_key(lmax) : 0xffffffffu));
-    const float umax = __shfl_sync(kAll, lmax, __ffs(__ballot_sync(kAll, larger == 0)) - 1);
-    __syncwarp();
+    // the k-th largest lane maximum, which at least k keys reach (rounded down)
+    float bound = kth_largest(lmax, a.k, s_ckey, lane);
     if (a.k > 16) {  // half as many lanes hold two keys that reach it
       Top2 two{NEG, NEG};
-      for (int e = VEC * lane; e < a.E; e += step) {
+      unsigned left = open;
+      for (int e = VEC * lane; e < a.E; e += step, left >>= 1) {
         float v[VEC];
-        const int g = kl.group(e);
-        const float most = limit(g);
-        get(e + g * kl.gap, v);
+        get(e, v);
+        if (left & 1u) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) two.add(fminf(v[j], most));
+          for (int j = 0; j < VEC; ++j) two.add(v[j]);
+        }
       }
-      s_ckey[lane] = two.k2;
-      __syncwarp();
-      const int l2 = count_larger(two.k2, s_ckey);
-      bound = fmaxf(bound, order_key_inverse(
-                               __reduce_min_sync(kAll, l2 < (a.k + 1) / 2 ? order_key(two.k2) : 0xffffffffu)));
-      __syncwarp();
+      bound = fmaxf(bound, kth_largest(two.k2, (a.k + 1) / 2, s_ckey, lane));
     }
     kk = a.k;
     if (!(bound > NEG)) {  // fewer lanes than slots have anything to choose from
       unsigned alive = 0;
-      for (int e = lane; e < a.E; e += 32) alive += fminf(s_key[kl.at(e)], limit(kl.group(e))) > NEG;
+      for (int e = lane; e < a.E; e += 32) alive += s_key[e] > NEG && ((kept >> (kl.group(e) * kl.lpg)) & 1u);
       kk = min(a.k, static_cast<int>(__reduce_add_sync(kAll, alive)));
       if (kk == 0) break;
       bound = -3.402823466e38f;  // the lowest finite key
     }
-    if (!exact && umax > 1e30f) {  // a key of such size, or infinite, has no margin
+    if (!exact && __any_sync(kAll, lmax > 1e30f)) {  // a key of such size, or infinite, has no margin
       redo = true;
       continue;
     }
     const float cut = margin_cut(bound, margin);
     unsigned mask = 0;  // this lane's keys that reach it
+    unsigned left = open;
     int bit = 0;
-    for (int e = VEC * lane; e < a.E; e += step, bit += VEC) {
+    for (int e = VEC * lane; e < a.E; e += step, bit += VEC, left >>= 1) {
       float v[VEC];
-      const int g = kl.group(e);
-      const float least = (kept >> (g * kl.lpg)) & 1u ? cut : __int_as_float(0x7fc00000);  // NaN: no key reaches it
-      get(e + g * kl.gap, v);
+      get(e, v);
+      const float least = left & 1u ? cut : __int_as_float(0x7fc00000);  // NaN: no key reaches it
       unsigned m = 0;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) m |= v[j] >= least ? 1u << j : 0u;
@@ -556,12 +583,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
       for (; mask != 0; mask &= mask - 1, ++pos) {
         const int i = __ffs(mask) - 1;
         const int e = VEC * (lane + 32 * (i / VEC)) + i % VEC;
-        s_ckey[pos] = s_key[kl.at(e)];
+        s_ckey[pos] = s_key[e];
         s_ce[pos] = e;
       }
       __syncwarp();
     } else {
-      n = cold_candidates(s_key, kl, kept, kk, bound, umax, margin, s_ckey, s_ce);
+      n = cold_candidates(s_key, kl, kept, kk, bound, warp_max(lmax), margin, s_ckey, s_ce);
       if (n > kMaxCand) {
         if (!exact) {
           redo = true;
@@ -614,10 +641,8 @@ cudaError_t launch_route_vec(const float* logits, const float* bias, const Route
   kl.per = a.E / a.n_group;
   kl.lpg = 32;
   while (kl.lpg * a.n_group > 32) kl.lpg >>= 1;
-  kl.gap = a.n_group > 1 ? ((VEC * kl.lpg - kl.per) % 32 + 32) % 32 : 0;
   kl.mul = (1 << 20) / kl.per + 1;
-  const int words = (kl.per + kl.gap) * a.n_group;
-  const int warp_words = 2 * kMaxCand + (words + 3) / 4 * 4;
+  const int warp_words = 2 * kMaxCand + (a.E + 3) / 4 * 4;
   if (a.T <= 152 * kRouteWarps)
     route_grouped_kernel<VEC, BIAS, kRouteWarps>
         <<<a.T, 32 * kRouteWarps, warp_words * 4, st>>>(logits, bias, a, kl, warp_words, ids, wts);
