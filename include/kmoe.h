@@ -261,8 +261,8 @@ int kmoe_forward_router(const kmoe_params* p, const void* x_bf16, const void* w_
 /* ---- the operators around the experts: the norm in front of the layer,
  * routing with groups, and the gradients of what trains beside the frozen
  * MXFP4 experts (norm weight, gate weight through the logits, residual
- * stream).  Their values are checked on the host like the forward's; they need
- * no device error word. */
+ * stream).  Arguments are checked on the host like the forward's; no device
+ * error word is needed.  At most 2^30 rows (tokens, or slots T * k). */
 
 /* kmoe_rmsnorm, kmoe_rmsnorm_backward: types of the residual stream (residual,
  * h, dh_in, dh) and of the norm's weight; bf16 without the flag. */

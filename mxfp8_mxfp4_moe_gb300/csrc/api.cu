@@ -490,12 +490,14 @@ int kmoe_router(const void* x_bf16, const void* w_gate_bf16, const float* bias, 
                     reinterpret_cast<int*>(ws + 256), err, stream);
 }
 
-// Type and alignment of the norm's arguments: flags, and element alignment of
-// the stream (residual, h and their gradients) and of the weight.
+// Rows, tokens and slots of the operators around the experts: row numbers and
+// what grids add to them stay within int.
+constexpr long long kMaxRows = 1LL << 30;
+
 static int check_norm(int T, int H, float eps, uint32_t flags) {
   if (T < 0 || H <= 0 || !(eps >= 0.f) || !std::isfinite(eps)) return KMOE_ERR_ARG;
   if ((flags & ~(KMOE_NORM_STREAM_F32 | KMOE_NORM_WEIGHT_F32)) != 0u) return KMOE_ERR_ARG;
-  if (H > kMaxNormH) return KMOE_ERR_SHAPE;
+  if (H > kMaxNormH || T > kMaxRows) return KMOE_ERR_SHAPE;
   return KMOE_OK;
 }
 
@@ -516,7 +518,7 @@ int kmoe_rmsnorm(const void* x_bf16, const void* residual, const void* weight, i
 }
 
 size_t kmoe_rmsnorm_workspace_size(int T, int H) {
-  if (T < 0 || H <= 0 || H > kMaxNormH) return 0;
+  if (T < 0 || T > kMaxRows || H <= 0 || H > kMaxNormH) return 0;
   return 256 + align_up(norm_part_bytes(T, H), 256);
 }
 
@@ -544,7 +546,7 @@ static int route_args(const kmoe_route_params* p, RouteGroupArgs* a) {
   if ((p->flags & ~(KMOE_ROUTE_SOFTMAX | KMOE_ROUTE_RENORMALIZE)) != 0u || !std::isfinite(p->scale))
     return KMOE_ERR_ARG;
   if (p->E % p->n_group != 0 || p->topk_group * (p->E / p->n_group) < p->k) return KMOE_ERR_SHAPE;
-  if (static_cast<long long>(p->T) * p->k >= (1LL << 31)) return KMOE_ERR_SHAPE;
+  if (static_cast<long long>(p->T) * p->k > kMaxRows) return KMOE_ERR_SHAPE;
   *a = RouteGroupArgs{p->T, p->E, p->k, p->n_group, p->topk_group, (p->flags & KMOE_ROUTE_SOFTMAX) != 0u,
                       (p->flags & KMOE_ROUTE_RENORMALIZE) != 0u, p->scale};
   return KMOE_OK;
@@ -577,7 +579,7 @@ int kmoe_route_backward(const kmoe_route_params* p, const float* d_w, const floa
 int kmoe_combine_backward(const void* d_out_bf16, const float* y, const int32_t* topk_ids, int T, int H, int k, int E,
                           float routed_scaling_factor, float* d_w, cudaStream_t stream) {
   if (T < 0 || H <= 0 || E <= 0 || E > kMaxE || k <= 0 || k > E || k > kMaxK) return KMOE_ERR_ARG;
-  if (H % 4 != 0 || static_cast<long long>(T) * k >= (1LL << 31)) return KMOE_ERR_SHAPE;
+  if (H % 4 != 0 || static_cast<long long>(T) * k > kMaxRows) return KMOE_ERR_SHAPE;
   if (T == 0) return KMOE_OK;
   if (!d_out_bf16 || !y || !topk_ids || !d_w) return KMOE_ERR_ARG;
   if (!aligned(d_out_bf16, 8) || !aligned(y, 16) || !aligned(topk_ids, 4) || !aligned(d_w, 4)) return KMOE_ERR_ALIGN;

@@ -344,7 +344,7 @@ __device__ __noinline__ Top2 cold_group_top2(const float* row, const float* lg, 
 // more here than the loads saved by keeping them in registers (28 keys a lane
 // in registers and unrolled passes: 20 warps an SM, a fifth of their cycles
 // without an instruction to issue; T = 8192, E = 896, k = 16, 8 groups: 23.4
-// us against 20.9).  VEC keys are consecutive on a lane (16-byte loads).
+// us against 20.6).  VEC keys are consecutive on a lane (16-byte loads).
 // WPT warps load a token's row and make its keys; the first chooses.  One, four
 // tokens a block, where tokens are many; four where they are few and a token's
 // latency counts.
@@ -403,11 +403,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
   // ---- keys: cheap ones; what cannot be chosen is -inf
   float lmax = NEG;  // of this lane's keys
   const bool denominator = a.softmax && (BIAS || !a.renormalize);
+  // the whole row in flight at once, without registers; a lane reads what it copied itself
+  for (int e = VEC * (WPT > 1 ? threadIdx.x : lane); e < a.E; e += step * WPT)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(s_key + e)), "l"(lg + e), "n"(4 * VEC)
+                 : "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 2
   for (int e = VEC * (WPT > 1 ? threadIdx.x : lane); e < a.E; e += step * WPT) {
     float v[VEC], b[VEC];
-    load(lg, e, v);
     if (BIAS) load(bias, e, b);
+    get(e, v);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = fmaxf(v[j], NEG);  // NaN to -inf
     if (BIAS && !a.softmax) sigmoid_keys(v, b);

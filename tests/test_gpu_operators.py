@@ -128,6 +128,16 @@ def test_norm_at_any_alignment(K, H, off):
         check_norm_gradient(got, ref, dy, r, w, di, 1e-6)
 
 
+def test_norm_codes_at_any_alignment(K):
+    T, H = 19, 160
+    x, r, w = randn(1, T, H).to(BF), randn(2, T, H), randn(3, H)
+    h, y, codes, scales = K.kmoe_rmsnorm(at_offset(x, 1), at_offset(w, 1), residual=at_offset(r, 1), mx=True)
+    c, s = K.kmoe_quantize_mx(torch.nn.functional.pad(y, (0, 256 - H)))  # that call wants multiples of 128 columns
+    assert torch.equal(codes, c[:, :H]) and torch.equal(scales, s[:, :H // 32])
+    ref = K.kmoe_rmsnorm(x.cuda(), w.cuda(), residual=r.cuda(), mx=True)
+    assert torch.equal(h, ref[0])
+
+
 def test_norm_special_rows(K):
     """Zero rows, subnormals, infinities and NaN, each in a row of its own."""
     H = 256

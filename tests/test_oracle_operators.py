@@ -100,6 +100,7 @@ def test_norm_refusals(K):
     assert call(r=None) == 1                                    # h without a residual
     assert call(h=None, y=None, c=None, s=None) == 1            # no output
     assert call(H=48) == 2 and call(H=32800) == 2               # scale groups; more columns than a block holds
+    assert call(T=(1 << 30) + 1) == 2                           # more rows than 2^30
     assert call(c=8) == 3 and call(x=17) == 3 and call(r=18, flags=1) == 3 and call(w=18, flags=2) == 3
     assert call(T=0) == 0 and call(T=0, x=None, w=None) == 0    # an empty batch launches nothing
 
@@ -108,7 +109,7 @@ def test_norm_backward_refusals(K):
     f = K.lib().kmoe_rmsnorm_backward
     n = K.kmoe_rmsnorm_workspace_size(4, 64)
     assert n > 0 and K.kmoe_rmsnorm_workspace_size(-1, 64) == 0 and K.kmoe_rmsnorm_workspace_size(4, 0) == 0
-    assert K.kmoe_rmsnorm_workspace_size(4, 32800) == 0
+    assert K.kmoe_rmsnorm_workspace_size(4, 32800) == 0 and K.kmoe_rmsnorm_workspace_size((1 << 30) + 1, 64) == 0
     ok = dict(dy=16, h=16, w=16, di=16, T=4, H=64, eps=1e-6, flags=0, dh=16, dw=16, ws=256, n=n)
 
     def call(**kw):
@@ -135,7 +136,7 @@ def test_route_refusals(K):
         assert call(topk_group=5) == 1 and call(flags=4) == 1 and call(scale=float("nan")) == 1
         assert call(scale=float("inf")) == 1
         assert call(E=18) == 2 and call(k=9) == 2                       # unequal groups; fewer experts than slots
-        assert call(T=1 << 30) == 2                                     # slot numbers pass 31 bits
+        assert call(T=(1 << 28) + 1) == 2                               # more slots than 2^30
         assert call(a=None) == 1 and call(c=None) == 1 and call(d=None) == 1
         assert call(a=18) == 3 and call(d=18) == 3
         assert call(T=0, a=None, b=None, c=None, d=None) == 0
