@@ -227,7 +227,7 @@ cudaError_t launch_quant_scatter(const void* x, int T, int H, int k, int E, int 
 // [T, H] and scales [T, H/32] token-major.  Moves bytes only: each thread
 // loads 16 codes once and stores them to every routed row; a 128-wide K
 // block's four scale bytes are one 32-bit word in both layouts.
-__global__ void __launch_bounds__(256) mx_scatter_kernel(
+__global__ void __launch_bounds__(512) mx_scatter_kernel(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int H, int k, int E, int BN, int thr,
     const int32_t* __restrict__ ids, const int32_t* __restrict__ rank, const int32_t* __restrict__ chunk_prefix,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ seg_start, const int32_t* __restrict__ tile_start,
@@ -262,7 +262,9 @@ cudaError_t launch_mx_scatter(const uint8_t* codes, const uint8_t* scales, int T
                               const int32_t* tile_start_big, int32_t* row_of_slot, int32_t* slot_of_row, uint8_t* xq,
                               uint8_t* xsf, uint8_t* xsf_big, cudaStream_t st, bool pdl) {
   if (T == 0) return cudaSuccess;
-  return launch_chained(mx_scatter_kernel, dim3(T), dim3(256), 0, st, pdl, codes, scales, H, k, E, BN, thr, ids, rank,
+  int threads = (H / 16 + 31) / 32 * 32;  // a row in one step where it fits
+  threads = threads < 128 ? 128 : (threads > 512 ? 512 : threads);
+  return launch_chained(mx_scatter_kernel, dim3(T), dim3(threads), 0, st, pdl, codes, scales, H, k, E, BN, thr, ids, rank,
                         chunk_prefix, counts, seg_start, tile_start, tile_start_big, row_of_slot, slot_of_row, xq, xsf,
                         xsf_big);
 }
