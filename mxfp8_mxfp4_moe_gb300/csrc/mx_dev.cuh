@@ -17,15 +17,22 @@ __device__ __forceinline__ uint8_t e4m3_code(float x, float inv_scale) {
 // instructions; the same codes and scales as the fp32 forms above (a power of
 // two scales a bf16 value exactly, down to results that round to 0).
 
-// Largest magnitude as bf16 bits, NaN dropped.
-__device__ __forceinline__ uint32_t bf16_amax(const uint4& q) {
+// Largest magnitude as bf16 bits; above infinity's (0x7F80) where one of the values is NaN.
+__device__ __forceinline__ uint32_t bf16_amax_nan(const uint4& q) {
   auto b2 = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-  const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(b2(q.x)), __habs2(b2(q.y))),
-                                   __hmax2(__habs2(b2(q.z)), __habs2(b2(q.w))));
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(b2(q.x)), __habs2(b2(q.y))),
+                                       __hmax2_nan(__habs2(b2(q.z)), __habs2(b2(q.w))));
   const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
-  // a lane whose four values were all NaN is left with NaN: magnitude above infinity's bits
-  const uint32_t lo = u & 0x7FFFu, hi = (u >> 16) & 0x7FFFu;
-  return max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi);
+  return max(u & 0x7FFFu, (u >> 16) & 0x7FFFu);
+}
+// The values with +0 for NaN, which neither counts in the scale nor has another code.
+__device__ __forceinline__ uint4 bf16_drop_nan(uint4 q) {
+  auto drop = [](uint32_t w) {
+    if ((w & 0x7FFFu) > 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7FFF0000u) > 0x7F800000u) w &= 0xFFFFu;
+    return w;
+  };
+  return make_uint4(drop(q.x), drop(q.y), drop(q.z), drop(q.w));
 }
 
 // e4m3_scale_exp + 127 of a bf16 magnitude: 448 = 1.75 * 2^8, so the exponent
@@ -35,7 +42,7 @@ __device__ __forceinline__ uint32_t e4m3_scale_byte(uint32_t amax) {
   return amax == 0x7F80u ? 254u : (e > 8u ? e - 8u : 0u);
 }
 
-// The 8 codes for a scale byte, packed little-endian.
+// The 8 codes for a scale byte, packed little-endian (no NaN).
 __device__ __forceinline__ uint2 e4m3_chunk(const uint4& q, uint32_t scale) {
   // 2^(127 - scale); 2^-127 is subnormal
   const uint32_t inv = scale == 254u ? 0x0040u : (254u - scale) << 7;
@@ -50,12 +57,7 @@ __device__ __forceinline__ uint2 e4m3_chunk(const uint4& q, uint32_t scale) {
     const float2 f = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     pair[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
   }
-  uint2 out = make_uint2(pair[0] | (pair[1] << 16), pair[2] | (pair[3] << 16));
-  // NaN converts to the NaN code (0x7F, either sign); its code is +0.  No other value gives it.
-  const uint32_t n0 = __vcmpeq4(out.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n1 = __vcmpeq4(out.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  out.x &= ~n0;
-  out.y &= ~n1;
-  return out;
+  return make_uint2(pair[0] | (pair[1] << 16), pair[2] | (pair[3] << 16));
 }
 
 }  // namespace kmoe

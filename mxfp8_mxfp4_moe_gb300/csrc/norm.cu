@@ -5,6 +5,12 @@
 // rounded once to the stream's type.  The codes are those of the bf16 row y
 // (not of the fp32 product), so that a layer fed with them gives what the
 // layer fed with y gives, bit for bit.
+//
+// Measured (row layout and ring in norm_dev.cuh): T = 8192, H = 7168, bf16
+// stream, with codes: 530 MB in 85 us, 6.2 TB/s, 0.93 of the copy rate;
+// without codes 470 MB in 81 us.  HBM bounds it: a fifth fewer instructions
+// left the time as it was.  T = 1024: 16.8 us, of which about 5 are launch and
+// the first rows' latency; one row: 4.1 us, a launch.
 #include "norm_dev.cuh"
 
 namespace kmoe {
@@ -114,9 +120,15 @@ __global__ void __launch_bounds__(512, NC == 4 ? 1 : 2) rmsnorm_kernel(const Nor
       }
       if (!RAGGED && a.codes) {
         // the quad's largest magnitude; H is a multiple of 32, so whole quads are active or not
-        uint32_t amax = bf16_amax(o.q[0]);
+        uint32_t amax = bf16_amax_nan(o.q[0]);
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        if (__any_sync(0xffffffffu, amax > 0x7F80u)) {  // rare: without the NaN
+          o.q[0] = bf16_drop_nan(o.q[0]);
+          amax = bf16_amax_nan(o.q[0]);
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        }
         if (active) {
           const uint32_t scale = e4m3_scale_byte(amax);
           reinterpret_cast<uint2*>(a.codes + base)[c] = e4m3_chunk(o.q[0], scale);
