@@ -416,12 +416,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
     float v[VEC], b[VEC];
     if (BIAS) load(bias, e, b);
     get(e, v);
+    if (BIAS && !a.softmax) {
+      sigmoid_keys(v, b);
+    } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = fmaxf(v[j], NEG);  // NaN to -inf
-    if (BIAS && !a.softmax) sigmoid_keys(v, b);
+      for (int j = 0; j < VEC; ++j) v[j] = fmaxf(v[j], NEG);  // NaN to -inf
+    }
     put(e, v);
+    if (denominator || a.n_group == 1) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) lmax = fmaxf(lmax, v[j]);
+      for (int j = 0; j < VEC; ++j) lmax = fmaxf(lmax, v[j]);
+    }
   }
   unsigned kept = kAll;  // groups that experts are chosen from, group g at bit g * lpg
   unsigned open = kAll;  // this lane's chunks in them, chunk q at bit q
@@ -497,7 +502,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
           float v[VEC];
           get(row + j, v);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) two.add(v[i]);
+          for (int i = 0; i < VEC; ++i) {
+            if (BIAS)
+              two.add(v[i]);
+            else
+              two.k1 = fmaxf(two.k1, v[i]);
+          }
         }
       }
       two.merge(kl.lpg);
@@ -507,9 +517,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
         gs = BIAS && two.k2 > NEG ? two.k1 + two.k2 : two.k1;
         better = 0;
 #pragma unroll 4
-        for (int q = 0; q < a.n_group; ++q) {
-          const float o = __shfl_sync(kAll, gs, q * kl.lpg);
-          better += o > gs || (o == gs && q < g);
+        for (int q = 0; q < a.n_group; ++q) better += __shfl_sync(kAll, gs, q * kl.lpg) > gs;
+        // equal groups have equal counts: then the index decides
+        if (__popc(__reduce_or_sync(kAll, mine ? 1u << better : 0u)) != a.n_group) {
+          for (int q = 0; q < a.n_group; ++q) better += __shfl_sync(kAll, gs, q * kl.lpg) == gs && q < g;
         }
       };
       rank_groups();
