@@ -331,11 +331,12 @@ typedef struct kmoe_route_params {
  * j-th largest key.
  *   topk_w[t, j] = scale * s_j / sum_j' s_j' with KMOE_ROUTE_RENORMALIZE,
  *   scale * s_j without
- * (a few fp32 units in the last place; 0 where the sum is 0, a sigmoid below
- * e^-700 counting as 0).  An expert whose logit is -inf or NaN, or whose key
- * is, cannot be chosen (and is no part of the softmax); slots that stay empty
- * get id -1 and weight 0, which the forward skips.  A +inf logit takes the
- * softmax's whole weight.
+ * (a few fp32 units in the last place; 0 where the sum is 0).  A score below
+ * e^-700 counts as 0 there, so experts masked with a type's lowest value weigh
+ * nothing.  An expert whose logit is -inf or NaN, or whose key is, cannot be
+ * chosen (and is no part of the softmax); slots that stay empty get id -1 and
+ * weight 0, which the forward skips.  A +inf logit takes the softmax's whole
+ * weight.
  *   logits [T, E] float; bias [E] float or null; topk_ids [T, k] int32 (out),
  *   topk_w [T, k] float (out). */
 int kmoe_route_grouped(const kmoe_route_params* p, const float* logits, const float* bias, int32_t* topk_ids,
@@ -344,8 +345,10 @@ int kmoe_route_grouped(const kmoe_route_params* p, const float* logits, const fl
 /* Gradient of topk_w with respect to the logits, for the ids that were chosen
  * (the choice itself and the bias have none):
  *   d_logits[t, e] = sum_j d_w[t, j] * d topk_w[t, j] / d logit[t, e]
- * with the scores recomputed from the logits.  Slots with an id outside
- * [0, E) take no part (their d_w is not read).  Every element of d_logits is
+ * with the scores recomputed from the logits (renormalised softmax weights
+ * from the chosen logits alone; the rest of the row is looked at only where
+ * those are all below -300).  Slots with an id outside [0, E) take no part
+ * (their d_w is not used).  Every element of d_logits is
  * written; n_group and topk_group are checked but play no part.
  *   d_w [T, k] float, logits [T, E] float, topk_ids [T, k] int32, d_logits
  *   [T, E] float (out). */

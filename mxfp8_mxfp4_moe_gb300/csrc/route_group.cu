@@ -40,20 +40,26 @@ struct Share {
   float slope;  // d log(score) / d logit without the softmax's common term: 1, or 1 - sigmoid
 };
 
-// total: the softmax's denominator relative to exp(top), used without
-// renormalisation only.  Shares do not change with a common factor of the
-// scores, so softmax shares are taken relative to the largest chosen logit and
-// sigmoid shares below -40 (where the sigmoid is its exponential to within
-// e^-40) likewise: they stay right where the scores themselves underflow.  A
-// row masked with the type's lowest values (below -700) has scores of 0.
+// top, total: the softmax's largest logit (-inf: not known, nor needed) and its
+// denominator relative to exp(top), the latter used without renormalisation
+// only.  Shares do not change with a common factor of the scores, so softmax
+// shares are taken relative to the largest chosen logit, and sigmoid shares
+// below -17 (where the sigmoid is its exponential to within e^-17, less than a
+// rounding) likewise: they stay right where the scores themselves underflow.
+// Scores below e^-700 are 0: experts masked with the type's lowest value weigh
+// nothing, not even among themselves.
 __device__ __forceinline__ Share chosen_share(float l, const RouteGroupArgs& a, float top, float total) {
+  constexpr float kLeast = 700.f;
   Share r{0.f, 1.f};
-  const bool live = l > neg_inf_f();
+  bool live = l > neg_inf_f();
   float base = top;
   bool expo = a.softmax;
-  if (a.renormalize && (a.softmax || !__any_sync(0xffffffffu, l >= -40.f))) {
-    base = warp_max(l);
-    expo = expo || base > -700.f;
+  if (a.renormalize) {
+    live = live && l >= (a.softmax ? top - kLeast : -kLeast);
+    if (a.softmax || !__any_sync(0xffffffffu, l >= -17.f)) {
+      base = warp_max(live ? l : neg_inf_f());
+      expo = true;
+    }
   }
   if (live) {
     if (expo) {
@@ -88,8 +94,9 @@ __device__ __forceinline__ Share chosen_share(float l, const RouteGroupArgs& a, 
 //      22 for k = 16.  More than 64 (many equal keys, mostly): the bound is
 //      raised by bisection over the keys' integer images.
 //   3. the candidates are sorted by (key, lower index).  Neighbours in the
-//      chosen order, or at its end, closer than the margin: the candidates get
-//      exact keys, one or two a lane, and are sorted again.
+//      chosen order, or at its end, closer than the margin, with a different
+//      logit or bias among them: the candidates get exact keys, one or two a
+//      lane, and are sorted again.
 //   4. softmax scores in doubt, infinite keys, or still more than 64
 //      candidates: all keys exactly, and the same steps without a margin; if
 //      equal keys leave more than 64 candidates even so, k rounds of arg-max.
@@ -317,6 +324,32 @@ __device__ __noinline__ void cold_exact_keys(float* s_key, const KeyLayout& kl, 
     s_key[e] = k;
   }
   __syncwarp();
+}
+
+// Whether the order of the sorted candidates around the kk chosen is in doubt:
+// runs of neighbours closer than the margin that begin among the chosen, and
+// hold two candidates of different inputs.  Equal inputs have equal keys, so
+// among those the index has decided, however many there are; but a run of them
+// can stand between a chosen expert and another that it is too close to.
+__device__ __noinline__ bool cold_doubt(const float* s_ckey, const int* s_ce, int n, int kk, float margin,
+                                        const float* lg, const float* bias) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long near = 0, differ = 0;  // bit r: candidates r and r + 1
+  for (int h = 0; h < 64; h += 32) {
+    const int r = lane + h;
+    bool close = false, other = false;
+    if (r + 1 < n) {
+      const float k0 = s_ckey[r], k1 = s_ckey[r + 1];
+      close = !(k0 - k1 > margin * fmaxf(1.f, fmaxf(fabsf(k0), fabsf(k1))));
+      other = close && !(lg[s_ce[r]] == lg[s_ce[r + 1]] && bias[s_ce[r]] == bias[s_ce[r + 1]]);
+    }
+    near |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, close)) << h;
+    differ |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, other)) << h;
+  }
+  // pairs up to the chosen's end, and on while the run lasts
+  int last = kk - 1;
+  while (last < 63 && ((near >> last) & 1u)) ++last;
+  return (differ & ((1ull << last) - 1u)) != 0;
 }
 
 // The two largest exact keys among a lane's share of a group (keys j = sub,
@@ -623,12 +656,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(con
       if (lane < kk && lane + 1 < n) {
         const float k0 = s_ckey[lane], k1 = s_ckey[lane + 1];
         close = !(k0 - k1 > margin * fmaxf(1.f, fmaxf(fabsf(k0), fabsf(k1))));
-        if (close) {  // equal inputs have equal keys: their index decides, as it did
-          const int e = s_ce[lane], f = s_ce[lane + 1];
-          close = !(lg[e] == lg[f] && bias[e] == bias[f]);
-        }
       }
-      if (__any_sync(kAll, close)) {
+      if (__any_sync(kAll, close) && cold_doubt(s_ckey, s_ce, n, kk, margin, lg, bias)) {
         if (a.softmax) {
           redo = true;
           continue;
@@ -759,6 +788,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
       total += p_all[i];
     }
     total = warp_sum(total);
+  }
+  if (a.softmax && a.renormalize && !__any_sync(0xffffffffu, l >= -300.f)) {  // masked with low values?
+    for (int e = lane; e < a.E; e += 32) top = fmaxf(top, __ldg(lg + e));
+    top = warp_max(top);
   }
   const Share sh = chosen_share(l, a, top, total);
   const float s = sh.p;

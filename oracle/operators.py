@@ -29,16 +29,17 @@ def rmsnorm_backward(dy, h, weight, dh_in, eps):
 
 
 def scores(logits, softmax):
-    """Scores of the experts that can be chosen, float64; 0 where the logit is -inf or NaN."""
+    """Scores of the experts that can be chosen, float64; 0 where the logit is
+    -inf or NaN and where the score is below e^-700."""
     l = np.asarray(logits, np.float64)
     dead = np.isnan(l) | np.isneginf(l)
     if not softmax:
         with np.errstate(over="ignore", invalid="ignore"):
-            return np.where(dead, 0.0, 1.0 / (1.0 + np.exp(-l)))
+            return np.where(dead | (l < -700), 0.0, 1.0 / (1.0 + np.exp(-l)))
     l = np.where(dead, -np.inf, l)
     top = l.max(axis=1, keepdims=True)
     with np.errstate(invalid="ignore"):
-        e = np.where(dead, 0.0, np.where(l == top, 1.0, np.exp(l - top)))
+        e = np.where(dead | (l < top - 700), 0.0, np.where(l == top, 1.0, np.exp(l - top)))
     total = e.sum(axis=1, keepdims=True)
     return e / np.where(total > 0, total, 1.0)
 

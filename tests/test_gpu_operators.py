@@ -292,6 +292,25 @@ def test_route_near_ties(K, softmax, with_bias):
 
 
 @pytest.mark.parametrize("softmax", [False, True])
+def test_route_near_tie_behind_equal_keys(K, softmax):
+    """Many equal keys at the cut, and behind them by index one that exceeds
+    them by less than a cheap key tells."""
+    T, E = 40, 64
+    logits = torch.full((T, E), -1.0)
+    for t in range(T):
+        logits[t, (7 * t) % E] += 2.0 ** -23 * (1 + t % 3)
+    logits[:, :2] = 2.0
+    for bias in (torch.zeros(E), torch.full((E,), 0.25)):
+        for k, G, Kg in ((6, 1, 1), (20, 1, 1), (31, 8, 5)):
+            check_route(K, logits, bias, k, G, Kg, softmax, True, 1.0)
+    low = torch.full((T, E), torch.finfo(torch.float32).min)
+    low[:, 0] = 1.0
+    low[torch.arange(T), 5 + torch.arange(T) % 50] = -80.0
+    check_route(K, low, torch.zeros(E), 4, 1, 1, softmax, False, 1.0)
+    check_route(K, low, torch.zeros(E), 4, 8, 2, softmax, False, 1.0)
+
+
+@pytest.mark.parametrize("softmax", [False, True])
 @pytest.mark.parametrize("with_bias", [False, True])
 @pytest.mark.parametrize("renormalize", [False, True])
 def test_route_masked_and_non_finite(K, softmax, with_bias, renormalize):
@@ -317,6 +336,31 @@ def test_route_masked_and_non_finite(K, softmax, with_bias, renormalize):
         bias[11], bias[12], bias[13] = float("nan"), -float("inf"), -3.0
     for g, kg in ((1, 1), (G, Kg)):
         check_route(K, logits, bias, k, g, kg, softmax, renormalize, 2.5)
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_route_masked_with_the_lowest_value(K, softmax, renormalize):
+    """Experts masked with finite lows that their bias puts first: they weigh
+    nothing, alone or beside others, and have no gradient."""
+    T, E, k = 6, 48, 4
+    low = torch.finfo(torch.float32).min
+    logits, bias = 1.7 * randn(1, T, E), 0.1 * randn(2, E)
+    bias[[3, 17, 30, 41]] = 5.0
+    logits[0, [3, 17, 30, 41]] = low
+    logits[1, [3, 17]] = low
+    logits[2] = low
+    logits[3, [3, 17, 30, 41]] = torch.tensor([-690.0, -750.0, -699.0, -1e30])
+    logits[4, [3, 17, 30, 41]] = -1e4
+    ids, w = check_route(K, logits, bias, k, 1, 1, softmax, renormalize, 2.5)
+    assert (ids[0].sort().values.cpu() == torch.tensor([3, 17, 30, 41])).all() and not w[0].any()
+    d_w = randn(3, T, k)
+    got = K.kmoe_route_backward(d_w.cuda(), logits.cuda(), ids, score="softmax" if softmax else "sigmoid",
+                                renormalize=renormalize, scale=2.5)
+    n = ids.cpu().numpy()
+    ref = P.route_backward(d_w.double().numpy(), logits.numpy(), n, softmax, renormalize, 2.5)
+    check_route_gradient(got, ref, d_w.double().numpy(), logits, n, softmax, renormalize, 2.5)
+    assert not got[0, n[0]].any()
 
 
 def test_route_matches_the_layers_routing(K):
