@@ -73,7 +73,7 @@ __device__ __forceinline__ Share chosen_share(float l, const RouteGroupArgs& a, 
   if (a.renormalize) {
     const float sum = warp_sum(r.p);
     r.p = sum > 0.f ? __fdividef(r.p, sum) : 0.f;
-  } else if (a.softmax) {
+  } else if (a.softmax && live) {  // total >= exp(top - top); it is 0 where the row has no expert left
     r.p /= total;
   }
   return r;

@@ -45,8 +45,8 @@ def at_offset(t, elements):
 def within(got, ref, tol, what):
     g = f64(got)
     assert g.shape == ref.shape
-    bad = np.abs(g - ref) > tol
-    i = np.unravel_index(np.argmax(np.abs(g - ref) - tol), ref.shape) if ref.size else None
+    bad = ~(np.abs(g - ref) <= tol)  # NaN is off
+    i = np.unravel_index(np.argmax(bad), ref.shape) if ref.size else None
     assert not bad.any(), f"{what}: {bad.sum()} of {ref.size} off, at {i}: {g[i]!r} against {ref[i]!r}, {tol[i]!r} allowed"
 
 
