@@ -243,7 +243,10 @@ cudaError_t launch_stream(NormGradArgs a, float* dweight, cudaStream_t st) {
                         reinterpret_cast<uintptr_t>(a.weight);
   const NormPlan p = (all & kVec) == 0 ? plan_norm(a.T, a.H, 16 * (1 + sizeof(S)), true) : NormPlan{};
   a.stages = p.stages;
-  int parts = p.blocks;
+  const int parts = p.nc ? p.blocks : (a.T < kNormMaxParts ? a.T : kNormMaxParts);
+  // one block's partial row is the sum
+  const bool alone = parts == 1 && (reinterpret_cast<uintptr_t>(dweight) & kVec) == 0;
+  if (alone) a.part = dweight;
   cudaError_t e;
   if (p.nc == 1) {
     e = launch_nc<S, 1>(a, p, st);
@@ -255,11 +258,10 @@ cudaError_t launch_stream(NormGradArgs a, float* dweight, cudaStream_t st) {
     static int ready[kMaxDevices] = {};
     e = allow_smem(rmsnorm_backward_elems_kernel<S>, ready);
     if (e != cudaSuccess) return e;
-    parts = a.T < kNormMaxParts ? a.T : kNormMaxParts;
     rmsnorm_backward_elems_kernel<S><<<parts, 256, static_cast<size_t>(a.H) * 4, st>>>(a);
     e = cudaGetLastError();
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || alone) return e;
   return launch_chained(rmsnorm_dweight_kernel, dim3((a.H + 31) / 32), dim3(512), 0, st, true,
                         static_cast<const float*>(a.part), parts, a.H, dweight);
 }
