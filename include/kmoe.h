@@ -283,7 +283,8 @@ int kmoe_forward_router(const kmoe_params* p, const void* x_bf16, const void* w_
  *   scales [T, H/32] uint8 (out, both or neither, H a multiple of 32).  At
  *   least one output; no other outputs overlap an input.  H <= 32768, any
  *   H >= 1 without codes.  codes 16-byte aligned, everything else aligned to
- *   its elements (rows that are 16-byte aligned throughout run faster).
+ *   its elements (tensors that start on 16-byte boundaries and rows of at
+ *   most 16384 columns run faster).
  *   eps finite and >= 0. */
 int kmoe_rmsnorm(const void* x_bf16, const void* residual, const void* weight, int T, int H, float eps, uint32_t flags,
                  void* h, void* y_bf16, uint8_t* codes, uint8_t* scales, cudaStream_t stream);

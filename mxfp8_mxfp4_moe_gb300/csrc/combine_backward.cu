@@ -8,15 +8,13 @@
 // 7168, k = 16 reads 3.76 GB in 522 us, 7.4 TB/s (reads alone go faster than
 // the copy that the peak is taken from).  A slot is one warp's dot product,
 // eight 16-byte loads of y in flight a lane (4-byte loads: 594 us), or, where
-// there are too few slots to fill the SMs that way, four warps' (T = 129, H =
-// 3584, k = 8: 1032 slots on 152 SMs, 6.1 us a call against 8.2).
+// there are too few slots for their length to fill the SMs that way, four
+// warps' (launch_combine_backward).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
 
 namespace kmoe {
-
-constexpr int kSlotsForOneWarp = 152 * 16;  // below: four warps a slot
 
 template <int WPS>  // warps a slot
 __global__ void __launch_bounds__(256) combine_backward_kernel(const __nv_bfloat16* __restrict__ d_out,
@@ -61,7 +59,9 @@ cudaError_t launch_combine_backward(const void* d_out, const float* y, const int
                                     float rsf, float* d_w, cudaStream_t st) {
   const int R = T * k;
   const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(d_out);
-  if (R < kSlotsForOneWarp)
+  // us with four warps a slot / one: H = 7168, R = 16 slots 5.2 / 8.2, 1216 10.1 / 17.9, 4864 24.7 / 26.1,
+  // 9728 45.0 / 44.5; H = 1024, R = 1216 4.2 / 4.1, 4864 8.2 / 7.5, 9728 12.4 / 10.0
+  if (static_cast<long long>(R) * 2048 < 152LL * 16 * H)
     combine_backward_kernel<4><<<(R + 1) / 2, 256, 0, st>>>(g, y, ids, R, H, k, E, rsf, d_w);
   else
     combine_backward_kernel<1><<<(R + 7) / 8, 256, 0, st>>>(g, y, ids, R, H, k, E, rsf, d_w);

@@ -382,8 +382,8 @@ __device__ __noinline__ Top2 cold_group_top2(const float* row, const float* lg, 
 // special-function operations each); the logits' 29 MB are 4.4 us at the copy
 // rate.  VEC keys are consecutive on a lane (16-byte loads).
 // WPT warps load a token's row and make its keys; the first chooses.  One, four
-// tokens a block, where tokens are many; four where they are few and a token's
-// latency counts.
+// tokens a block, where tokens are many or rows short; four where a token's
+// latency counts (launch_route_vec).
 template <int VEC, bool BIAS, int WPT>
 __global__ void __launch_bounds__(32 * kRouteWarps, 10) route_grouped_kernel(const float* __restrict__ logits,
                                                                              const float* __restrict__ bias,
@@ -691,7 +691,9 @@ cudaError_t launch_route_vec(const float* logits, const float* bias, const Route
   while (kl.lpg * a.n_group > 32) kl.lpg >>= 1;
   kl.mul = (1 << 20) / kl.per + 1;
   const int warp_words = 2 * kMaxCand + (a.E + 3) / 4 * 4;
-  if (a.T <= 152 * kRouteWarps)
+  // E = 896, 8 groups, us with four warps a token / one: T = 16 6.2 / 7.2, 152 7.2 / 8.2, 1216 8.6 / 10.0,
+  // 2432 13.0 / 11.0; E = 256: T = 16 4.2 / 4.2, 608 5.6 / 4.2
+  if (a.E >= 512 && a.T <= 152 * 8)
     route_grouped_kernel<VEC, BIAS, kRouteWarps>
         <<<a.T, 32 * kRouteWarps, warp_words * 4, st>>>(logits, bias, a, kl, warp_words, ids, wts);
   else

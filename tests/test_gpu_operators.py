@@ -400,6 +400,26 @@ def test_route_gradient(K, T, E, k, softmax, renormalize, scale):
     check_route_gradient(got, ref, d, logits, ids, softmax, renormalize, scale)
 
 
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_route_gradient_against_differences(K, softmax, renormalize):
+    """The gradient along a direction against differences of the routing's own
+    weights.  A step of 2^-7 either way: the weights' roundings (40 units each)
+    over it, and the third derivative's share, at most 10 of the weight."""
+    T, E, k, step = 200, 96, 6, 2.0 ** -7
+    logits, d_w = (1.7 * randn(1, T, E)).cuda(), randn(2, T, k).cuda()
+    kw = dict(score="softmax" if softmax else "sigmoid", renormalize=renormalize, scale=2.5)
+    ids, w = K.kmoe_route_grouped(logits, None, k, **kw)
+    along = torch.where(torch.rand(T, E, generator=torch.Generator().manual_seed(3)) < 0.5, -1.0, 1.0).cuda()
+    hi, lo = (K.kmoe_route_grouped(logits + s * along, None, k, **kw) for s in (step, -step))
+    same = (hi[0] == ids).all(1) & (lo[0] == ids).all(1)
+    assert same.sum() > T // 4
+    num = ((hi[1] - lo[1]).double() * d_w.double()).sum(1) / (2 * step)
+    got = (K.kmoe_route_backward(d_w, logits, ids, **kw).double() * along.double()).sum(1)
+    bound = (40 * U32 / step + 10 * step ** 2) * (d_w.double() * w.double()).abs().sum(1)
+    assert torch.all(((num - got).abs() <= bound)[same])
+
+
 def check_route_gradient(got, ref, d, logits, ids, softmax, renormalize, scale):
     """An element is its score (or share) times a difference of two terms:
     fp32 chains of k + 40 operations over their absolute values (E more in the
