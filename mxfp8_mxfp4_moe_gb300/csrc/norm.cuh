@@ -29,7 +29,10 @@ struct NormPlan {
 // H = 7168 with codes 85.5 / 97.0, H = 4096 86 / 98, H = 2048 (2 / 4 blocks)
 // 83 / 99; the gradient, 1024 chunks an SM: H = 7168 75.9 / 78.4, H = 3584
 // 90 / 77.8.  Ragged rows do more for each byte and want twice as many: H =
-// 7001, T = 4096, forward 45.5 / 42.7, gradient 59.6 / 51.6.
+// 7001, T = 4096, forward 45.5 / 42.7, gradient 59.6 / 51.6.  So do batches of
+// a bf16 stream whose outputs mostly stay in L2, up to 2^24 elements: H = 7168,
+// forward with codes, T = 512 10.3 / 9.0, 2048 26.8 / 24.9, 4096 44.0 / 49.0;
+// H = 4096, T = 2048 18.1 / 16.6 (an fp32 stream: H = 5000, T = 1024 16.8 / 18.7).
 __host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, bool backward) {
   NormPlan p{};
   const bool ragged = H % 8 != 0;
@@ -47,6 +50,8 @@ __host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, bool backward)
     if (p.threads > 512) return NormPlan{};
     per_sm = (backward ? 1024 / (p.threads * p.nc) : 512 / p.threads) * (ragged ? 2 : 1);
     if (per_sm < 1) per_sm = 1;
+    const bool bf16_forward = !backward && chunk_bytes == 32;
+    if (bf16_forward && !ragged && static_cast<long long>(T) * H <= (1 << 24)) per_sm *= 2;
   }
   if (backward && per_sm > 2) per_sm = 2;  // kNormMaxParts
   const size_t stage = static_cast<size_t>(p.threads) * p.nc * chunk_bytes;
