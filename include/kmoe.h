@@ -346,11 +346,10 @@ int kmoe_route_grouped(const kmoe_route_params* p, const float* logits, const fl
 /* Gradient of topk_w with respect to the logits, for the ids that were chosen
  * (the choice itself and the bias have none):
  *   d_logits[t, e] = sum_j d_w[t, j] * d topk_w[t, j] / d logit[t, e]
- * with the scores recomputed from the logits (renormalised softmax weights
- * from the chosen logits alone; the rest of the row is looked at only where
- * those are all below -300).  Slots with an id outside [0, E) take no part
- * (their d_w is not used).  Every element of d_logits is
- * written; n_group and topk_group are checked but play no part.
+ * with the scores recomputed from the logits, those that weigh nothing (below
+ * e^-700) the same as in the weights, without a gradient.  Slots with an id
+ * outside [0, E) take no part (their d_w is not used).  Every element of
+ * d_logits is written; n_group and topk_group are checked but play no part.
  *   d_w [T, k] float, logits [T, E] float, topk_ids [T, k] int32, d_logits
  *   [T, E] float (out). */
 int kmoe_route_backward(const kmoe_route_params* p, const float* d_w, const float* logits, const int32_t* topk_ids,

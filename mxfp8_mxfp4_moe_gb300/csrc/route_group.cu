@@ -721,19 +721,25 @@ cudaError_t launch_route_grouped(const float* logits, const float* bias, const R
 //                 elsewhere (the softmax's common term cancels);
 //   sigmoid:      d_logit = g s (1 - s) at the chosen experts;
 //   softmax:      d_logit = p (g - sum g p) for all experts, g = 0 where not
-//                 chosen: the one form that reads the whole row (FULL).
-// Memory bounds it: E floats are written a token.  The row goes out as 16-byte
-// zeros (or softmax terms), then the chosen elements over them; a slot whose
-// expert an earlier slot has too (routing gives none) is added there.
-// T = 8192, E = 896, k = 16: 29 MB written in 9.8 us, about 4 of them launch
-// and the dependent look-up of the slots' logits (zeros stored before the
-// look-up: 11.7); FULL, 59 MB: 14.4 us.
-template <int KPL, int VEC, bool FULL>
+//                 chosen.
+// Softmax forms read the whole row: that one for its terms (kRowTerms), the
+// renormalised one for its largest logit (kRowTop), which decides what weighs
+// nothing (chosen_share) and which a bias can have kept out of the chosen.
+// Memory bounds it: E floats are written a token, and read for a softmax.  The
+// row goes out as 16-byte zeros (or softmax terms), then the chosen elements
+// over them; a slot whose expert an earlier slot has too (routing gives none)
+// is added there.
+// T = 8192, E = 896, k = 16: sigmoid, 29 MB written in 10.3 us, about 4 of them
+// launch and the dependent look-up of the slots' logits (zeros stored before
+// the look-up: 2 us more); softmax, 59 MB, 14.4 us in both forms.
+enum RowUse { kNoRow, kRowTop, kRowTerms };
+template <int KPL, int VEC, RowUse ROW>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const float* __restrict__ d_w,
                                                                           const float* __restrict__ logits,
                                                                           const int32_t* __restrict__ ids,
                                                                           const RouteGroupArgs a,
                                                                           float* __restrict__ d_logits) {
+  constexpr bool FULL = ROW == kRowTerms;
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.T) return;
@@ -741,7 +747,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
   const float* lg = logits + static_cast<size_t>(t) * a.E;
   float* out = d_logits + static_cast<size_t>(t) * a.E;
   constexpr int kChunks = KPL / VEC;
-  float p_all[FULL ? KPL : 1];
+  float p_all[ROW != kNoRow ? KPL : 1];
   auto store_row = [&](float factor) {  // p_all * factor, or zeros
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
@@ -758,15 +764,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
       }
     }
   };
-  int id = lane < a.k ? ids[static_cast<size_t>(t) * a.k + lane] : -1;
-  const float given_w = lane < a.k ? d_w[static_cast<size_t>(t) * a.k + lane] : 0.f;
-  if (id < 0 || id >= a.E) id = -1;
-  const float given = id >= 0 ? __ldg(lg + id) : NEG;
-  const float l = given > NEG ? given : NEG;  // NaN too
-  const float g = l > NEG ? a.scale * given_w : 0.f;
-
-  float top = NEG, total = 1.f;
-  if constexpr (FULL) {
+  if constexpr (ROW != kNoRow) {  // in flight while the slots are looked up
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
       const int e = VEC * (lane + 32 * q);
@@ -780,9 +778,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
         p_all[q] = e < a.E ? __ldg(lg + e) : NEG;
       }
     }
+  }
+  int id = lane < a.k ? ids[static_cast<size_t>(t) * a.k + lane] : -1;
+  const float given_w = lane < a.k ? d_w[static_cast<size_t>(t) * a.k + lane] : 0.f;
+  if (id < 0 || id >= a.E) id = -1;
+  const float given = id >= 0 ? __ldg(lg + id) : NEG;
+  const float l = given > NEG ? given : NEG;  // NaN too
+  const float g = l > NEG ? a.scale * given_w : 0.f;
+
+  float top = NEG, total = 1.f;
+  if constexpr (ROW != kNoRow) {
 #pragma unroll
     for (int i = 0; i < KPL; ++i) top = fmaxf(top, p_all[i]);  // fmaxf drops NaN
     top = warp_max(top);
+  }
+  if constexpr (FULL) {
     total = 0.f;
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
@@ -790,10 +800,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
       total += p_all[i];
     }
     total = warp_sum(total);
-  }
-  if (a.softmax && a.renormalize && !__any_sync(0xffffffffu, l >= -300.f)) {  // masked with low values?
-    for (int e = lane; e < a.E; e += 32) top = fmaxf(top, __ldg(lg + e));
-    top = warp_max(top);
   }
   const Share sh = chosen_share(l, a, top, total);
   const float s = sh.p;
@@ -820,23 +826,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
 template <int VEC>
 cudaError_t launch_route_backward_vec(const float* d_w, const float* logits, const int32_t* ids,
                                       const RouteGroupArgs& a, float* d_logits, cudaStream_t st) {
-  const bool full = a.softmax && !a.renormalize;
+  const RowUse row = !a.softmax ? kNoRow : (a.renormalize ? kRowTop : kRowTerms);
   const int warps = a.T <= 152 * kRouteWarps ? 1 : kRouteWarps;
   const int blocks = (a.T + warps - 1) / warps;
   const int kpl = (a.E + 32 * VEC - 1) / (32 * VEC) * VEC;
-#define KMOE_ROUTE(N)                                                                                          \
-  if (kpl <= N) {                                                                                              \
-    if (full)                                                                                                  \
-      route_backward_kernel<N, VEC, true><<<blocks, 32 * warps, 0, st>>>(d_w, logits, ids, a, d_logits);       \
-    else                                                                                                       \
-      route_backward_kernel<N, VEC, false><<<blocks, 32 * warps, 0, st>>>(d_w, logits, ids, a, d_logits);      \
-    return cudaGetLastError();                                                                                 \
+#define KMOE_ROUTE_ROW(N, ROW) \
+  route_backward_kernel<N, VEC, ROW><<<blocks, 32 * warps, 0, st>>>(d_w, logits, ids, a, d_logits)
+#define KMOE_ROUTE(N)                   \
+  if (kpl <= N) {                       \
+    if (row == kRowTerms)               \
+      KMOE_ROUTE_ROW(N, kRowTerms);     \
+    else if (row == kRowTop)            \
+      KMOE_ROUTE_ROW(N, kRowTop);       \
+    else                                \
+      KMOE_ROUTE_ROW(N, kNoRow);        \
+    return cudaGetLastError();          \
   }
   KMOE_ROUTE(4)
   KMOE_ROUTE(8)
   KMOE_ROUTE(16)
   KMOE_ROUTE(32)
 #undef KMOE_ROUTE
+#undef KMOE_ROUTE_ROW
   return cudaErrorInvalidValue;
 }
 
