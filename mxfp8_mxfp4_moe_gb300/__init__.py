@@ -172,6 +172,19 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
+def _new(shape, dtype, dev, stream):
+    """An output or workspace of a call, from the memory of the stream that the
+    call runs on: a block of the current stream may still be in use there when
+    another stream writes it.  The current stream, where the caller goes on with
+    the outputs, holds the memory from reuse too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _rows(t, name, ncols_name):
     """(rows, cols) of a 2-D argument."""
     if t is None or t.dim() != 2:
@@ -218,9 +231,9 @@ def kmoe_route(logits, bias, k, topk_ids=None, topk_w=None, stream=None):
     _arg(topk_w, "topk_w", torch.float32, (T, k))
     _gpu(logits=logits, bias=bias, topk_ids=topk_ids, topk_w=topk_w)
     if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        topk_ids = _new((T, k), torch.int32, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        topk_w = _new((T, k), torch.float32, logits.device, stream)
     _check("kmoe_route", _lib.kmoe_route(_ptr(logits), _ptr(bias), T, E, k, _ptr(topk_ids), _ptr(topk_w),
                                          _stream(stream)))
     return topk_ids, topk_w
@@ -233,10 +246,9 @@ def kmoe_quantize_mx(x, fmt=KMOE_MXFP8_E4M3, codes=None, scales=None, stream=Non
     _arg(scales, "scales", torch.uint8, (rows, cols // 32))
     _gpu(x=x, codes=codes, scales=scales)
     if codes is None:
-        codes = torch.empty((rows, cols if fmt == KMOE_MXFP8_E4M3 else cols // 2), dtype=torch.uint8,
-                            device=x.device)
+        codes = _new((rows, cols if fmt == KMOE_MXFP8_E4M3 else cols // 2), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
+        scales = _new((rows, cols // 32), torch.uint8, x.device, stream)
     _check("kmoe_quantize_mx", _lib.kmoe_quantize_mx(_ptr(x), rows, cols, fmt, _ptr(codes), _ptr(scales),
                                                      _stream(stream)))
     return codes, scales
@@ -254,8 +266,8 @@ def kmoe_prepare_weights(p, w13, w13_sf, w2, w2_sf, stream=None):
     if (w13.numel() != p.E * 2 * p.I * p.H // 2 or w13_sf.numel() != p.E * 2 * p.I * p.H // 32 or
             w2.numel() != p.E * p.H * p.I // 2 or w2_sf.numel() != p.E * p.H * p.I // 32):
         raise ValueError("weight sizes do not match the parameters (w13 [E, 2I, H/2], w2 [E, H, I/2])")
-    a = torch.empty(kmoe_prepared_weight_bytes(p, 0), dtype=torch.uint8, device=w13.device)
-    b = torch.empty(kmoe_prepared_weight_bytes(p, 1), dtype=torch.uint8, device=w13.device)
+    a = _new(kmoe_prepared_weight_bytes(p, 0), torch.uint8, w13.device, stream)
+    b = _new(kmoe_prepared_weight_bytes(p, 1), torch.uint8, w13.device, stream)
     _check("kmoe_prepare_weights", _lib.kmoe_prepare_weights(ctypes.byref(p), _ptr(w13), _ptr(w13_sf), _ptr(w2),
                                                              _ptr(w2_sf), _ptr(a), _ptr(b), _stream(stream)))
     return a, b
@@ -283,9 +295,9 @@ def kmoe_forward(p, x, logits, bias, w13_k, w2_k, topk_ids=None, topk_w=None, ou
     _gpu(x=x, logits=logits, bias=bias, w13_k=w13_k, w2_k=w2_k, topk_ids=topk_ids, topk_w=topk_w, out=out,
          workspace=workspace)
     if out is None:
-        out = torch.empty((p.T, p.H), dtype=torch.bfloat16, device=x.device)
+        out = _new((p.T, p.H), torch.bfloat16, x.device, stream)
     if workspace is None:
-        workspace = torch.empty(kmoe_workspace_size(p), dtype=torch.uint8, device=x.device)
+        workspace = _new(kmoe_workspace_size(p), torch.uint8, x.device, stream)
     args = (ctypes.byref(p), _ptr(x), _ptr(logits), _ptr(bias), _ptr(w13_k), _ptr(w2_k), _ptr(topk_ids),
             _ptr(topk_w), _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream))
     if stage_events is None:
@@ -316,13 +328,13 @@ def kmoe_router(x, w_gate, bias, k, logits=None, topk_ids=None, topk_w=None, wor
     _gpu(x=x, w_gate=w_gate, bias=bias, logits=logits, topk_ids=topk_ids, topk_w=topk_w, workspace=workspace)
     dev = x.device
     if logits is None:
-        logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        logits = _new((T, E), torch.float32, dev, stream)
     if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_ids = _new((T, k), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        topk_w = _new((T, k), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(kmoe_router_workspace_size(T, H, E), dtype=torch.uint8, device=dev)
+        workspace = _new(kmoe_router_workspace_size(T, H, E), torch.uint8, dev, stream)
     _check("kmoe_router", _lib.kmoe_router(_ptr(x), _ptr(w_gate), _ptr(bias), T, H, E, k, _ptr(logits),
                                            _ptr(topk_ids), _ptr(topk_w), _ptr(workspace), _nbytes(workspace),
                                            _stream(stream)))
@@ -338,9 +350,9 @@ def kmoe_forward_router(p, x, w_gate, bias, w13_k, w2_k, out=None, workspace=Non
     _arg(bias, "bias", torch.float32, (p.E,))
     _gpu(x=x, w_gate=w_gate, bias=bias, w13_k=w13_k, w2_k=w2_k, out=out, workspace=workspace)
     if out is None:
-        out = torch.empty((p.T, p.H), dtype=torch.bfloat16, device=x.device)
+        out = _new((p.T, p.H), torch.bfloat16, x.device, stream)
     if workspace is None:
-        workspace = torch.empty(kmoe_workspace_size(p), dtype=torch.uint8, device=x.device)
+        workspace = _new(kmoe_workspace_size(p), torch.uint8, x.device, stream)
     ev = None if stage_events is None else kmoe_stage_events(*[e.cuda_event for e in stage_events])
     _check("kmoe_forward_router", _lib.kmoe_forward_router(
         ctypes.byref(p), _ptr(x), _ptr(w_gate), _ptr(bias), _ptr(w13_k), _ptr(w2_k), _ptr(out), _ptr(workspace),
@@ -365,7 +377,7 @@ def kmoe_forward_noalloc(p, x, logits, bias, w13_k, w2_k, topk_ids=None, topk_w=
     _gpu(x=x, logits=logits, bias=bias, w13_k=w13_k, w2_k=w2_k, topk_ids=topk_ids, topk_w=topk_w, out=out,
          device_error=device_error)
     if out is None:
-        out = torch.empty((p.T, p.H), dtype=torch.bfloat16, device=x.device)
+        out = _new((p.T, p.H), torch.bfloat16, x.device, stream)
     _check("kmoe_forward_noalloc", _lib.kmoe_forward_noalloc(
         ctypes.byref(p), _ptr(x), _ptr(logits), _ptr(bias), _ptr(w13_k), _ptr(w2_k), _ptr(topk_ids), _ptr(topk_w),
         _ptr(out), _ptr(device_error), _stream(stream)))
@@ -441,15 +453,6 @@ def _rows_on(t, name, ncols_name):
         _rows(t, name, ncols_name)
     rows, cols = t.shape
     return rows, cols, t.get_device()
-
-
-def _new(shape, dtype, dev, stream):
-    """An output or workspace of a call on `stream`: the allocator keeps its
-    memory from reuse until that stream is through with it."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 KMOE_NORM_STREAM_F32 = 1
@@ -613,7 +616,7 @@ def kmoe_selftest_activation(p, gate, up, out=None, stream=None):
     _arg(gate, "gate", torch.float32, tuple(gate.shape))
     _arg(up, "up", torch.float32, tuple(gate.shape))
     if out is None:
-        out = torch.empty_like(gate)
+        out = _new(tuple(gate.shape), torch.float32, gate.device, stream)
     _arg(out, "out", torch.float32, tuple(gate.shape))
     _gpu(gate=gate, up=up, out=out)
     _check("kmoe_selftest_activation", _lib.kmoe_selftest_activation(
