@@ -162,10 +162,16 @@ def _arg(t, name, dtype=None, shape=None, min_bytes=None):
         raise ValueError(f"{name} must be contiguous (strided input is rejected, not copied)")
 
 
-def _gpu(**tensors):
+def _gpu(on_stream=None, **tensors):
+    """Every tensor lives on the GPU.  A given stream that uses them keeps them
+    from reuse until it is through."""
     for name, t in tensors.items():
         if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
+    if on_stream is not None:
+        for t in tensors.values():
+            if t is not None:
+                t.record_stream(on_stream)
 
 
 def _nbytes(t):
@@ -229,7 +235,7 @@ def kmoe_route(logits, bias, k, topk_ids=None, topk_w=None, stream=None):
     _arg(bias, "bias", torch.float32, (E,))
     _arg(topk_ids, "topk_ids", torch.int32, (T, k))
     _arg(topk_w, "topk_w", torch.float32, (T, k))
-    _gpu(logits=logits, bias=bias, topk_ids=topk_ids, topk_w=topk_w)
+    _gpu(stream, logits=logits, bias=bias, topk_ids=topk_ids, topk_w=topk_w)
     if topk_ids is None:
         topk_ids = _new((T, k), torch.int32, logits.device, stream)
     if topk_w is None:
@@ -244,7 +250,7 @@ def kmoe_quantize_mx(x, fmt=KMOE_MXFP8_E4M3, codes=None, scales=None, stream=Non
     _arg(x, "x", torch.bfloat16)
     _arg(codes, "codes", torch.uint8, (rows, cols if fmt == KMOE_MXFP8_E4M3 else cols // 2))
     _arg(scales, "scales", torch.uint8, (rows, cols // 32))
-    _gpu(x=x, codes=codes, scales=scales)
+    _gpu(stream, x=x, codes=codes, scales=scales)
     if codes is None:
         codes = _new((rows, cols if fmt == KMOE_MXFP8_E4M3 else cols // 2), torch.uint8, x.device, stream)
     if scales is None:
@@ -262,7 +268,7 @@ def kmoe_prepare_weights(p, w13, w13_sf, w2, w2_sf, stream=None):
     """Raw checkpoint tensors -> (w13_k, w2_k) prepared weight blocks."""
     for n, t in (("w13", w13), ("w13_sf", w13_sf), ("w2", w2), ("w2_sf", w2_sf)):
         _arg(t, n, torch.uint8)
-    _gpu(w13=w13, w13_sf=w13_sf, w2=w2, w2_sf=w2_sf)
+    _gpu(stream, w13=w13, w13_sf=w13_sf, w2=w2, w2_sf=w2_sf)
     if (w13.numel() != p.E * 2 * p.I * p.H // 2 or w13_sf.numel() != p.E * 2 * p.I * p.H // 32 or
             w2.numel() != p.E * p.H * p.I // 2 or w2_sf.numel() != p.E * p.H * p.I // 32):
         raise ValueError("weight sizes do not match the parameters (w13 [E, 2I, H/2], w2 [E, H, I/2])")
@@ -292,7 +298,7 @@ def kmoe_forward(p, x, logits, bias, w13_k, w2_k, topk_ids=None, topk_w=None, ou
     else:
         _arg(topk_ids, "topk_ids", torch.int32, (p.T, p.k))
         _arg(topk_w, "topk_w", torch.float32, (p.T, p.k))
-    _gpu(x=x, logits=logits, bias=bias, w13_k=w13_k, w2_k=w2_k, topk_ids=topk_ids, topk_w=topk_w, out=out,
+    _gpu(stream, x=x, logits=logits, bias=bias, w13_k=w13_k, w2_k=w2_k, topk_ids=topk_ids, topk_w=topk_w, out=out,
          workspace=workspace)
     if out is None:
         out = _new((p.T, p.H), torch.bfloat16, x.device, stream)
@@ -325,7 +331,7 @@ def kmoe_router(x, w_gate, bias, k, logits=None, topk_ids=None, topk_w=None, wor
     _arg(topk_ids, "topk_ids", torch.int32, (T, k))
     _arg(topk_w, "topk_w", torch.float32, (T, k))
     _arg(workspace, "workspace", torch.uint8, min_bytes=kmoe_router_workspace_size(T, H, E))
-    _gpu(x=x, w_gate=w_gate, bias=bias, logits=logits, topk_ids=topk_ids, topk_w=topk_w, workspace=workspace)
+    _gpu(stream, x=x, w_gate=w_gate, bias=bias, logits=logits, topk_ids=topk_ids, topk_w=topk_w, workspace=workspace)
     dev = x.device
     if logits is None:
         logits = _new((T, E), torch.float32, dev, stream)
@@ -348,7 +354,7 @@ def kmoe_forward_router(p, x, w_gate, bias, w13_k, w2_k, out=None, workspace=Non
     _layer_args(p, x, w13_k, w2_k, out, workspace)
     _arg(w_gate, "w_gate", torch.bfloat16, (p.E, p.H))
     _arg(bias, "bias", torch.float32, (p.E,))
-    _gpu(x=x, w_gate=w_gate, bias=bias, w13_k=w13_k, w2_k=w2_k, out=out, workspace=workspace)
+    _gpu(stream, x=x, w_gate=w_gate, bias=bias, w13_k=w13_k, w2_k=w2_k, out=out, workspace=workspace)
     if out is None:
         out = _new((p.T, p.H), torch.bfloat16, x.device, stream)
     if workspace is None:
@@ -374,7 +380,7 @@ def kmoe_forward_noalloc(p, x, logits, bias, w13_k, w2_k, topk_ids=None, topk_w=
         _arg(topk_ids, "topk_ids", torch.int32, (p.T, p.k))
         _arg(topk_w, "topk_w", torch.float32, (p.T, p.k))
     _arg(device_error, "device_error", min_bytes=4)
-    _gpu(x=x, logits=logits, bias=bias, w13_k=w13_k, w2_k=w2_k, topk_ids=topk_ids, topk_w=topk_w, out=out,
+    _gpu(stream, x=x, logits=logits, bias=bias, w13_k=w13_k, w2_k=w2_k, topk_ids=topk_ids, topk_w=topk_w, out=out,
          device_error=device_error)
     if out is None:
         out = _new((p.T, p.H), torch.bfloat16, x.device, stream)
@@ -395,11 +401,7 @@ def kmoe_forward_mx(p, x_codes, x_scales, topk_ids, topk_w, w13_k, w2_k, out=Non
     _arg(w13_k, "w13_k", torch.uint8, min_bytes=kmoe_prepared_weight_bytes(p, 0))
     _arg(w2_k, "w2_k", torch.uint8, min_bytes=kmoe_prepared_weight_bytes(p, 1))
     _arg(workspace, "workspace", torch.uint8, min_bytes=kmoe_workspace_size(p))
-    _gpu(w13_k=w13_k, w2_k=w2_k, workspace=workspace)
-    if stream is not None:
-        for t in (w13_k, w2_k, workspace):
-            if t is not None:
-                t.record_stream(stream)
+    _gpu(stream, w13_k=w13_k, w2_k=w2_k, workspace=workspace)
     if out is None:
         out = _new((p.T, p.H), torch.bfloat16, dev, stream)
     if workspace is None:
@@ -521,9 +523,7 @@ def kmoe_rmsnorm_backward(dy, h, weight, dh_in=None, eps=1e-6, dh=None, dweight=
     n = _lib.kmoe_rmsnorm_workspace_size(T, H)
     if workspace is not None:
         _arg(workspace, "workspace", torch.uint8, min_bytes=n)
-        _gpu(workspace=workspace)
-        if stream is not None:
-            workspace.record_stream(stream)
+        _gpu(stream, workspace=workspace)
     if dh is None:
         dh = _new(rows, st, dev, stream)
         at[4] = dh.data_ptr()
@@ -618,7 +618,7 @@ def kmoe_selftest_activation(p, gate, up, out=None, stream=None):
     if out is None:
         out = _new(tuple(gate.shape), torch.float32, gate.device, stream)
     _arg(out, "out", torch.float32, tuple(gate.shape))
-    _gpu(gate=gate, up=up, out=out)
+    _gpu(stream, gate=gate, up=up, out=out)
     _check("kmoe_selftest_activation", _lib.kmoe_selftest_activation(
         ctypes.byref(p), _ptr(gate), _ptr(up), gate.numel(), _ptr(out), _stream(stream)))
     return out
@@ -626,7 +626,7 @@ def kmoe_selftest_activation(p, gate, up, out=None, stream=None):
 
 def kmoe_device_error(workspace, stream=None):
     _arg(workspace, "workspace", min_bytes=4)
-    _gpu(workspace=workspace)
+    _gpu(stream, workspace=workspace)
     word = ctypes.c_uint32(0)
     st = _lib.kmoe_device_error(_ptr(workspace), ctypes.byref(word), _stream(stream))
     return st, word.value
@@ -639,7 +639,7 @@ def kmoe_tile_sf_offset(tile, local_row, g, tile_rows, K, max_tiles):
 def kmoe_mma_peak_run(iters, N, workspace, stream=None):
     """Launch the tensor-pipe roof kernel; returns the launch's FLOP count."""
     _arg(workspace, "workspace", min_bytes=4)
-    _gpu(workspace=workspace)
+    _gpu(stream, workspace=workspace)
     _check("kmoe_mma_peak_run", _lib.kmoe_mma_peak_run(iters, N, _ptr(workspace), _stream(stream)))
     sms = torch.cuda.get_device_properties(workspace.device).multi_processor_count
     return sms * iters * 4 * 2 * 128 * N * 32
@@ -647,7 +647,7 @@ def kmoe_mma_peak_run(iters, N, workspace, stream=None):
 
 def kmoe_selftest_wait_timeout(workspace, budget_us, stream=None):
     _arg(workspace, "workspace", min_bytes=4)
-    _gpu(workspace=workspace)
+    _gpu(stream, workspace=workspace)
     _check("kmoe_selftest_wait_timeout",
            _lib.kmoe_selftest_wait_timeout(_ptr(workspace), budget_us, _stream(stream)))
 

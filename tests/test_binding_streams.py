@@ -90,8 +90,8 @@ def gpu(monkeypatch):
         monkeypatch.setattr(torch._C, name, fn, raising=False)
     for name in ("_current_stream", "_scratch_alloc", "_scratch_free"):  # names bound when the package was imported
         if hasattr(K, name):
-            monkeypatch.setattr(K, name, {"_current_stream": lambda dev: box.stream.cuda_stream, "_scratch_alloc": alloc,
-                                          "_scratch_free": lambda at: None}[name])
+            monkeypatch.setattr(K, name, {"_current_stream": lambda dev: box.stream.cuda_stream,
+                                          "_scratch_alloc": alloc, "_scratch_free": lambda at: None}[name])
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch, "empty_like", lambda t: empty(t.shape, t.dtype, t.device))
     monkeypatch.setattr(torch.cuda, "stream", on)
@@ -168,3 +168,30 @@ def test_without_a_stream_calls_use_the_current_one(gpu, name):
     fn()
     assert gpu.made and all(t.pool is gpu.current and not t.used_by for t in gpu.made)
     assert all(handle == gpu.current.cuda_stream for _, handle in gpu.lib.launched) and gpu.lib.launched
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_are_held_for_the_stream_that_uses_them(gpu, name):
+    """The caller's tensors are kept from reuse until the given stream is through with them."""
+    given, fn = dict((c[0], c[1:]) for c in calls())[name]
+    fn(stream=gpu.side)
+    assert all(gpu.side in t.used_by for t in given.values())
+
+
+@pytest.mark.parametrize("fn", [K.kmoe_device_error, lambda ws, stream: K.kmoe_mma_peak_run(1, 64, ws, stream),
+                                lambda ws, stream: K.kmoe_selftest_wait_timeout(ws, 1, stream)])
+def test_workspaces_are_held_too(gpu, monkeypatch, fn):
+    monkeypatch.setattr(torch.cuda, "get_device_properties",
+                        lambda dev: types.SimpleNamespace(multi_processor_count=152))
+    ws = Tensor((4096,), U8)
+    fn(ws, stream=gpu.side)
+    assert gpu.side in ws.used_by
+
+
+def test_outputs_that_are_given_are_held(gpu):
+    x, w = Tensor((4, 128), BF), Tensor((128,), F32)
+    out = [Tensor((4, 128), BF), Tensor((128,), F32), Tensor((K.kmoe_rmsnorm_workspace_size(4, 128),), U8)]
+    K.kmoe_rmsnorm_backward(x, x, w, dh=out[0], dweight=out[1], workspace=out[2], stream=gpu.side)
+    q = [Tensor((4, 128), U8), Tensor((4, 4), U8)]
+    K.kmoe_quantize_mx(x, codes=q[0], scales=q[1], stream=gpu.side)
+    assert all(gpu.side in t.used_by for t in out + q)

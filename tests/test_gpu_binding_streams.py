@@ -46,3 +46,23 @@ def test_outputs_do_not_take_memory_in_use(K):  # noqa: F811
     assert all(torch.equal(a, b) for a, b in zip(ref, got))
     torch.cuda.synchronize()
     assert all(bool((t == 7).all()) for t in read)
+
+
+def test_inputs_are_kept_until_their_stream_is_through(K):  # noqa: F811
+    """The caller lets go of its inputs while the other stream has yet to read them."""
+    T, E, k, H = 256, 256, 8, 1024
+    lg, bias = randn(1, T, E).cuda(), randn(2, E).cuda()
+    x = randn(3, T, H).to(BF).cuda()
+    ref = (*K.kmoe_route(lg, bias, k), *K.kmoe_quantize_mx(x))
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        a, b, c = lg.clone(), bias.clone(), x.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = (*K.kmoe_route(a, b, k, stream=side), *K.kmoe_quantize_mx(c, stream=side))
+        del a, b, c
+        again = [torch.full_like(t, float("nan")) for t in (lg, bias, x)]  # what the allocator hands out next
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(ref, got))
+        del again
