@@ -162,12 +162,25 @@ def _arg(t, name, dtype=None, shape=None, min_bytes=None):
         raise ValueError(f"{name} must be contiguous (strided input is rejected, not copied)")
 
 
+def _current_gpu(stream):
+    """The current GPU's number.  Launches go to it, whatever the tensors, so
+    they and a given stream have to be its."""
+    dev = torch.cuda.current_device()
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the current device is cuda:{dev}")
+    return dev
+
+
 def _gpu(on_stream=None, **tensors):
-    """Every tensor lives on the GPU.  A given stream that uses them keeps them
-    from reuse until it is through."""
+    """Every tensor lives on the current GPU.  A given stream that uses them
+    keeps them from reuse until it is through."""
     for name, t in tensors.items():
         if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
+    dev = _current_gpu(on_stream)
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     if on_stream is not None:
         for t in tensors.values():
             if t is not None:
@@ -417,9 +430,9 @@ def kmoe_forward_mx(p, x_codes, x_scales, topk_ids, topk_w, w13_k, w2_k, out=Non
 
 def _args(stream, dev, named):
     """Checks (name, tensor, dtype, shape) of each argument, None passing, on
-    device ordinal `dev`, and returns their addresses.  The errors are _arg's
-    and _gpu's.  A tensor that a given stream uses is kept from reuse until
-    that stream is through."""
+    the current GPU, whose number `dev` has to be, and returns their addresses.
+    The errors are _arg's and _gpu's.  A tensor that a given stream uses is kept
+    from reuse until that stream is through."""
     at = []
     for name, t, dtype, shape in named:
         if t is None:
@@ -429,15 +442,14 @@ def _args(stream, dev, named):
         else:
             for n, u, d, s in named:
                 _arg(u, n, d, s)
-            _gpu(**{n: u for n, u, _, _ in named})
-            raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
-    if stream is not None:
-        for _, t, _, _ in named:
-            if t is not None:
-                t.record_stream(stream)
+            _gpu(stream, **{n: u for n, u, _, _ in named})
+            at.append(t.data_ptr())
+    if stream is not None or dev != _current_device():
+        _gpu(stream, **{n: u for n, u, _, _ in named})
     return at
 
 
+_current_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its 0.3 us
 _current_stream = torch._C._cuda_getCurrentRawStream
 # scratch of one call, from the caching allocator without a tensor around it (a
 # tensor costs about 5 us beside a launch)
@@ -615,10 +627,10 @@ def kmoe_selftest_activation(p, gate, up, out=None, stream=None):
     arrays of one shape), by the forward's own device functions."""
     _arg(gate, "gate", torch.float32, tuple(gate.shape))
     _arg(up, "up", torch.float32, tuple(gate.shape))
-    if out is None:
-        out = _new(tuple(gate.shape), torch.float32, gate.device, stream)
     _arg(out, "out", torch.float32, tuple(gate.shape))
     _gpu(stream, gate=gate, up=up, out=out)
+    if out is None:
+        out = _new(tuple(gate.shape), torch.float32, gate.device, stream)
     _check("kmoe_selftest_activation", _lib.kmoe_selftest_activation(
         ctypes.byref(p), _ptr(gate), _ptr(up), gate.numel(), _ptr(out), _stream(stream)))
     return out

@@ -84,14 +84,16 @@ def gpu(monkeypatch):
     def alloc(size, handle):
         box.scratch.append(handle)
         return 1 << 20
-    for name, fn in (("_cuda_getCurrentRawStream", lambda dev: box.stream.cuda_stream),
-                     ("_cuda_cudaCachingAllocator_raw_alloc", alloc),
-                     ("_cuda_cudaCachingAllocator_raw_delete", lambda at: None)):
+    driver = {"_cuda_getCurrentRawStream": lambda dev: box.stream.cuda_stream, "_cuda_getDevice": lambda: box.device,
+              "_cuda_cudaCachingAllocator_raw_alloc": alloc, "_cuda_cudaCachingAllocator_raw_delete": lambda at: None}
+    for name, fn in driver.items():
         monkeypatch.setattr(torch._C, name, fn, raising=False)
-    for name in ("_current_stream", "_scratch_alloc", "_scratch_free"):  # names bound when the package was imported
+    # what the package bound of them when it was imported
+    for name, of in (("_current_stream", "_cuda_getCurrentRawStream"), ("_current_device", "_cuda_getDevice"),
+                     ("_scratch_alloc", "_cuda_cudaCachingAllocator_raw_alloc"),
+                     ("_scratch_free", "_cuda_cudaCachingAllocator_raw_delete")):
         if hasattr(K, name):
-            monkeypatch.setattr(K, name, {"_current_stream": lambda dev: box.stream.cuda_stream,
-                                          "_scratch_alloc": alloc, "_scratch_free": lambda at: None}[name])
+            monkeypatch.setattr(K, name, driver[of])
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch, "empty_like", lambda t: empty(t.shape, t.dtype, t.device))
     monkeypatch.setattr(torch.cuda, "stream", on)
@@ -195,3 +197,39 @@ def test_outputs_that_are_given_are_held(gpu):
     q = [Tensor((4, 128), U8), Tensor((4, 4), U8)]
     K.kmoe_quantize_mx(x, codes=q[0], scales=q[1], stream=gpu.side)
     assert all(gpu.side in t.used_by for t in out + q)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_on_another_gpu_are_refused(gpu, name):
+    """Launches go to the current GPU: tensors or a stream of another are refused before anything is allocated."""
+    given, fn = dict((c[0], c[1:]) for c in calls())[name]
+    gpu.device = 1
+    with pytest.raises(ValueError, match=r"on cuda:0.*cuda:1"):
+        fn()
+    gpu.device = 0
+    for arg, t in given.items():
+        t.index, t.device = 1, torch.device("cuda", 1)
+        with pytest.raises(ValueError, match="on cuda:"):
+            fn()
+        t.index, t.device = 0, torch.device("cuda", 0)
+    gpu.side.device_index, gpu.side.device = 1, torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        fn(stream=gpu.side)
+    assert not gpu.made and not gpu.lib.launched and not gpu.scratch
+    fn()
+    assert gpu.lib.launched
+
+
+def test_outputs_and_workspaces_on_another_gpu_are_refused(gpu):
+    x, w = Tensor((4, 128), BF), Tensor((128,), F32)
+    n = K.kmoe_rmsnorm_workspace_size(4, 128)
+    far = dict(dh=Tensor((4, 128), BF, 1), dweight=Tensor((128,), F32, 1), workspace=Tensor((n,), U8, 1))
+    for arg, t in far.items():
+        with pytest.raises(ValueError, match=f"{arg} is on cuda:1"):
+            K.kmoe_rmsnorm_backward(x, x, w, **{arg: t})
+    given, fn = dict((c[0], c[1:]) for c in calls())["kmoe_forward_mx"]
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        fn(workspace=Tensor((1 << 24,), U8, 1))
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        K.kmoe_device_error(Tensor((4096,), U8, 1))
+    assert not gpu.made and not gpu.lib.launched and not gpu.scratch
