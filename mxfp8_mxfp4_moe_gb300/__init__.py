@@ -449,12 +449,13 @@ def _args(stream, dev, named):
     return at
 
 
-_current_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its 0.3 us
-_current_stream = torch._C._cuda_getCurrentRawStream
+# None in a torch without CUDA, where no call gets past its checks
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # torch.cuda.current_device without its 0.3 us
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # scratch of one call, from the caching allocator without a tensor around it (a
 # tensor costs about 5 us beside a launch)
-_scratch_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
-_scratch_free = torch._C._cuda_cudaCachingAllocator_raw_delete
+_scratch_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_scratch_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 
 
 def _raw_stream(dev, stream):
