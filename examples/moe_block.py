@@ -4,13 +4,16 @@ Serving: the residual's addition, the norm and its MXFP8 codes in one call
 (kmoe_rmsnorm), the gate's logits (kmoe_router), group-limited routing
 (kmoe_route_grouped) and the experts on the norm's codes (kmoe_forward_mx).
 
-Tuning: the experts stay frozen MXFP4 weights; the gate and the norm's weight
-learn.  The output's gradient goes to the routing weights
-(kmoe_combine_backward, from the per-slot outputs that the forward left in its
-workspace), to the logits (kmoe_route_backward), through the gate to the normed
-row and from there to the norm's weight and the stream (kmoe_rmsnorm_backward).
-The target is the output of the same block under another gate, so the loss can
-fall by routing alone.
+Tuning: the experts stay frozen MXFP4 weights; the gate learns.  The output's
+gradient goes to the routing weights (kmoe_combine_backward, from the per-slot
+outputs that the forward left in its workspace), to the logits
+(kmoe_route_backward) and to the gate.  Through the gate it also reaches the
+normed row, the norm's weight and the stream (kmoe_rmsnorm_backward), but that
+is the router's share of their gradients only: the row acts on the output
+through the experts too, and no call here gives that share (the experts'
+weights are frozen, their dependence on the row is not).  So the norm's weight
+is not stepped.  The target is the output of the same block under another gate,
+so the loss can fall by routing alone.
 
     python examples/moe_block.py            # on a GB300
 """
@@ -26,7 +29,7 @@ import workloads as W  # noqa: E402
 
 
 class Block:
-    """A block over T rows: frozen experts, a gate and a norm."""
+    """A block over T rows: a norm, a gate and frozen experts."""
 
     def __init__(self, w: W.Workload, n_group=4, topk_group=2, scale=2.5, seed=0):
         g = torch.Generator("cuda").manual_seed(seed)
@@ -48,8 +51,9 @@ class Block:
         return out, (h, y, logits, ids)
 
     def backward(self, d_out, saved):
-        """Gradients of the gate, the norm's weight and the stream (the experts'
-        own dependence on the row is frozen with them)."""
+        """The gate's gradient, and what reaches the norm's weight and the
+        stream through the router: their gradients without the experts' share.
+        The stream that goes on is h + out, so d_out is h's gradient too."""
         h, y, logits, ids = saved
         slots = K.stage_views(self.p, self.workspace)["y"]
         d_w = K.kmoe_combine_backward(d_out, slots, ids, self.w.E)
@@ -75,10 +79,9 @@ def main(steps=20, rate=0.02):
         out, saved = block.forward(x, residual)
         diff = (out.float() - target) / target.norm()
         losses.append(float(diff.square().sum()))
-        d_gate, d_norm, _ = block.backward(diff.to(torch.bfloat16), saved)
+        d_gate, _, _ = block.backward(diff.to(torch.bfloat16), saved)
         # steps of one size, whatever the gradient's
         block.gate -= rate * block.gate.norm() * d_gate / d_gate.norm()
-        block.norm -= 0.1 * rate * block.norm.norm() * d_norm / d_norm.norm()
     st, word = K.kmoe_device_error(block.workspace)
     assert st == 0, f"device error {word:#x}"
     print(f"relative squared error: {losses[0]:.4f} -> {losses[-1]:.4f} in {steps} steps")

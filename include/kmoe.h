@@ -259,10 +259,14 @@ int kmoe_forward_router(const kmoe_params* p, const void* x_bf16, const void* w_
                         cudaStream_t stream, const kmoe_stage_events* ev /* host */);
 
 /* ---- the operators around the experts: the norm in front of the layer,
- * routing with groups, and the gradients of what trains beside the frozen
- * MXFP4 experts (norm weight, gate weight through the logits, residual
- * stream).  Arguments are checked on the host like the forward's; no device
- * error word is needed.  At most 2^30 rows (tokens, or slots T * k). */
+ * routing with groups, and the gradients of the norm, of the routing weights
+ * and of the combine with respect to them, for training beside frozen MXFP4
+ * experts.  The gate's gradient is whole.  The rows that enter the layer act on
+ * its output through the gate and through the experts, and no call here gives
+ * the experts' share: a dy made from the logits' gradient alone gives
+ * kmoe_rmsnorm_backward's dweight and dh without it.  Arguments are checked on
+ * the host like the forward's; no device error word is needed.  At most 2^30
+ * rows (tokens, or slots T * k). */
 
 /* kmoe_rmsnorm, kmoe_rmsnorm_backward: types of the residual stream (residual,
  * h, dh_in, dh) and of the norm's weight; bf16 without the flag. */
