@@ -300,7 +300,8 @@ int kmoe_rmsnorm(const void* x_bf16, const void* residual, const void* weight, i
  * dh is the gradient of x and of residual alike; dh_in (null: 0) is what the
  * stored h received elsewhere (the residual connection).  The factor is
  * recomputed from the stored h.  dweight is summed in a fixed order that
- * depends only on (T, H).
+ * depends on (T, H), the stream's type and whether the tensors start on 16-byte
+ * boundaries, and on nothing else.
  *   dy [T, H] bf16; h, dh_in, dh [T, H] of the stream's type; weight [H];
  *   dh (out) may be dh_in itself; dweight [H] float (out, written even for
  *   T = 0: zeros).  H <= 32768.  workspace: kmoe_rmsnorm_workspace_size(T, H)

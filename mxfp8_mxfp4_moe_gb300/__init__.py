@@ -3,8 +3,10 @@
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 The functions carry the C entry points' names (include/kmoe.h); torch is used
-for device memory and the current stream.  Importing this package loads the
-in-tree libkmoe.so and raises if it is missing (build it with
+for device memory and the current stream.  Tensors live on the current GPU.
+With `stream` a call runs on that stream and allocates from its memory; the
+caller orders it with the streams that make and use the tensors.  Importing
+this package loads the in-tree libkmoe.so and raises if it is missing (build it with
 `python -m mxfp8_mxfp4_moe_gb300.build` or __graft_entry__.build()).
 """
 from __future__ import annotations

@@ -5,9 +5,9 @@
 //
 // The y rows are read once and nothing else comes near them in bytes (a d_out
 // row is shared by k slots and stays in L2), so HBM bounds it: T = 8192, H =
-// 7168, k = 16 reads 3.76 GB in 522 us, 7.4 TB/s (reads alone go faster than
-// the copy that the peak is taken from).  A slot is one warp's dot product,
-// eight 16-byte loads of y in flight a lane (4-byte loads: 594 us), or, where
+// 7168, k = 16 reads 3.88 GB, 3.76 of them y, in 528 us, 7.3 TB/s (reads alone
+// go faster than the copy that the peak is taken from).  A slot is one warp's
+// dot product, eight 16-byte loads of y in flight a lane (4-byte loads: 594 us), or, where
 // there are too few slots for their length to fill the SMs that way, four
 // warps' (launch_combine_backward).
 #include <cuda_bf16.h>

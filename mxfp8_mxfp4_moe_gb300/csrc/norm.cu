@@ -6,11 +6,12 @@
 // (not of the fp32 product), so that a layer fed with them gives what the
 // layer fed with y gives, bit for bit.
 //
-// Measured (row layout and ring in norm_dev.cuh): T = 8192, H = 7168, bf16
-// stream, with codes: 530 MB in 85 us, 6.2 TB/s, 0.93 of the copy rate;
-// without codes 470 MB in 81 us.  HBM bounds it: a fifth fewer instructions
-// left the time as it was.  T = 1024: 16.8 us, of which about 5 are launch and
-// the first rows' latency; one row: 4.1 us, a launch.
+// Measured (row layout and ring in norm_dev.cuh; GPU time, inputs from HBM): T =
+// 8192, H = 7168, bf16 stream, with codes: 530 MB in 87 us, 6.1 TB/s, 0.91 of
+// the copy rate; without codes 470 MB in 84 us.  HBM bounds it: a fifth fewer
+// instructions left the time as it was.  An fp32 stream, with codes: 763 MB in
+// 141 us, 5.4 TB/s, 0.81.  T = 1024, bf16: 16.5 us, of which about 5 are launch
+// and the first rows' latency; one row: 4.1 us, a launch.
 #include "norm_dev.cuh"
 
 namespace kmoe {

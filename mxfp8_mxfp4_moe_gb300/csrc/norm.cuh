@@ -7,9 +7,11 @@ namespace kmoe {
 constexpr int kMaxNormH = 32768;       // columns of the element-wise path (a row of fp32 in shared memory)
 constexpr int kNormSmem = 224 * 1024;  // shared memory that a block may ask for
 constexpr int kNormSMs = 152;          // SMs the grids are laid out for
+constexpr int kMaxStages = 4;          // of a row kernel's ring (cp_async_wait knows so many)
 
-// Partial rows of the weight gradient: at most two blocks an SM.  A function
-// of the shape alone, so that the summation order is the same on every GPU.
+// Partial rows of the weight gradient: at most two blocks an SM.  Their number
+// and so the summation order follow from the shape, the stream's type and
+// whether the tensors take the row kernels, not from the GPU.
 constexpr int kNormMaxParts = 2 * kNormSMs;
 __host__ inline size_t norm_part_bytes(int T, int H) {
   return static_cast<size_t>(T < kNormMaxParts ? T : kNormMaxParts) * H * 4;
@@ -31,8 +33,9 @@ struct NormPlan {
 // 90 / 77.8.  Ragged rows do more for each byte and want twice as many: H =
 // 7001, T = 4096, forward 45.5 / 42.7, gradient 59.6 / 51.6.  So do batches of
 // a bf16 stream whose outputs mostly stay in L2, up to 2^24 elements: H = 7168,
-// forward with codes, T = 512 10.3 / 9.0, 2048 26.8 / 24.9, 4096 44.0 / 49.0;
-// H = 4096, T = 2048 18.1 / 16.6 (an fp32 stream: H = 5000, T = 1024 16.8 / 18.7).
+// forward with codes, T = 256 8.2 / 7.8, 512 12.3 / 10.3, 1024 16.5 / 16.5, 2048
+// 26.6 / 24.7, 4096 44.0 / 49.0; H = 4096, T = 2048 17.7 / 16.4 (an fp32 stream:
+// H = 5000, T = 1024 16.8 / 18.7).
 __host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, bool backward) {
   NormPlan p{};
   const bool ragged = H % 8 != 0;
@@ -63,7 +66,7 @@ __host__ inline NormPlan plan_norm(int T, int H, int chunk_bytes, bool backward)
   p.blocks = (want + rows - 1) / rows;
   if (ragged && rows > 1) p.blocks = (p.blocks + 7) / 8 * 8;  // most is a multiple of 8
   p.stages = static_cast<int>(kNormSmem / per_sm / stage);
-  if (p.stages > 4) p.stages = 4;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
   if (p.stages > rows) p.stages = rows;
   p.smem = stage * p.stages;
   return p;

@@ -4,9 +4,11 @@
 // its rows' share of dw in fp32 and writes one partial row; a second kernel
 // adds the partial rows in order, so dw does not depend on timing.
 //
-// Measured: T = 8192, H = 7168, bf16: 470 MB in 76 us, 6.2 TB/s, 0.93 of the
-// copy rate, the second kernel (about 4 us, most of it hidden by its early
-// launch) included; T = 333, H = 3584, fp32 stream: 12.3 us for both kernels.
+// Measured (GPU time, inputs from HBM): T = 8192, H = 7168, bf16: 470 MB in 76
+// us, 6.2 TB/s, 0.93 of the copy rate, the second kernel (about 4 us, most of
+// it hidden by its early launch) included; an fp32 stream: 822 MB in 183 us,
+// 4.5 TB/s, 0.67 (one block an SM, three rows of 72 KB in its ring).  T = 333, H
+// = 3584, fp32 stream: 12.6 us for both kernels.
 #include "norm_dev.cuh"
 
 namespace kmoe {

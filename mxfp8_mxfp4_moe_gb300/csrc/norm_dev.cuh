@@ -86,7 +86,6 @@ __device__ __forceinline__ void cp_async_wait(int left) {
   else
     asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
-constexpr int kMaxStages = 4;
 
 // One chunk of a tensor of `total` elements into its ring slot (the planes of
 // a 4-byte type are `slots` apart, so that lanes touch consecutive words).

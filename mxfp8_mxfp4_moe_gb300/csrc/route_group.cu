@@ -106,7 +106,13 @@ __device__ __forceinline__ Share chosen_share(float l, const RouteGroupArgs& a, 
 // last place, which the sigmoid damps to at most 0.62 units of 2^-23; the sum
 // and the fast reciprocal add 1.5 more, the exact key's own two roundings one:
 // 6e-7 * max(1, |key|).  Two keys: 1.2e-6; 2e-6 is used.  Softmax: the
-// denominator's fp32 sum over up to 37 steps adds up to 2.3e-6; 1e-5 is used.
+// denominator's fp32 sum over up to 37 steps adds up to 2.3e-6 of a score; 1e-5
+// is used, of 1 as for a sigmoid.  That is safe, since no score exceeds 1, and
+// wide: scores of many experts are about 1 / E, and where logits or biases
+// differ little many rows hold closer neighbours and go through step 4.  T =
+// 8192, E = 896, k = 16, 8 groups: 85 us for logits of deviation 1.7 and biases
+// of deviation 0.1, 212 with biases of 0.01, 332 with 1.0 and 0.001, 628 with
+// 0.3 and 0.001 (sigmoid with a bias 21, softmax without one 16).
 constexpr int kMaxCand = 64;  // two a lane
 constexpr float kMarginSigmoid = 2e-6f;
 constexpr float kMarginSoftmax = 1e-5f;
@@ -376,11 +382,12 @@ __device__ __noinline__ Top2 cold_group_top2(const float* row, const float* lg, 
 // registers (so that many tokens share an SM) and little code, which matter
 // more here than the loads saved by keeping them in registers (28 keys a lane
 // in registers and unrolled passes: 20 warps an SM, a fifth of their cycles
-// without an instruction to issue).  T = 8192, E = 896, k = 16, 8 groups, bias:
-// 20.6 us against 23.4; all keys in double precision: 365.  What bounds it is
-// the issue of about 1500 instructions a token, a third of them the keys (two
-// special-function operations each); the logits' 29 MB are 4.4 us at the copy
-// rate.  VEC keys are consecutive on a lane (16-byte loads).
+// without an instruction to issue, 1.14 times the time).  T = 8192, E = 896, k =
+// 16, sigmoid, bias, GPU time with the inputs in HBM: 21.3 us with 8 groups,
+// 18.5 without; all keys in double precision: 365.  What bounds it is the issue
+// of about 1500 instructions a token (two special-function operations a key);
+// the logits' 29 MB are 4.4 us at the copy rate.  VEC keys are consecutive on a
+// lane (16-byte loads).
 // WPT warps load a token's row and make its keys; the first chooses.  One, four
 // tokens a block, where tokens are many or rows short; four where a token's
 // latency counts (launch_route_vec).
