@@ -453,4 +453,6 @@ int kmoe_forward_noalloc(const kmoe_params* p, const void* x_bf16, const float* 
 #ifdef __cplusplus
 }
 #endif
+#include "kmoe_products.h" /* expert products in 8 bits with block scales, the sort by expert and back */
+
 #endif /* KMOE_H_ */

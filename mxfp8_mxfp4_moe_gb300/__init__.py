@@ -695,3 +695,6 @@ def stage_views(p, workspace):
         "y": v(L.y, R * p.H, torch.float32).view(R, p.H),
         "logits": v(L.logits, p.T * p.E, torch.float32).view(p.T, p.E),
     }
+
+
+from .products import *  # noqa: E402,F401,F403  (the expert products in 8 bits; they use what is above)

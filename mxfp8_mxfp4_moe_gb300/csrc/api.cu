@@ -6,8 +6,8 @@
 
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
+#include "api.cuh"
 #include "gemm.cuh"
 #include "norm.cuh"
 #include "route_group.cuh"
@@ -39,40 +39,6 @@ using namespace kmoe;
 
 namespace {
 
-constexpr unsigned long long kWaitBudgetNs = 2000000000ull;  // 2 s per device-side wait
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
-// 2-D tensor map over [rows, cols] elements with row stride `stride_bytes`.
-bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t cols, uint64_t rows,
-              uint64_t stride_bytes, uint32_t box_cols, uint32_t box_rows, bool swizzle128 = true) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t gdim[2] = {cols, rows};
-  cuuint64_t gstr[1] = {stride_bytes};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, dt, 2, const_cast<void*>(base), gdim, gstr, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Tensor map over the code region of prepared weights: [nblk][128 rows][128
 // E2M1 codes] (64 bytes per row, 8192 per block); a box holds `depth`
 // consecutive blocks (K blocks of one weight tile).
@@ -92,8 +58,6 @@ size_t weight_blocks(const kmoe_params* p, int which) {
   if (which == 0) return static_cast<size_t>(p->E) * (p->I / 64) * (p->H / 128);
   return static_cast<size_t>(p->E) * (p->H / 128) * (p->I / 128);
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int check_params(const kmoe_params* p) {
   if (!p) return KMOE_ERR_ARG;
@@ -115,13 +79,6 @@ int check_params(const kmoe_params* p) {
     return KMOE_ERR_SHAPE;
   if (static_cast<long long>(p->T) * p->k >= (1LL << 31)) return KMOE_ERR_SHAPE;
   return KMOE_OK;
-}
-
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
 }
 
 // Tensor maps and launch of the fused router (router.cu) over caller memory.
@@ -161,11 +118,6 @@ int check_router_args(const void* x_bf16, const void* w_gate_bf16, const float* 
   if (T > 0 && (!aligned(x_bf16, 16) || !aligned(w_gate_bf16, 16))) return KMOE_ERR_ALIGN;
   return KMOE_OK;
 }
-
-#define KMOE_CK(call)                           \
-  do {                                          \
-    if ((call) != cudaSuccess) return KMOE_ERR_CUDA; \
-  } while (0)
 
 }  // namespace
 
@@ -489,10 +441,6 @@ int kmoe_router(const void* x_bf16, const void* w_gate_bf16, const float* bias, 
   return run_router(x_bf16, w_gate_bf16, bias, T, H, E, k, logits, part, topk_ids, topk_w,
                     reinterpret_cast<int*>(ws + 256), err, stream);
 }
-
-// Rows, tokens and slots of the operators around the experts: row numbers and
-// what grids add to them stay within int.
-constexpr long long kMaxRows = 1LL << 30;
 
 static int check_norm(int T, int H, float eps, uint32_t flags) {
   if (T < 0 || H <= 0 || !(eps >= 0.f) || !std::isfinite(eps)) return KMOE_ERR_ARG;

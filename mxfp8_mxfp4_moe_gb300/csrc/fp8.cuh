@@ -1,0 +1,117 @@
+// Arguments and launchers of the products of E4M3 operands with a scale for
+// each block of 128 (fp8_gemm.cu) and of their quantisers (fp8_quant.cu).
+#pragma once
+#include "common.cuh"
+
+namespace kmoe {
+
+constexpr int kScaleBlock = 128;  // values a scale
+
+// What a product computes; all three accumulate D[feature, column] with the
+// features in the tensor core's M slot.
+enum Fp8Kind {
+  FP8_ROWS = 0,         // out[row, n] = sum_k x[row, k] w[n, k]:  features n, columns rows
+  FP8_ROWS_GRAD = 1,    // out[row, k] = sum_n x[row, n] w[n, k]:  features k, columns rows
+  FP8_WEIGHT_GRAD = 2,  // out[n, k] = sum_row dy[row, n] x[row, k]:  features k, columns n
+};
+
+struct Fp8Maps {
+  CUtensorMap a;  // features: weights in boxes of 128 x 128, or x's columns
+  CUtensorMap b;  // columns: rows in boxes of kFp8BoxRows rows, or dy's columns
+};
+
+struct Fp8Args {
+  const int32_t* seg;  // [E + 1] first row of each expert; null: one expert, all rows
+  const float* a_sf;   // weights' scales [E][.][.] (strides below); weight gradient: x's, [blocks][F]
+  const float* b_sf;   // rows' scales [KB][ldb]; weight gradient: dy's, [blocks][ldb]
+  void* out;
+  uint32_t* err;
+  unsigned long long budget_ns;
+  long long a_se;  // strides of a weight scale by expert, feature block and sum block
+  int a_sm, a_sk;
+  int E, M;        // experts, rows
+  int F, FT;       // features and tiles of 128 of them
+  int C, CT;       // weight gradient: columns and tiles of them
+  int KB;          // blocks of the sum (weight gradient: blocks there are)
+  int ldb;
+  int f32;         // out is fp32, else bf16
+};
+
+// Rows (columns of D) of a tile by the number of rows an expert has on
+// average, and rows of a TMA box of them.
+int fp8_tile_columns(int M, int E);
+constexpr int kFp8BoxRows = 32;
+
+cudaError_t launch_fp8_gemm(Fp8Kind kind, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
+
+cudaError_t launch_fp8_quant_rows(const void* x, int rows, int cols, uint8_t* codes, float* scales, cudaStream_t st);
+cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, const int32_t* row_of_slot, uint8_t* codes,
+                                     float* scales, cudaStream_t st);
+cudaError_t launch_fp8_quant_weights(const void* w, int E, int N, int K, uint8_t* codes, float* scales,
+                                     cudaStream_t st);
+cudaError_t launch_fp8_quant_cols(const void* x, int rows, int cols, const int32_t* seg, int E, uint8_t* codes,
+                                  float* scales, cudaStream_t st);
+
+// Rows that hold `rows` rows of E experts with every expert's first on a
+// multiple of 128: sum of ceil(c_e / 128) blocks over any counts c_e.
+__host__ inline long long fp8_padded_rows(long long rows, int E) {
+  const long long with = rows < E ? rows : E;  // experts that can have rows
+  return (rows + 127 * with) / 128 * 128;
+}
+
+// The first row of expert e, held inside the rows there are whatever the
+// table says.
+__device__ __forceinline__ int segment_start(const int32_t* seg, int e, int M) {
+  return seg == nullptr ? (e == 0 ? 0 : M) : min(max(__ldg(seg + e), 0), M);
+}
+
+// Shared-memory prefixes over the experts, for all threads of a block:
+// first[e] = expert e's first row (held in [0, M]), unit[e] = units before it,
+// a unit being up to `per` rows; both with E + 1 entries.  `tmp` holds 33 ints.
+__device__ __forceinline__ void segment_prefix(const int32_t* seg, int E, int M, int per, int32_t* first,
+                                               int32_t* unit, int32_t* tmp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) first[e] = segment_start(seg, e, M);
+  __syncthreads();
+  // chunks of 32 experts: prefixes inside, then over the (at most 32) chunks
+  const int chunks = (E + 31) / 32;
+  for (int c = warp; c < chunks; c += nw) {
+    const int e = c * 32 + lane;
+    const int rows = e < E ? max(first[e + 1] - first[e], 0) : 0;
+    int v = (rows + per - 1) / per;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += u;
+    }
+    if (e < E) unit[e + 1] = v;
+    if (lane == 31) tmp[c] = v;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int v = lane < chunks ? tmp[lane] : 0;
+    const int own = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += u;
+    }
+    if (lane < chunks) tmp[lane] = v - own;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) unit[e + 1] += tmp[e >> 5];
+  if (threadIdx.x == 0) unit[0] = 0;
+  __syncthreads();
+}
+
+// The expert whose units [unit[e], unit[e + 1]) hold u < unit[E].
+__device__ __forceinline__ int segment_of_unit(const int32_t* unit, int E, int u) {
+  int lo = 0, hi = E;  // the largest e with unit[e] <= u has units
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (unit[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace kmoe

@@ -1,0 +1,258 @@
+// Quantisers of the block-scaled products: bf16 to E4M3 codes with one
+// power-of-two fp32 scale for each 128 values, the rule of kmoe_quantize_mx
+// over other groups:
+//   s = 2^e, the smallest e >= -126 with amax <= 448 * 2^e;  code = e4m3(x / s)
+// (round to nearest even, saturating; NaN is left out of amax and becomes 0).
+// A power of two makes x / s exact, so codes and scales are the definition's
+// bit for bit; e4m3 keeps its relative precision under any scale.
+//
+//   fp8_quant_rows_kernel     128 columns of one row: the sum of rows x weights
+//   fp8_quant_scatter_kernel  the same, each token's row once, written to the
+//                             expert-sorted rows of its k slots
+//   fp8_quant_tile_kernel     128 rows of one column (the sum of the weights'
+//                             gradient; every expert's rows from a multiple of
+//                             128 on, zeros behind them), or 128 x 128 weights
+#include "fp8.cuh"
+#include "mx_dev.cuh"
+
+namespace kmoe {
+
+// Scale byte (e + 127 of 2^e) for the largest magnitude of a group.
+__device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax) { return max(e4m3_scale_byte(amax), 1u); }
+__device__ __forceinline__ float fp8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+__device__ __forceinline__ uint32_t bf16x2_amax(const uint4& q) {
+  auto b2 = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+  const __nv_bfloat162 m =
+      __hmax2(__hmax2(__habs2(b2(q.x)), __habs2(b2(q.y))), __hmax2(__habs2(b2(q.z)), __habs2(b2(q.w))));
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+  return max(u & 0x7FFFu, u >> 16);
+}
+
+// 16 values of one row, NaN dropped, and their largest magnitude.
+struct Vals16 {
+  uint4 a, b;
+  uint32_t amax;
+};
+__device__ __forceinline__ Vals16 load16(const __nv_bfloat16* p) {
+  Vals16 v;
+  v.a = __ldg(reinterpret_cast<const uint4*>(p));
+  v.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  v.amax = max(bf16_amax_nan(v.a), bf16_amax_nan(v.b));
+  if (v.amax > 0x7F80u) {
+    v.a = bf16_drop_nan(v.a);
+    v.b = bf16_drop_nan(v.b);
+    v.amax = max(bf16x2_amax(v.a), bf16x2_amax(v.b));
+  }
+  return v;
+}
+// The largest of a group's eight lanes.
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
+#pragma unroll
+  for (int off = 1; off < 8; off <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+
+// A warp takes 512 columns of one row (16 a lane), a block the same columns of
+// eight rows, whose scales of one group are adjacent: whole sectors.
+__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const __nv_bfloat16* __restrict__ x, int rows, int cols,
+                                                             uint8_t* __restrict__ codes,
+                                                             float* __restrict__ scales) {
+  chain_wait();
+  __shared__ float s_scale[4][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * 8 + warp;
+  const int col = blockIdx.y * 512 + lane * 16;
+  const bool in = row < rows && col < cols;
+  const long long at = static_cast<long long>(row) * cols + col;
+  Vals16 v{};
+  if (in) v = load16(x + at);
+  const uint32_t byte = fp8_scale_byte(max8(v.amax));
+  if (in) {
+    const uint2 lo = e4m3_chunk(v.a, byte), hi = e4m3_chunk(v.b, byte);
+    *reinterpret_cast<uint4*>(codes + at) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+  if ((lane & 7) == 0) s_scale[lane >> 3][warp] = fp8_scale(byte);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int g = threadIdx.x >> 3, r = blockIdx.x * 8 + (threadIdx.x & 7);
+    const int grp = blockIdx.y * 4 + g;
+    if (r < rows && grp * 128 < cols) scales[static_cast<long long>(grp) * rows + r] = s_scale[g][threadIdx.x & 7];
+  }
+}
+
+__global__ void __launch_bounds__(512) fp8_quant_scatter_kernel(const __nv_bfloat16* __restrict__ x, int cols, int k,
+                                                                long long R, const int32_t* __restrict__ row_of_slot,
+                                                                uint8_t* __restrict__ codes,
+                                                                float* __restrict__ scales) {
+  chain_wait();
+  __shared__ int s_row[kMaxK];
+  const long long t = blockIdx.x;
+  if (threadIdx.x < k) {
+    const int r = row_of_slot[t * k + threadIdx.x];
+    s_row[threadIdx.x] = r >= 0 && r < R ? r : -1;
+  }
+  __syncthreads();
+  const int step = blockDim.x * 16 * gridDim.y;
+  // whole groups of eight lanes stay in the loop together
+  for (int c0 = (blockIdx.y * blockDim.x + (threadIdx.x & ~31)) * 16; c0 < cols; c0 += step) {
+    const int col = c0 + (threadIdx.x & 31) * 16;
+    const bool in = col < cols;
+    Vals16 v{};
+    if (in) v = load16(x + t * cols + col);
+    const uint32_t byte = fp8_scale_byte(max8(v.amax));
+    if (!in) continue;
+    const uint2 lo = e4m3_chunk(v.a, byte), hi = e4m3_chunk(v.b, byte);
+    const uint4 out = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    const float scale = fp8_scale(byte);
+    for (int j = 0; j < k; ++j) {
+      const int r = s_row[j];
+      if (r < 0) continue;
+      *reinterpret_cast<uint4*>(codes + static_cast<long long>(r) * cols + col) = out;
+      if ((threadIdx.x & 7) == 0) scales[(col >> 7) * R + r] = scale;
+    }
+  }
+}
+
+// One tile of 128 rows x 128 columns a step: 16 lanes of 8 columns by 16 rows,
+// eight rows a thread.  WEIGHTS: one scale for the tile, blockIdx.x = expert
+// and row tile; else one for each column, blockIdx.x = a block of 128 rows of
+// the padded order.
+template <bool WEIGHTS>
+__global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const __nv_bfloat16* __restrict__ x, int rows, int cols,
+                                                             int E, const int32_t* __restrict__ seg,
+                                                             uint8_t* __restrict__ codes,
+                                                             float* __restrict__ scales) {
+  chain_wait();
+  __shared__ int32_t first[WEIGHTS ? 1 : kMaxE + 1], unit[WEIGHTS ? 1 : kMaxE + 1], tmp[33];
+  __shared__ uint32_t s_max[8][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cg = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  long long src, dst;  // first row of the tile in x and in codes
+  int n, nd;           // rows it has in x, and in codes
+  if constexpr (WEIGHTS) {
+    const int tiles = (rows + 127) / 128;
+    const int e = blockIdx.x / tiles, i = blockIdx.x % tiles;
+    src = dst = static_cast<long long>(e) * rows + i * 128;
+    n = nd = min(128, rows - i * 128);
+  } else {
+    segment_prefix(seg, E, rows, 128, first, unit, tmp);
+    const int b = blockIdx.x;
+    if (b >= unit[E]) return;
+    const int e = segment_of_unit(unit, E, b);
+    const int at = (b - unit[e]) * 128;
+    src = first[e] + at;
+    dst = static_cast<long long>(b) * 128;
+    n = min(128, first[e + 1] - first[e] - at);
+    nd = 128;
+  }
+  for (int c0 = blockIdx.y * 128; c0 < cols; c0 += gridDim.y * 128) {
+    const int col = c0 + cg * 8;
+    uint4 v[8];
+    uint32_t m[4] = {0, 0, 0, 0};  // largest magnitudes of the columns, two a word
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 16 * i;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r < n && col < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(x + (src + r) * cols + col));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (bf16_amax_nan(v[i]) > 0x7F80u) v[i] = bf16_drop_nan(v[i]);
+      m[0] = __vmaxu2(m[0], v[i].x & 0x7FFF7FFFu);
+      m[1] = __vmaxu2(m[1], v[i].y & 0x7FFF7FFFu);
+      m[2] = __vmaxu2(m[2], v[i].z & 0x7FFF7FFFu);
+      m[3] = __vmaxu2(m[3], v[i].w & 0x7FFF7FFFu);
+    }
+    // over the two rows of a warp, then over the warps
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = __vmaxu2(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+    __syncthreads();
+    if (lane < 16)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s_max[warp][cg * 8 + 2 * j] = m[j] & 0xFFFFu;
+        s_max[warp][cg * 8 + 2 * j + 1] = m[j] >> 16;
+      }
+    __syncthreads();
+    if (threadIdx.x < 128) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) a = max(a, s_max[w][threadIdx.x]);
+      if constexpr (WEIGHTS) a = __reduce_max_sync(0xffffffffu, a);
+      s_max[0][threadIdx.x] = a;
+    }
+    __syncthreads();
+    if constexpr (WEIGHTS) {
+      const uint32_t a = max(max(s_max[0][0], s_max[0][32]), max(s_max[0][64], s_max[0][96]));
+      const uint32_t byte = fp8_scale_byte(a);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r < nd && col < cols)
+          *reinterpret_cast<uint2*>(codes + (dst + r) * cols + col) = e4m3_chunk(v[i], byte);
+      }
+      if (threadIdx.x == 0)
+        scales[static_cast<long long>(blockIdx.x) * ((cols + 127) / 128) + c0 / 128] = fp8_scale(byte);
+    } else if (col < cols) {
+      // eight columns with scales of their own
+      uint32_t byte[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) byte[j] = fp8_scale_byte(s_max[0][cg * 8 + j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t pair[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // x / s: exact, s = 2^(byte - 127)
+          const float lo = __uint_as_float(w[j] << 16) * exp2i(127 - static_cast<int>(byte[2 * j]));
+          const float hi = __uint_as_float(w[j] & 0xFFFF0000u) * exp2i(127 - static_cast<int>(byte[2 * j + 1]));
+          pair[j] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+        }
+        *reinterpret_cast<uint2*>(codes + (dst + r0 + 16 * i) * cols + col) =
+            make_uint2(pair[0] | (pair[1] << 16), pair[2] | (pair[3] << 16));
+      }
+      if (r0 == 0) {
+        float* s = scales + static_cast<long long>(blockIdx.x) * cols + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = fp8_scale(byte[j]);
+      }
+    }
+  }
+}
+
+cudaError_t launch_fp8_quant_rows(const void* x, int rows, int cols, uint8_t* codes, float* scales, cudaStream_t st) {
+  return launch_chained(fp8_quant_rows_kernel, dim3((rows + 7) / 8, (cols + 511) / 512), dim3(256), 0, st, true,
+                        static_cast<const __nv_bfloat16*>(x), rows, cols, codes, scales);
+}
+
+cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, const int32_t* row_of_slot, uint8_t* codes,
+                                     float* scales, cudaStream_t st) {
+  const int chunks = (cols / 16 + 31) / 32;  // warps a row takes
+  // few tokens: a warp a block, so that their stores spread over the SMs
+  const int threads = T < 304 ? 32 : 32 * (chunks < 16 ? chunks : 16);
+  const int split = T < 304 ? chunks : 1;
+  return launch_chained(fp8_quant_scatter_kernel, dim3(T, split), dim3(threads), 0, st, true,
+                        static_cast<const __nv_bfloat16*>(x), cols, k, static_cast<long long>(T) * k, row_of_slot,
+                        codes, scales);
+}
+
+cudaError_t launch_fp8_quant_weights(const void* w, int E, int N, int K, uint8_t* codes, float* scales,
+                                     cudaStream_t st) {
+  return launch_chained(fp8_quant_tile_kernel<true>, dim3(E * ((N + 127) / 128), 1), dim3(256), 0, st, true,
+                        static_cast<const __nv_bfloat16*>(w), N, K, E, static_cast<const int32_t*>(nullptr), codes,
+                        scales);
+}
+
+cudaError_t launch_fp8_quant_cols(const void* x, int rows, int cols, const int32_t* seg, int E, uint8_t* codes,
+                                  float* scales, cudaStream_t st) {
+  const int blocks = static_cast<int>(fp8_padded_rows(rows, E) / 128);
+  const int tiles = (cols + 127) / 128;
+  int split = (1216 + blocks - 1) / blocks;  // about eight blocks an SM
+  split = split < 1 ? 1 : (split < tiles ? split : tiles);
+  return launch_chained(fp8_quant_tile_kernel<false>, dim3(blocks, split), dim3(256), 0, st, true,
+                        static_cast<const __nv_bfloat16*>(x), rows, cols, E, seg, codes, scales);
+}
+
+}  // namespace kmoe
