@@ -120,7 +120,7 @@ int kmoe_quantize_fp8_cols(const void* x_bf16, int rows, int cols, const int32_t
  *   ceil(K/128)] float (kmoe_quantize_fp8_weights', or a checkpoint's);
  *   seg_start [E + 1] int32 on the device, ascending, from 0 (null: E = 1, all
  *   rows); out [M, N] (transposed: [M, K]).  Rows outside all segments keep
- *   their contents.  N and K multiples of 16, x and w 16-byte aligned.
+ *   their contents.  N and K multiples of 16; x, w and out 16-byte aligned.
  *   workspace: KMOE_GEMM_FP8_WORKSPACE_BYTES, 256-byte aligned: its first word
  *   is the device error word (kmoe_device_error), cleared by every call that
  *   has rows.  Calls that can overlap on the GPU take a workspace each. */

@@ -183,7 +183,7 @@ int kmoe_gemm_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   if (M == 0) return KMOE_OK;
   if (!x || !x_scales || !w || !w_scales || !out) return KMOE_ERR_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(seg_start, 4) ||
-      !aligned(out, f32 ? 4 : 2))
+      !aligned(out, 16))
     return KMOE_ERR_ALIGN;
   a.seg = seg_start;
   a.a_sf = w_scales;
@@ -201,11 +201,13 @@ int kmoe_gemm_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   a.ldb = M;
   a.f32 = f32;
   Fp8Maps m;
-  if (!make_weights_map(&m.a, w, E, N, K) || !make_codes_map(&m.b, x, M, back ? N : K, kFp8BoxRows))
+  if (!make_weights_map(&m.a, w, E, N, K) ||
+      !make_codes_map(&m.b, x, M, back ? N : K, fp8_box_rows(fp8_tile_columns(M, E))))
     return KMOE_ERR_CUDA;
   const int sms = num_sms();
   if (sms <= 0) return KMOE_ERR_CUDA;
-  KMOE_CK(launch_fp8_gemm(back ? FP8_ROWS_GRAD : FP8_ROWS, m, a, sms, stream));
+  KMOE_CK(fp8_tile_columns(M, E) == 0 ? launch_fp8_gemm_wide(back, m, a, sms, stream)
+                                      : launch_fp8_gemm(back ? FP8_ROWS_GRAD : FP8_ROWS, m, a, sms, stream));
   return KMOE_OK;
 }
 
@@ -243,7 +245,7 @@ int kmoe_gemm_fp8_wgrad(const uint8_t* dy, const float* dy_scales, const uint8_t
   a.F = K;
   a.FT = blocks_of(K);
   a.C = N;
-  a.CT = (N + 255) / 256;
+  a.CT = (N + kWeightGradColumns - 1) / kWeightGradColumns;
   a.ldb = N;
   Fp8Maps m;
   if (!make_codes_map(&m.a, x, P, K, 128) || !make_codes_map(&m.b, dy, P, N, 128)) return KMOE_ERR_CUDA;

@@ -17,7 +17,7 @@ enum Fp8Kind {
 
 struct Fp8Maps {
   CUtensorMap a;  // features: weights in boxes of 128 x 128, or x's columns
-  CUtensorMap b;  // columns: rows in boxes of kFp8BoxRows rows, or dy's columns
+  CUtensorMap b;  // columns: rows in boxes of fp8_box_rows, or dy's columns
 };
 
 struct Fp8Args {
@@ -37,12 +37,18 @@ struct Fp8Args {
   int f32;         // out is fp32, else bf16
 };
 
-// Rows (columns of D) of a tile by the number of rows an expert has on
-// average, and rows of a TMA box of them.
-int fp8_tile_columns(int M, int E);
-constexpr int kFp8BoxRows = 32;
+// The kernel for M rows of E experts, by the rows an expert has on average:
+// fp8_gemm.cu with tiles of 32 or 128 rows, or (0) fp8_gemm_wide.cu.
+inline int fp8_tile_columns(int M, int E) {
+  const int avg = (M + E - 1) / E;
+  return avg <= 32 ? 32 : (avg <= 128 ? 128 : 0);
+}
+constexpr int kWeightGradColumns = 192;
+// Rows of a TMA box of such tiles.
+constexpr int fp8_box_rows(int tile_columns) { return tile_columns == 0 ? 128 : (tile_columns < 64 ? tile_columns : 64); }
 
 cudaError_t launch_fp8_gemm(Fp8Kind kind, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
+cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
 
 cudaError_t launch_fp8_quant_rows(const void* x, int rows, int cols, uint8_t* codes, float* scales, cudaStream_t st);
 cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, const int32_t* row_of_slot, uint8_t* codes,

@@ -1,0 +1,54 @@
+// Device pieces shared by the kernels of the block-scaled E4M3 products.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "fp8.cuh"
+
+namespace kmoe {
+
+// Instruction descriptor of kind::f8f6f4: fp32 D (bits 4-5), E4M3 operands,
+// bit 15 / 16 A / B is MN-major, 17-22 N >> 3, 24-28 M >> 4.
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8_el(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Waits for this warp's TMEM reads; the values of `r` are read after it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// mbar_wait_warp for waits of a few hundred cycles: the clock that bounds them
+// (its read takes longer than that) is looked at from the 256th poll on.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t budget_ns, uint32_t* err,
+                                          volatile int* abort) {
+  for (int i = 0; i < 256; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  }
+  return mbar_wait_warp(bar, parity, budget_ns, err, abort);
+}
+
+// A work item: features f0 .. of expert e for the columns (rows of the batch)
+// c0 .. c0 + n, over blocks kb .. kb + kn of the sum.
+struct Fp8Item {
+  int e, f0;
+  int c0, n;
+  int kb, kn;
+};
+
+}  // namespace kmoe

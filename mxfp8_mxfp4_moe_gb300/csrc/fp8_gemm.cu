@@ -7,9 +7,9 @@
 // A block's inner sum is four tcgen05.mma (kind::f8f6f4, K = 32) into a fresh
 // TMEM accumulator; the epilogue warps read it while the next block's runs in
 // another accumulator, multiply by the two scales and add in fp32 registers.
-// The features f are the MMA's M (128 lanes), the rows its N (16 .. BN), so
-// that a few rows cost few columns; sa is one value a block for a weight tile
-// (its scales are for 128 x 128) and one a lane for the weights' gradient.
+// The features f are the MMA's M, the rows its N (16 .. BN), so that a few
+// rows cost few columns; sa is one value a block for a weight tile (its scales
+// are for 128 x 128) and one a feature for the weights' gradient.
 //
 // Operands that are contiguous along the sum are K-major; the transposed
 // weights and both operands of the weights' gradient are read as they lie in
@@ -17,26 +17,29 @@
 //
 // Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues),
 // the others the epilogue: groups of four warps (one per TMEM lane quarter)
-// that take the 16-column chunks in turn.  Every wait is bounded.
+// that take the 32-column chunks in turn.  Every wait is bounded.
 #include <cuda_bf16.h>
 
-#include "fp8.cuh"
+#include "fp8_dev.cuh"
 
 namespace kmoe {
 
-// Instruction descriptor of kind::f8f6f4: fp32 D (bits 4-5), E4M3 operands,
-// bit 15 / 16 A / B is MN-major, 17-22 N >> 3, 24-28 M >> 4.
-__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
-  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_f8_el(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// 16 lanes x 32 columns: this thread reads, of each 8 columns g, columns 2q
+// and 2q + 1 (q = lane % 4) of lane lane / 4 (r[4g], r[4g + 1]) and of the lane
+// eight below (r[4g + 2], r[4g + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 8x8 matrices of 16-bit values, a row a quad of lanes, transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 template <Fp8Kind KIND_, int BN_>
@@ -47,37 +50,35 @@ struct Fp8Cfg {
   static constexpr bool A_MN = KIND != FP8_ROWS;
   static constexpr bool B_MN = WGRAD;
   static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_BYTES = BN * 128;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int BOX = WGRAD ? 128 : fp8_box_rows(BN);
+  static constexpr int STAGE = A_BYTES + (BN + BOX - 1) / BOX * BOX * 128;
   static constexpr int STAGES = 200 * 1024 / STAGE < 10 ? 200 * 1024 / STAGE : 10;
-  static constexpr int NG = BN >= 128 ? 2 : 1;  // epilogue groups of four warps
+  // an epilogue warp holds 64 columns of 32 features (a TMEM quarter): as many
+  // registers again for the block being read, and three warps a scheduler to
+  // cover the latency of the reads
+  static constexpr int CW = BN < 64 ? BN : 64;
+  static constexpr int NCH = CW / 32;  // 32-column chunks
+  static constexpr int NG = BN / CW;   // groups of four warps
   static constexpr int EPI_WARPS = 4 * NG;
-  static constexpr int THREADS = 32 * (2 + EPI_WARPS);
-  static constexpr int CW = BN / NG;      // columns of a group
-  static constexpr int CPL = CW / 32;     // scales a lane loads for a block
+  // twelve such warps: the loading and issuing warps are a warpgroup of their
+  // own that gives registers up (2 of its 4 idle)
+  static constexpr bool SPLIT_REGS = NG == 3;
+  static constexpr int CTRL_WARPS = SPLIT_REGS ? 4 : 2;
+  static constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
+  static constexpr int CTRL_REGS = 32, EPI_REGS = 160;
   static constexpr int NACC = 512 / BN < 4 ? 512 / BN : 4;
-  static constexpr int TMEM_COLS = NACC * BN < 32 ? 32 : NACC * BN;
+  static constexpr int TMEM_COLS = BN * NACC <= 128 ? 128 : 512;
   static constexpr int SC_OFF = STAGES * STAGE;
   static constexpr int SC_BYTES = EPI_WARPS * 2 * CW * 4;
   static constexpr int BAR_OFF = SC_OFF + SC_BYTES;
-  static constexpr int TAB_OFF = BAR_OFF + 512;
+  static constexpr int TAB_OFF = BAR_OFF + 256;
   static constexpr int TAB_INTS = kMaxE + 1;
   static constexpr int SMEM = 1024 + TAB_OFF + (2 * TAB_INTS + 40) * 4;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert((2 * STAGES + 2 * NACC + 1) * 8 + 8 <= 512, "barriers");
-  static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "TMEM columns");
+  static_assert((2 * STAGES + 2 * NACC + 1) * 8 + 8 <= 256, "barriers");
+  static_assert(BN * NACC <= TMEM_COLS, "TMEM columns");
+  static_assert(!SPLIT_REGS || 128 * CTRL_REGS + 32 * EPI_WARPS * EPI_REGS <= THREADS * 128, "register split");
 };
-
-struct Fp8Item {
-  int e, f0;   // expert, first feature
-  int c0, n;   // first column (a row of the batch, or of dW's n) and how many
-  int kb, kn;  // first block of the sum and how many
-};
-
-template <class C>
-__device__ __forceinline__ int fp8_items(const Fp8Args& a, const int32_t* unit) {
-  return C::WGRAD ? a.E * a.FT * a.CT : a.FT * unit[a.E];
-}
 
 template <class C>
 __device__ __forceinline__ Fp8Item fp8_item(const Fp8Args& a, const int32_t* first, const int32_t* unit, int w) {
@@ -150,181 +151,211 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
   segment_prefix(a.seg, a.E, a.M, C::WGRAD ? kScaleBlock : C::BN, first, unit, unit + C::TAB_INTS);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int total = fp8_items<C>(a, unit);
+  const int total = C::WGRAD ? a.E * a.FT * a.CT : a.FT * unit[a.E];
   const uint64_t budget = a.budget_ns;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
-    const uint64_t pol_a = policy_evict_normal(), pol_b = policy_evict_last();
-    uint32_t it = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-      const Fp8Item wk = fp8_item<C>(a, first, unit, w);
-      constexpr int kBox = C::WGRAD ? 128 : kFp8BoxRows;
-      const int boxes = (wk.n + kBox - 1) / kBox;
-      const uint32_t tx = C::A_BYTES + boxes * kBox * 128;
-      for (int kb = 0; kb < wk.kn; ++kb, ++it) {
-        const int s = it % C::STAGES;
-        if (!mbar_wait_warp(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, budget, a.err, abort_flag)) {
-          ok = false;
-          break;
-        }
-        uint8_t* sa = smem + s * C::STAGE;
-        uint8_t* sb = sa + C::A_BYTES;
-        const int k0 = (wk.kb + kb) * kScaleBlock;
-        mbar_arrive_expect_tx_el(&full[s], tx);
-        if constexpr (C::WGRAD) {
-          tma_load_2d_el(sa, &maps.a, &full[s], wk.f0, k0, pol_a);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d_el(sb + i * kBox * 128, &maps.b, &full[s], wk.c0 + i * kBox, k0, pol_b);
-        } else {
-          if constexpr (C::A_MN)
-            tma_load_3d_el(sa, &maps.a, &full[s], wk.f0, k0, wk.e, pol_a);
+  if (warp < C::CTRL_WARPS) {
+    // (of the registers that the block was launched with)
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CTRL_REGS));
+    if (warp == 0) {
+      // ------------------------------------------------------------ loads
+      const uint64_t pol_a = policy_evict_normal(), pol_b = policy_evict_last();
+      uint32_t it = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+        const Fp8Item wk = fp8_item<C>(a, first, unit, w);
+        const int boxes = (wk.n + C::BOX - 1) / C::BOX;
+        const uint32_t tx = C::A_BYTES + boxes * C::BOX * 128;
+        for (int kb = 0; kb < wk.kn; ++kb, ++it) {
+          const int s = it % C::STAGES;
+          if (!wait_warp(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, budget, a.err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + s * C::STAGE;
+          uint8_t* sb = sa + C::A_BYTES;
+          const int k0 = (wk.kb + kb) * kScaleBlock;
+          mbar_arrive_expect_tx_el(&full[s], tx);
+          if constexpr (C::WGRAD)
+            tma_load_2d_el(sa, &maps.a, &full[s], wk.f0, k0, pol_a);
           else
-            tma_load_3d_el(sa, &maps.a, &full[s], k0, wk.f0, wk.e, pol_a);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d_el(sb + i * kBox * 128, &maps.b, &full[s], k0, wk.c0 + i * kBox, pol_b);
+            tma_load_3d_el(sa, &maps.a, &full[s], C::A_MN ? wk.f0 : k0, C::A_MN ? k0 : wk.f0, wk.e, pol_a);
+          for (int i = 0; i < boxes; ++i) {
+            const int c = wk.c0 + i * C::BOX;
+            tma_load_2d_el(sb + i * C::BOX * 128, &maps.b, &full[s], C::B_MN ? c : k0, C::B_MN ? k0 : c, pol_b);
+          }
         }
       }
-    }
-    if (!ok) {
-      // let the copies already issued land before the CTA can exit
-      const uint32_t from = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
-      for (uint32_t i = from; i < it; ++i)
-        mbar_wait_warp(&full[i % C::STAGES], (i / C::STAGES) & 1u, 20000000ull, nullptr, nullptr);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA
-    // Steps of 32 along the sum: 32 bytes inside a K-major swizzle atom, 32
-    // rows of 128 bytes of an MN-major one (8-row groups 1024 bytes apart, the
-    // next 128 columns 16 KB on).
-    constexpr uint32_t kStepA = C::A_MN ? 256 : 2, kStepB = C::B_MN ? 256 : 2;
-    const uint64_t adesc0 = C::A_MN ? make_sdesc(smem_u32(smem), 16384, 1024, 2) : sdesc_kmajor_sw128(smem_u32(smem));
-    const uint64_t bdesc0 = C::B_MN ? make_sdesc(smem_u32(smem + C::A_BYTES), 16384, 1024, 2)
-                                    : sdesc_kmajor_sw128(smem_u32(smem + C::A_BYTES));
-    uint32_t it = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-      const Fp8Item wk = fp8_item<C>(a, first, unit, w);
-      const uint32_t idesc = idesc_f8(128, (wk.n + 15) & ~15, C::A_MN, C::B_MN);
-      for (int kb = 0; kb < wk.kn; ++kb, ++it) {
-        const int s = it % C::STAGES;
-        const uint32_t b = it % C::NACC;
-        if (!mbar_wait_warp(&acc_empty[b], ((it / C::NACC) & 1u) ^ 1u, budget, a.err, abort_flag) ||
-            !mbar_wait_warp(&full[s], (it / C::STAGES) & 1u, budget, a.err, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t so = static_cast<uint64_t>(s) * (C::STAGE >> 4);
-        const uint32_t d = tmem + b * C::BN;
+      if (!ok) {
+        // let the copies already issued land before the CTA can exit
+        const uint32_t from = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
+        for (uint32_t i = from; i < it; ++i)
+          mbar_wait_warp(&full[i % C::STAGES], (i / C::STAGES) & 1u, 20000000ull, nullptr, nullptr);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA
+      // Steps of 32 along the sum: 32 bytes inside a K-major swizzle atom, 32
+      // rows of 128 bytes of an MN-major one (8-row groups 1024 bytes apart,
+      // the next 128 columns 16 KB on).
+      constexpr uint32_t kStepA = C::A_MN ? 256 : 2, kStepB = C::B_MN ? 256 : 2;
+      const uint64_t adesc0 =
+          C::A_MN ? make_sdesc(smem_u32(smem), 16384, 1024, 2) : sdesc_kmajor_sw128(smem_u32(smem));
+      const uint64_t bdesc0 = C::B_MN ? make_sdesc(smem_u32(smem + C::A_BYTES), 16384, 1024, 2)
+                                      : sdesc_kmajor_sw128(smem_u32(smem + C::A_BYTES));
+      uint32_t it = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+        const Fp8Item wk = fp8_item<C>(a, first, unit, w);
+        const uint32_t idesc = idesc_f8(128, (wk.n + 15) & ~15, C::A_MN, C::B_MN);
+        for (int kb = 0; kb < wk.kn; ++kb, ++it) {
+          const int s = it % C::STAGES;
+          const uint32_t b = it % C::NACC;
+          if (!wait_warp(&acc_empty[b], ((it / C::NACC) & 1u) ^ 1u, budget, a.err, abort_flag) ||
+              !wait_warp(&full[s], (it / C::STAGES) & 1u, budget, a.err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t so = static_cast<uint64_t>(s) * (C::STAGE >> 4);
+          const uint32_t d = tmem + b * C::BN;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma_f8_el(d, adesc0 + so + i * kStepA, bdesc0 + so + i * kStepB, idesc, i > 0);
-        tc_commit_el(&empty[s]);
-        tc_commit_el(&acc_full[b]);
+          for (int i = 0; i < 4; ++i)
+            mma_f8_el(d, adesc0 + so + i * kStepA, bdesc0 + so + i * kStepB, idesc, i > 0);
+          tc_commit_el(&empty[s]);
+          tc_commit_el(&acc_full[b]);
+        }
       }
+      tc_commit_el(done);
+      mbar_wait_warp(done, 0, budget, a.err, nullptr);
     }
-    tc_commit_el(done);
-    mbar_wait_warp(done, 0, budget, a.err, nullptr);
   } else {
+    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::EPI_REGS));
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int grp = (warp - 2) >> 2;
-    float* sc = reinterpret_cast<float*>(smem + C::SC_OFF) + (warp - 2) * 2 * C::CW;
+    const int ew = warp - C::CTRL_WARPS;
+    const int grp = ew >> 2;
+    float* const ring = reinterpret_cast<float*>(smem + C::SC_OFF) + ew * 2 * C::CW;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    // A chunk's scales lie in the order in which the eight that a thread needs
+    // are two 16-byte pieces: columns 8g + 2q + {0, 1}, g even and the g after it.
+    float* const my_scale = ring + (lane >> 4) * 16 + ((lane & 7) >> 1) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1);
     uint32_t it = 0;
     bool ok = true;
     for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
       const Fp8Item wk = fp8_item<C>(a, first, unit, w);
-      const int f = wk.f0 + q * 32 + lane;
-      // column of the group's value i (i-th of CW), 16-column chunks in turn
-      auto column = [&](int i) { return ((i >> 4) * C::NG + grp) * 16 + (i & 15); };
-      const float* a_sf;
-      long long a_step;
-      if constexpr (C::WGRAD) {
-        a_sf = a.a_sf + static_cast<long long>(wk.kb) * a.F + min(f, a.F - 1);
-        a_step = a.F;
-      } else {
+      const int f0 = wk.f0 + q * 32;  // the warp's first feature
+      // the group's 32-column chunks start at column(0), column(1)
+      auto column = [&](int i) { return (i * C::NG + grp) * 32; };
+      const int nch = (wk.n - grp * 32 + C::NG * 32 - 1) / (C::NG * 32);  // chunks with columns of the tile
+      const float *a_sf, *b_sf = a.b_sf + static_cast<long long>(wk.kb) * a.ldb + wk.c0 + lane;
+      if constexpr (C::WGRAD)
+        a_sf = a.a_sf + static_cast<long long>(wk.kb) * a.F + f0 + (lane >> 2);
+      else
         a_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm;
-        a_step = a.a_sk;
-      }
-      const float* b_sf = a.b_sf + static_cast<long long>(wk.kb) * a.ldb + wk.c0;
-      // the scales of a block: this lane's columns (0 past the tile) and sa
+      // a block's scales: this lane's column of each chunk (0 past the tile), and
+      // of the weights' or of the features lane / 4 + 8 v
+      constexpr int NA = C::WGRAD ? 4 : 1;
       struct Scales {
-        float b[C::CPL], a;
+        float b[C::NCH], a[NA];
       };
-      auto load = [&](int kb) {
-        Scales s{};
-        if (kb >= wk.kn) return s;
+      auto load = [&](int kb, Scales& s) {
+        if (kb >= wk.kn) return;
 #pragma unroll
-        for (int j = 0; j < C::CPL; ++j) {
-          const int c = column(lane + 32 * j);
-          s.b[j] = c < wk.n ? __ldg(b_sf + static_cast<long long>(kb) * a.ldb + c) : 0.f;
+        for (int j = 0; j < C::NCH; ++j) {
+          s.b[j] = 0.f;
+          if (column(j) + lane < wk.n) s.b[j] = __ldg(b_sf + column(j));
         }
-        s.a = __ldg(a_sf + kb * a_step);
-        return s;
+#pragma unroll
+        for (int v = 0; v < NA; ++v) {
+          s.a[v] = 0.f;
+          if (!C::WGRAD || f0 + (lane >> 2) + 8 * v < a.F) s.a[v] = __ldg(a_sf + 8 * v);
+        }
+        b_sf += a.ldb;
+        a_sf += C::WGRAD ? a.F : a.a_sk;
       };
       float2 acc[C::CW / 2];
 #pragma unroll
       for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      Scales s0 = load(0), s1 = load(1);
+      Scales s0{}, s1{};
+      load(0, s0);
+      load(1, s1);
       for (int kb = 0; kb < wk.kn; ++kb, ++it) {
-        const Scales s = s0;
-        s0 = s1;
-        s1 = load(kb + 2);
-        float* buf = sc + (kb & 1) * C::CW;
-#pragma unroll
-        for (int j = 0; j < C::CPL; ++j) buf[lane + 32 * j] = C::WGRAD ? s.b[j] : s.b[j] * s.a;
-        __syncwarp();
         const uint32_t b = it % C::NACC;
-        if (!mbar_wait_warp(&acc_full[b], (it / C::NACC) & 1u, budget, a.err, abort_flag)) {
+        float* const mine = my_scale + (kb & 1) * C::CW;
+#pragma unroll
+        for (int j = 0; j < C::NCH; ++j) mine[32 * j] = C::WGRAD ? s0.b[j] : s0.b[j] * s0.a[0];
+        float sa[NA];
+#pragma unroll
+        for (int v = 0; v < NA; ++v) sa[v] = s0.a[v];
+        s0 = s1;
+        load(kb + 2, s1);
+        if (!wait_warp(&acc_full[b], (it / C::NACC) & 1u, budget, a.err, abort_flag)) {
           ok = false;
           break;
         }
+        __syncwarp();
         tc_fence_after();
         const uint32_t t = tmem + lanes + b * C::BN;
+        uint32_t r[C::NCH][32];
 #pragma unroll
-        for (int i = 0; i < C::CW / 16; ++i) {
-          const int c = (i * C::NG + grp) * 16;
-          if (c < wk.n) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(t + c, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const float4 sv = reinterpret_cast<const float4*>(buf + 16 * i)[v];
-              float2 x0 = make_float2(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]));
-              float2 x1 = make_float2(__uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
-              if constexpr (C::WGRAD) {
-                x0 = __fmul2_rn(x0, make_float2(s.a, s.a));
-                x1 = __fmul2_rn(x1, make_float2(s.a, s.a));
-              }
-              acc[8 * i + 2 * v] = __ffma2_rn(x0, make_float2(sv.x, sv.y), acc[8 * i + 2 * v]);
-              acc[8 * i + 2 * v + 1] = __ffma2_rn(x1, make_float2(sv.z, sv.w), acc[8 * i + 2 * v + 1]);
-            }
+        for (int i = 0; i < C::NCH; ++i)
+          if (i < nch) {
+            tmem_ld_16x256b_x4(t + column(i), r[i]);
+            tmem_ld_16x256b_x4(t + (16u << 16) + column(i), r[i] + 16);
           }
-        }
+#pragma unroll
+        for (int i = 0; i < C::NCH; ++i) tmem_ld_wait_for(r[i]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[b]);
+        const float* const scale = ring + (kb & 1) * C::CW + (lane & 3) * 4;
+#pragma unroll
+        for (int i = 0; i < C::NCH; ++i) {
+          if (i >= nch) continue;
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            const float4 sv = *reinterpret_cast<const float4*>(scale + 32 * i + 8 * g);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {  // features lane / 4 + 8 h
+              const uint32_t* v = r[i] + (h >> 1) * 16 + 4 * g + (h & 1) * 2;
+              float2 x0 = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+              float2 x1 = make_float2(__uint_as_float(v[4]), __uint_as_float(v[5]));
+              if constexpr (C::WGRAD) {
+                x0 = __fmul2_rn(x0, make_float2(sa[h], sa[h]));
+                x1 = __fmul2_rn(x1, make_float2(sa[h], sa[h]));
+              }
+              float2* d = acc + (4 * i + h) * 4 + g;
+              d[0] = __ffma2_rn(x0, make_float2(sv.x, sv.y), d[0]);
+              d[1] = __ffma2_rn(x1, make_float2(sv.z, sv.w), d[1]);
+            }
+          }
+        }
       }
       if (!ok) break;
-      if (f < a.F) {
-        const long long row0 = C::WGRAD ? static_cast<long long>(wk.e) * a.C + wk.c0 : wk.c0;
-        auto store = [&](int i, float v) {
-          const int c = column(i);
-          if (c >= wk.n) return;
-          const long long at = (row0 + c) * a.F + f;
-          if (C::WGRAD || a.f32)
-            static_cast<float*>(a.out)[at] = v;
-          else
-            static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
-        };
+      const long long row0 = C::WGRAD ? static_cast<long long>(wk.e) * a.C + wk.c0 : wk.c0;
 #pragma unroll
-        for (int i = 0; i < C::CW / 2; ++i) {
-          store(2 * i, acc[i].x);
-          store(2 * i + 1, acc[i].y);
+      for (int i = 0; i < C::NCH; ++i) {
+        if (i >= nch) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = column(i) + 8 * g;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float2 d = acc[(4 * i + h) * 4 + g];
+            if (C::WGRAD || a.f32) {
+              const int f = f0 + 8 * h + (lane >> 2), cc = c + 2 * (lane & 3);
+              float* o = static_cast<float*>(a.out) + (row0 + cc) * a.F + f;
+              if (f < a.F && cc < wk.n) o[0] = d.x;
+              if (f < a.F && cc + 1 < wk.n) o[a.F] = d.y;
+            } else {
+              // two features of one row a lane
+              const __nv_bfloat162 p = __floats2bfloat162_rn(d.x, d.y);
+              const uint32_t u = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p));
+              const int f = f0 + 8 * h + 2 * (lane & 3), cc = c + (lane >> 2);
+              if (f < a.F && cc < wk.n)
+                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row0 + cc) * a.F + f) = u;
+            }
+          }
         }
       }
     }
@@ -335,11 +366,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-}
-
-int fp8_tile_columns(int M, int E) {
-  const int avg = (M + E - 1) / E;
-  return avg <= 32 ? 32 : (avg <= 128 ? 128 : 256);
 }
 
 template <class C>
@@ -361,17 +387,18 @@ static cudaError_t launch_cfg(const Fp8Maps& maps, const Fp8Args& a, int sms, cu
                         C::SMEM, st, true, maps, a);
 }
 
+template <Fp8Kind KIND>
+static cudaError_t launch_rows(const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
+  return fp8_tile_columns(a.M, a.E) == 32 ? launch_cfg<Fp8Cfg<KIND, 32>>(maps, a, sms, st)
+                                          : launch_cfg<Fp8Cfg<KIND, 128>>(maps, a, sms, st);
+}
+
 cudaError_t launch_fp8_gemm(Fp8Kind kind, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
-  if (kind == FP8_WEIGHT_GRAD) return launch_cfg<Fp8Cfg<FP8_WEIGHT_GRAD, 256>>(maps, a, sms, st);
-  const int bn = fp8_tile_columns(a.M, a.E);
-  if (kind == FP8_ROWS) {
-    if (bn == 32) return launch_cfg<Fp8Cfg<FP8_ROWS, 32>>(maps, a, sms, st);
-    if (bn == 128) return launch_cfg<Fp8Cfg<FP8_ROWS, 128>>(maps, a, sms, st);
-    return launch_cfg<Fp8Cfg<FP8_ROWS, 256>>(maps, a, sms, st);
+  switch (kind) {
+    case FP8_WEIGHT_GRAD: return launch_cfg<Fp8Cfg<FP8_WEIGHT_GRAD, kWeightGradColumns>>(maps, a, sms, st);
+    case FP8_ROWS_GRAD: return launch_rows<FP8_ROWS_GRAD>(maps, a, sms, st);
+    default: return launch_rows<FP8_ROWS>(maps, a, sms, st);
   }
-  if (bn == 32) return launch_cfg<Fp8Cfg<FP8_ROWS_GRAD, 32>>(maps, a, sms, st);
-  if (bn == 128) return launch_cfg<Fp8Cfg<FP8_ROWS_GRAD, 128>>(maps, a, sms, st);
-  return launch_cfg<Fp8Cfg<FP8_ROWS_GRAD, 256>>(maps, a, sms, st);
 }
 
 }  // namespace kmoe
