@@ -33,14 +33,28 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// mbar_wait_warp for waits of a few hundred cycles: the clock that bounds them
-// (its read takes longer than that) is looked at from the 256th poll on.
+__device__ __forceinline__ void tmem_ld_wait_for16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// mbar_wait_warp for waits of a few hundred cycles, once or twice a block: the
+// lanes poll without a vote and the clock that bounds the wait (reading it takes
+// longer than most of these waits) is looked at from the 256th poll on.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t budget_ns, uint32_t* err,
                                           volatile int* abort) {
-  for (int i = 0; i < 256; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  }
+  bool there = false;
+  for (int i = 0; i < 256 && !there; ++i) there = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, there)) return true;
   return mbar_wait_warp(bar, parity, budget_ns, err, abort);
+}
+
+// 4 bytes to shared memory, in the thread's cp.async group.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // A work item: features f0 .. of expert e for the columns (rows of the batch)

@@ -9,6 +9,7 @@
 // column, from shared memory that the tensor core is reading.
 //
 // Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues),
+// warp 2 the scales (a ring in shared memory, some blocks ahead of their use),
 // warps 4 .. 15 the epilogue: three groups of four (one warp per TMEM lane
 // quarter) that take the eight 32-column chunks in turn.  Every wait is
 // bounded.
@@ -23,19 +24,27 @@ struct Fp8WideCfg {
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 4;
-  static constexpr int NG = 3, NCH = 3;  // groups, and the most 32-column chunks of one
+  // a group's four warps hold 128 features of the tile, 16 of which they read
+  // while the 16 before are added
+  static constexpr int NG = 2, NCH = 8;
   static constexpr int EPI_WARPS = 4 * NG;
   static constexpr int CTRL_WARPS = 4;
   static constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
-  // 96 accumulators a thread and 32 values being read
-  static constexpr int CTRL_REGS = 32, EPI_REGS = 160;
+  static constexpr int CTRL_REGS = 104, EPI_REGS = 200;
   static constexpr int NACC = 2;
-  static constexpr int BAR_OFF = STAGES * STAGE;
+  // ring of scales: a block's 128 rows and its tile's two blocks of features
+  static constexpr int RING = 8, AHEAD = 4;  // slots, and blocks loaded ahead
+  static constexpr int SLOT = 128 + 4;       // floats
+  static constexpr int SC_OFF = STAGES * STAGE;
+  // rows on their way out: 32 of 64 bytes a warp
+  static constexpr int OUT_OFF = SC_OFF + (RING * SLOT * 4 + 15) / 16 * 16;
+  static constexpr int BAR_OFF = OUT_OFF + EPI_WARPS * 2048;
   static constexpr int TAB_OFF = BAR_OFF + 256;
   static constexpr int TAB_INTS = kMaxE + 1;
   static constexpr int SMEM = 1024 + TAB_OFF + (2 * TAB_INTS + 40) * 4;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(128 * CTRL_REGS + 32 * EPI_WARPS * EPI_REGS <= THREADS * 128, "register split");
+  static_assert(RING >= AHEAD + NACC + 1, "a slot is written again when its block has been read");
+  static_assert(128 * CTRL_REGS + 32 * EPI_WARPS * EPI_REGS <= THREADS * 168, "register split");
 };
 
 template <class C>
@@ -76,7 +85,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < C::NACC; ++b) {
-      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_full[b], 2);  // the block's products, and its scales
       mbar_init(&acc_empty[b], C::EPI_WARPS);
     }
     mbar_init(done, 1);
@@ -163,6 +172,54 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
       }
       tc_commit_el(done);
       mbar_wait_warp(done, 0, budget, a.err, nullptr);
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ scales
+      const uint32_t ring = smem_u32(smem + C::SC_OFF);
+      // the block that is loaded next: the issued-th of this CTA's
+      int w = blockIdx.x - gridDim.x, kb = 0, kn = 0;
+      const float *x_sf = nullptr, *w_sf = nullptr;
+      bool more = true;
+      uint32_t issued = 0;
+      int n = 0, second = 0;
+      auto issue = [&] {
+        if (kb == kn) {  // the next item
+          w += gridDim.x;
+          more = w < total;
+          if (more) {
+            const Fp8Item wk = wide_item<C>(a, first, unit, w);
+            kb = 0;
+            kn = wk.kn;
+            n = wk.n;
+            x_sf = a.b_sf + wk.c0;
+            w_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm;
+            second = a.F - wk.f0 > 128 ? a.a_sm : 0;
+          }
+        }
+        if (more) {
+          const uint32_t at = ring + (issued & (C::RING - 1)) * (C::SLOT * 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) cp_async4(at + (32 * j + lane) * 4, x_sf + min(32 * j + lane, n - 1));
+          if (lane < 2) cp_async4(at + (128 + lane) * 4, w_sf + lane * second);
+          x_sf += a.ldb;
+          w_sf += a.a_sk;
+          ++kb;
+          ++issued;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll 1
+      for (int i = 0; i < C::AHEAD; ++i) issue();
+#pragma unroll 1
+      for (uint32_t it = 0;; ++it) {
+        const uint32_t b = it % C::NACC;
+        if (it < issued && !wait_warp(&acc_empty[b], ((it / C::NACC) & 1u) ^ 1u, budget, a.err, abort_flag)) break;
+        issue();  // the slot's last block was read before the accumulator above was released
+        if (it >= issued) break;
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_full[b]);
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::EPI_REGS));
@@ -170,99 +227,107 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
     const int q = warp & 3;
     const int grp = (warp - C::CTRL_WARPS) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    uint8_t* const out_smem = smem + C::OUT_OFF + (warp - C::CTRL_WARPS) * 2048;
     uint32_t it = 0;
     bool ok = true;
     for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
       const Fp8Item wk = wide_item<C>(a, first, unit, w);
       const int row = q * 32 + lane;
-      const int nf = min(C::BN, a.F - wk.f0);
-      // the group's chunk i holds features 32 (3 i + grp) ..
-      const int nch = ((nf + 31) / 32 - grp + C::NG - 1) / C::NG;
-      // scales of a block of the sum: this row's, and the tile's two blocks of
-      // 128 features'; rows past the tile take its last one's
-      const float* x_sf = a.b_sf + wk.c0 + min(row, wk.n - 1);
-      const float* w_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm;
-      const int second = nf > 128 ? a.a_sm : 0;
-      float2 acc[C::NCH][16];
+      const int g0 = wk.f0 + grp * 128;  // the group's first feature
+      const int ng = a.F - g0;           // and how many there are from there (128 used)
+      float2 acc[C::NCH][8];
 #pragma unroll
       for (int i = 0; i < C::NCH; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[i][j] = make_float2(0.f, 0.f);
-      struct Scales {
-        float x, w0, w1;
-      };
-      auto load = [&](int kb, Scales& s) {
-        if (kb >= wk.kn) return;
-        s.x = __ldg(x_sf);
-        s.w0 = __ldg(w_sf);
-        s.w1 = __ldg(w_sf + second);
-        x_sf += a.ldb;
-        w_sf += a.a_sk;
-      };
-      Scales s0{}, s1{};
-      load(0, s0);
-      load(1, s1);
+        for (int j = 0; j < 8; ++j) acc[i][j] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < wk.kn; ++kb, ++it) {
         const uint32_t b = it % C::NACC;
-        const float lo = s0.x * s0.w0, hi = s0.x * s0.w1;
-        s0 = s1;
-        load(kb + 2, s1);
         if (!wait_warp(&acc_full[b], (it / C::NACC) & 1u, budget, a.err, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t t = tmem + lanes + b * C::BN + grp * 32;
+        const uint32_t t = tmem + lanes + b * C::BN + grp * 128;
+        const float* slot = reinterpret_cast<const float*>(smem + C::SC_OFF) + (it & (C::RING - 1)) * C::SLOT;
+        auto add = [&](int i, const uint32_t(&v)[16], float2 f) {
 #pragma unroll
-        for (int i = 0; i < C::NCH; ++i) {
-          if (i < nch) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(t + i * C::NG * 32, r);
-            tmem_ld_wait_for(r);
-            if (i == nch - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&acc_empty[b]);
-            }
-            const float f = i * C::NG + grp < 4 ? lo : hi;
-            const float2 ff = make_float2(f, f);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[i][j] = __ffma2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), ff,
-                                     acc[i][j]);
-          }
-        }
-        if (nch <= 0) {
+          for (int j = 0; j < 8; ++j)
+            acc[i][j] = __ffma2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f, acc[i][j]);
+        };
+        auto release = [&] {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[b]);
+        };
+        if (ng >= 128) {  // without branches: the values read stay where they are
+          uint32_t r[2][16];
+          tmem_ld_32x32b_x16(t, r[0]);
+          const float f = slot[row] * slot[128 + grp];
+#pragma unroll
+          for (int i = 0; i < C::NCH; ++i) {
+            tmem_ld_wait_for16(r[i & 1]);
+            if (i + 1 < C::NCH)
+              tmem_ld_32x32b_x16(t + 16 * (i + 1), r[(i + 1) & 1]);
+            else
+              release();
+            add(i, r[i & 1], make_float2(f, f));
+          }
+        } else {
+          const float f = slot[row] * slot[128 + grp];
+#pragma unroll
+          for (int i = 0; i < C::NCH; ++i) {
+            if (16 * i >= ng) continue;
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(t + 16 * i, v);
+            tmem_ld_wait_for16(v);
+            add(i, v, make_float2(f, f));
+          }
+          release();
         }
       }
       if (!ok) break;
-      if (row < wk.n) {
+      // Rows go out by way of shared memory, 64 bytes of each at a time: a
+      // store covers eight rows' pieces instead of 32 rows' 16 bytes.  The
+      // 16-byte pieces of a row are stored at piece ^ (row / 2 & 3).
+      uint8_t* const mine = out_smem + lane * 64;
+      const int o_row = lane >> 2, o_piece = lane & 3;
+      auto out_piece = [&](int j, const uint4& v) {
+        *reinterpret_cast<uint4*>(mine + ((j ^ ((lane >> 1) & 3)) << 4)) = v;
+      };
+      // the staged 64 bytes of the rows, from byte `at` of a row of `bytes` on
+      auto flush = [&](long long at, long long bytes, int pieces) {
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < C::NCH; ++i) {
-          if (i >= nch) continue;
-          const int f = wk.f0 + (i * C::NG + grp) * 32;
-          const long long at = static_cast<long long>(wk.c0 + row) * a.F + f;
+        for (int v = 0; v < 4; ++v) {
+          const int r = 8 * v + o_row;
+          const uint4 u = *reinterpret_cast<const uint4*>(out_smem + r * 64 + ((o_piece ^ ((r >> 1) & 3)) << 4));
+          if (q * 32 + r < wk.n && o_piece < pieces)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (wk.c0 + q * 32 + r) * bytes + at + o_piece * 16) =
+                u;
+        }
+        __syncwarp();
+      };
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // eight features
-            if (f + 8 * j >= a.F) continue;
-            const float2* d = acc[i] + 4 * j;
-            if (a.f32) {
-              float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) + 2 * j;
-              o[0] = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);
-              o[1] = make_float4(d[2].x, d[2].y, d[3].x, d[3].y);
-            } else {
-              uint32_t u[4];
+      for (int i = 0; i < C::NCH; ++i) {
+        const float2* d = acc[i];
+        if (a.f32) {
+          if (16 * i < ng) {
 #pragma unroll
-              for (int v = 0; v < 4; ++v) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(d[v].x, d[v].y);
-                u[v] = *reinterpret_cast<const uint32_t*>(&p);
-              }
-              reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at)[j] = make_uint4(u[0], u[1], u[2], u[3]);
-            }
+            for (int j = 0; j < 4; ++j)
+              out_piece(j, make_uint4(__float_as_uint(d[2 * j].x), __float_as_uint(d[2 * j].y),
+                                      __float_as_uint(d[2 * j + 1].x), __float_as_uint(d[2 * j + 1].y)));
+            flush((g0 + 16 * i) * 4LL, a.F * 4LL, 4);
           }
+        } else {
+          uint32_t u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(d[j].x, d[j].y);
+            u[j] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          out_piece((i & 1) * 2, make_uint4(u[0], u[1], u[2], u[3]));
+          out_piece((i & 1) * 2 + 1, make_uint4(u[4], u[5], u[6], u[7]));
+          if ((i & 1) && 16 * (i - 1) < ng) flush((g0 + 16 * (i - 1)) * 2LL, a.F * 2LL, 16 * i < ng ? 4 : 2);
         }
       }
     }
