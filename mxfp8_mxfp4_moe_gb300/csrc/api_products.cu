@@ -207,7 +207,7 @@ int kmoe_gemm_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   const int sms = num_sms();
   if (sms <= 0) return KMOE_ERR_CUDA;
   KMOE_CK(fp8_tile_columns(M, E) == 0 ? launch_fp8_gemm_wide(back, m, a, sms, stream)
-                                      : launch_fp8_gemm(back ? FP8_ROWS_GRAD : FP8_ROWS, m, a, sms, stream));
+                                      : launch_fp8_gemm(back, m, a, sms, stream));
   return KMOE_OK;
 }
 
@@ -251,7 +251,7 @@ int kmoe_gemm_fp8_wgrad(const uint8_t* dy, const float* dy_scales, const uint8_t
   if (!make_codes_map(&m.a, x, P, K, 128) || !make_codes_map(&m.b, dy, P, N, 128)) return KMOE_ERR_CUDA;
   const int sms = num_sms();
   if (sms <= 0) return KMOE_ERR_CUDA;
-  KMOE_CK(launch_fp8_gemm(FP8_WEIGHT_GRAD, m, a, sms, stream));
+  KMOE_CK(launch_fp8_wgrad(m, a, sms, stream));
   return KMOE_OK;
 }
 

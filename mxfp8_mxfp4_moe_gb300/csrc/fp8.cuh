@@ -7,17 +7,9 @@ namespace kmoe {
 
 constexpr int kScaleBlock = 128;  // values a scale
 
-// What a product computes; all three accumulate D[feature, column] with the
-// features in the tensor core's M slot.
-enum Fp8Kind {
-  FP8_ROWS = 0,         // out[row, n] = sum_k x[row, k] w[n, k]:  features n, columns rows
-  FP8_ROWS_GRAD = 1,    // out[row, k] = sum_n x[row, n] w[n, k]:  features k, columns rows
-  FP8_WEIGHT_GRAD = 2,  // out[n, k] = sum_row dy[row, n] x[row, k]:  features k, columns n
-};
-
 struct Fp8Maps {
-  CUtensorMap a;  // features: weights in boxes of 128 x 128, or x's columns
-  CUtensorMap b;  // columns: rows in boxes of fp8_box_rows, or dy's columns
+  CUtensorMap a;  // weights in boxes of 128 x 128 (weight gradient: x)
+  CUtensorMap b;  // rows in boxes of fp8_box_rows (weight gradient: dy)
 };
 
 struct Fp8Args {
@@ -43,12 +35,13 @@ inline int fp8_tile_columns(int M, int E) {
   const int avg = (M + E - 1) / E;
   return avg <= 32 ? 32 : (avg <= 128 ? 128 : 0);
 }
-constexpr int kWeightGradColumns = 192;
 // Rows of a TMA box of such tiles.
 constexpr int fp8_box_rows(int tile_columns) { return tile_columns == 0 ? 128 : (tile_columns < 64 ? tile_columns : 64); }
 
-cudaError_t launch_fp8_gemm(Fp8Kind kind, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
+cudaError_t launch_fp8_gemm(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
 cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
+constexpr int kWeightGradColumns = 240;  // n of a tile of the weights' gradient
+cudaError_t launch_fp8_wgrad(const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
 
 cudaError_t launch_fp8_quant_rows(const void* x, int rows, int cols, uint8_t* codes, float* scales, cudaStream_t st);
 cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, const int32_t* row_of_slot, uint8_t* codes,

@@ -1,25 +1,22 @@
 // Products of E4M3 operands with a scale for each block of 128 values of the
-// sum: rows times weights, rows times transposed weights (the rows' gradient)
-// and columns times columns (the weights' gradient), dense or by expert.
+// sum: rows times weights and rows times transposed weights (the rows'
+// gradient), dense or by expert.  This kernel takes the batches with few rows
+// for each expert, fp8_gemm_wide.cu those with many; fp8_wgrad.cu has the
+// weights' gradient.
 //
-//   D[f, c] = sum over blocks b of 128:  sa(f, b) sb(c, b) sum_{i in b} A[f, i] B[c, i]
+//   out[r, f] = sum over blocks b of 128:  sx[b, r] sw(f, b) sum_{i in b} x[r, i] w[f, i]
 //
 // A block's inner sum is four tcgen05.mma (kind::f8f6f4, K = 32) into a fresh
 // TMEM accumulator; the epilogue warps read it while the next block's runs in
 // another accumulator, multiply by the two scales and add in fp32 registers.
 // The features f are the MMA's M, the rows its N (16 .. BN), so that a few
-// rows cost few columns; sa is one value a block for a weight tile (its scales
-// are for 128 x 128) and one a feature for the weights' gradient.
-//
-// Operands that are contiguous along the sum are K-major; the transposed
-// weights and both operands of the weights' gradient are read as they lie in
-// memory, MN-major (128-byte swizzle either way).
+// rows cost few columns.  Operands that are contiguous along the sum are
+// K-major; transposed weights are read as they lie in memory, MN-major
+// (128-byte swizzle either way).
 //
 // Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues),
 // the others the epilogue: groups of four warps (one per TMEM lane quarter)
 // that take the 32-column chunks in turn.  Every wait is bounded.
-#include <cuda_bf16.h>
-
 #include "fp8_dev.cuh"
 
 namespace kmoe {
@@ -42,30 +39,22 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   return r;
 }
 
-template <Fp8Kind KIND_, int BN_>
+template <bool BACK_, int BN_>
 struct Fp8Cfg {
-  static constexpr Fp8Kind KIND = KIND_;
-  static constexpr int BN = BN_;  // columns of a tile
-  static constexpr bool WGRAD = KIND == FP8_WEIGHT_GRAD;
-  static constexpr bool A_MN = KIND != FP8_ROWS;
-  static constexpr bool B_MN = WGRAD;
+  static constexpr bool BACK = BACK_;  // the weights transposed, read MN-major
+  static constexpr int BN = BN_;       // columns of a tile
   static constexpr int A_BYTES = 128 * 128;
-  static constexpr int BOX = WGRAD ? 128 : fp8_box_rows(BN);
-  static constexpr int STAGE = A_BYTES + (BN + BOX - 1) / BOX * BOX * 128;
+  static constexpr int BOX = fp8_box_rows(BN);
+  static constexpr int STAGE = A_BYTES + BN * 128;
   static constexpr int STAGES = 200 * 1024 / STAGE < 10 ? 200 * 1024 / STAGE : 10;
-  // an epilogue warp holds 64 columns of 32 features (a TMEM quarter): as many
-  // registers again for the block being read, and three warps a scheduler to
-  // cover the latency of the reads
+  // an epilogue warp holds up to 64 columns of 32 features (a TMEM quarter), and
+  // in as many registers the block being read
   static constexpr int CW = BN < 64 ? BN : 64;
   static constexpr int NCH = CW / 32;  // 32-column chunks
   static constexpr int NG = BN / CW;   // groups of four warps
   static constexpr int EPI_WARPS = 4 * NG;
-  // twelve such warps: the loading and issuing warps are a warpgroup of their
-  // own that gives registers up (2 of its 4 idle)
-  static constexpr bool SPLIT_REGS = NG == 3;
-  static constexpr int CTRL_WARPS = SPLIT_REGS ? 4 : 2;
+  static constexpr int CTRL_WARPS = 2;
   static constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
-  static constexpr int CTRL_REGS = 32, EPI_REGS = 160;
   static constexpr int NACC = 512 / BN < 4 ? 512 / BN : 4;
   static constexpr int TMEM_COLS = BN * NACC <= 128 ? 128 : 512;
   static constexpr int SC_OFF = STAGES * STAGE;
@@ -77,35 +66,23 @@ struct Fp8Cfg {
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert((2 * STAGES + 2 * NACC + 1) * 8 + 8 <= 256, "barriers");
   static_assert(BN * NACC <= TMEM_COLS, "TMEM columns");
-  static_assert(!SPLIT_REGS || 128 * CTRL_REGS + 32 * EPI_WARPS * EPI_REGS <= THREADS * 128, "register split");
 };
 
 template <class C>
 __device__ __forceinline__ Fp8Item fp8_item(const Fp8Args& a, const int32_t* first, const int32_t* unit, int w) {
   Fp8Item it;
-  if constexpr (C::WGRAD) {
-    const int per = a.FT * a.CT;
-    it.e = w / per;
-    const int r = w - it.e * per;
-    it.f0 = r / a.CT * 128;
-    it.c0 = r % a.CT * C::BN;
-    it.n = min(C::BN, a.C - it.c0);
-    it.kb = min(unit[it.e], a.KB);
-    it.kn = min(unit[it.e + 1], a.KB) - it.kb;
-  } else {
-    it.e = segment_of_unit(unit, a.E, w / a.FT);
-    const int u0 = unit[it.e], nt = unit[it.e + 1] - u0;
-    const int r = w - u0 * a.FT;
-    it.f0 = r / nt * 128;
-    // an expert's rows in tiles of nearly the same size
-    const int rows = first[it.e + 1] - first[it.e];
-    const int per = ((rows + nt - 1) / nt + 15) / 16 * 16;
-    const int at = r % nt * per;
-    it.c0 = first[it.e] + at;
-    it.n = min(per, rows - at);
-    it.kb = 0;
-    it.kn = a.KB;
-  }
+  it.e = segment_of_unit(unit, a.E, w / a.FT);
+  const int u0 = unit[it.e], nt = unit[it.e + 1] - u0;
+  const int r = w - u0 * a.FT;
+  it.f0 = r / nt * 128;
+  // an expert's rows in tiles of nearly the same size
+  const int rows = first[it.e + 1] - first[it.e];
+  const int per = ((rows + nt - 1) / nt + 15) / 16 * 16;
+  const int at = r % nt * per;
+  it.c0 = first[it.e] + at;
+  it.n = min(per, rows - at);
+  it.kb = 0;
+  it.kn = a.KB;
   return it;
 }
 
@@ -148,15 +125,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;  // long before any wait can give up
   tc_fence_before();
-  segment_prefix(a.seg, a.E, a.M, C::WGRAD ? kScaleBlock : C::BN, first, unit, unit + C::TAB_INTS);
+  segment_prefix(a.seg, a.E, a.M, C::BN, first, unit, unit + C::TAB_INTS);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int total = C::WGRAD ? a.E * a.FT * a.CT : a.FT * unit[a.E];
+  const int total = a.FT * unit[a.E];
   const uint64_t budget = a.budget_ns;
 
   if (warp < C::CTRL_WARPS) {
-    // (of the registers that the block was launched with)
-    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CTRL_REGS));
     if (warp == 0) {
       // ------------------------------------------------------------ loads
       const uint64_t pol_a = policy_evict_normal(), pol_b = policy_evict_last();
@@ -174,16 +149,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
           }
           uint8_t* sa = smem + s * C::STAGE;
           uint8_t* sb = sa + C::A_BYTES;
-          const int k0 = (wk.kb + kb) * kScaleBlock;
+          const int k0 = kb * kScaleBlock;
           mbar_arrive_expect_tx_el(&full[s], tx);
-          if constexpr (C::WGRAD)
-            tma_load_2d_el(sa, &maps.a, &full[s], wk.f0, k0, pol_a);
-          else
-            tma_load_3d_el(sa, &maps.a, &full[s], C::A_MN ? wk.f0 : k0, C::A_MN ? k0 : wk.f0, wk.e, pol_a);
-          for (int i = 0; i < boxes; ++i) {
-            const int c = wk.c0 + i * C::BOX;
-            tma_load_2d_el(sb + i * C::BOX * 128, &maps.b, &full[s], C::B_MN ? c : k0, C::B_MN ? k0 : c, pol_b);
-          }
+          tma_load_3d_el(sa, &maps.a, &full[s], C::BACK ? wk.f0 : k0, C::BACK ? k0 : wk.f0, wk.e, pol_a);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d_el(sb + i * C::BOX * 128, &maps.b, &full[s], k0, wk.c0 + i * C::BOX, pol_b);
         }
       }
       if (!ok) {
@@ -195,18 +165,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA
       // Steps of 32 along the sum: 32 bytes inside a K-major swizzle atom, 32
-      // rows of 128 bytes of an MN-major one (8-row groups 1024 bytes apart,
-      // the next 128 columns 16 KB on).
-      constexpr uint32_t kStepA = C::A_MN ? 256 : 2, kStepB = C::B_MN ? 256 : 2;
+      // rows of 128 bytes of an MN-major one (8-row groups 1024 bytes apart).
+      constexpr uint32_t kStepA = C::BACK ? 256 : 2;
       const uint64_t adesc0 =
-          C::A_MN ? make_sdesc(smem_u32(smem), 16384, 1024, 2) : sdesc_kmajor_sw128(smem_u32(smem));
-      const uint64_t bdesc0 = C::B_MN ? make_sdesc(smem_u32(smem + C::A_BYTES), 16384, 1024, 2)
-                                      : sdesc_kmajor_sw128(smem_u32(smem + C::A_BYTES));
+          C::BACK ? make_sdesc(smem_u32(smem), 16384, 1024, 2) : sdesc_kmajor_sw128(smem_u32(smem));
+      const uint64_t bdesc0 = sdesc_kmajor_sw128(smem_u32(smem + C::A_BYTES));
       uint32_t it = 0;
       bool ok = true;
       for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
         const Fp8Item wk = fp8_item<C>(a, first, unit, w);
-        const uint32_t idesc = idesc_f8(128, (wk.n + 15) & ~15, C::A_MN, C::B_MN);
+        const uint32_t idesc = idesc_f8(128, (wk.n + 15) & ~15, C::BACK, false);
         for (int kb = 0; kb < wk.kn; ++kb, ++it) {
           const int s = it % C::STAGES;
           const uint32_t b = it % C::NACC;
@@ -220,7 +188,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
           const uint32_t d = tmem + b * C::BN;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            mma_f8_el(d, adesc0 + so + i * kStepA, bdesc0 + so + i * kStepB, idesc, i > 0);
+            mma_f8_el(d, adesc0 + so + i * kStepA, bdesc0 + so + i * 2, idesc, i > 0);
           tc_commit_el(&empty[s]);
           tc_commit_el(&acc_full[b]);
         }
@@ -229,7 +197,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
       mbar_wait_warp(done, 0, budget, a.err, nullptr);
     }
   } else {
-    if constexpr (C::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::EPI_REGS));
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     const int ew = warp - C::CTRL_WARPS;
@@ -247,16 +214,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
       // the group's 32-column chunks start at column(0), column(1)
       auto column = [&](int i) { return (i * C::NG + grp) * 32; };
       const int nch = (wk.n - grp * 32 + C::NG * 32 - 1) / (C::NG * 32);  // chunks with columns of the tile
-      const float *a_sf, *b_sf = a.b_sf + static_cast<long long>(wk.kb) * a.ldb + wk.c0 + lane;
-      if constexpr (C::WGRAD)
-        a_sf = a.a_sf + static_cast<long long>(wk.kb) * a.F + f0 + (lane >> 2);
-      else
-        a_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm;
-      // a block's scales: this lane's column of each chunk (0 past the tile), and
-      // of the weights' or of the features lane / 4 + 8 v
-      constexpr int NA = C::WGRAD ? 4 : 1;
+      const float* b_sf = a.b_sf + wk.c0 + lane;
+      const float* a_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm;
+      // a block's scales: this lane's column of each chunk (0 past the tile), and the weights'
       struct Scales {
-        float b[C::NCH], a[NA];
+        float b[C::NCH], a;
       };
       auto load = [&](int kb, Scales& s) {
         if (kb >= wk.kn) return;
@@ -265,13 +227,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
           s.b[j] = 0.f;
           if (column(j) + lane < wk.n) s.b[j] = __ldg(b_sf + column(j));
         }
-#pragma unroll
-        for (int v = 0; v < NA; ++v) {
-          s.a[v] = 0.f;
-          if (!C::WGRAD || f0 + (lane >> 2) + 8 * v < a.F) s.a[v] = __ldg(a_sf + 8 * v);
-        }
+        s.a = __ldg(a_sf);
         b_sf += a.ldb;
-        a_sf += C::WGRAD ? a.F : a.a_sk;
+        a_sf += a.a_sk;
       };
       float2 acc[C::CW / 2];
 #pragma unroll
@@ -283,10 +241,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
         const uint32_t b = it % C::NACC;
         float* const mine = my_scale + (kb & 1) * C::CW;
 #pragma unroll
-        for (int j = 0; j < C::NCH; ++j) mine[32 * j] = C::WGRAD ? s0.b[j] : s0.b[j] * s0.a[0];
-        float sa[NA];
-#pragma unroll
-        for (int v = 0; v < NA; ++v) sa[v] = s0.a[v];
+        for (int j = 0; j < C::NCH; ++j) mine[32 * j] = s0.b[j] * s0.a;
         s0 = s1;
         load(kb + 2, s1);
         if (!wait_warp(&acc_full[b], (it / C::NACC) & 1u, budget, a.err, abort_flag)) {
@@ -318,12 +273,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
 #pragma unroll
             for (int h = 0; h < 4; ++h) {  // features lane / 4 + 8 h
               const uint32_t* v = r[i] + (h >> 1) * 16 + 4 * g + (h & 1) * 2;
-              float2 x0 = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-              float2 x1 = make_float2(__uint_as_float(v[4]), __uint_as_float(v[5]));
-              if constexpr (C::WGRAD) {
-                x0 = __fmul2_rn(x0, make_float2(sa[h], sa[h]));
-                x1 = __fmul2_rn(x1, make_float2(sa[h], sa[h]));
-              }
+              const float2 x0 = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+              const float2 x1 = make_float2(__uint_as_float(v[4]), __uint_as_float(v[5]));
               float2* d = acc + (4 * i + h) * 4 + g;
               d[0] = __ffma2_rn(x0, make_float2(sv.x, sv.y), d[0]);
               d[1] = __ffma2_rn(x1, make_float2(sv.z, sv.w), d[1]);
@@ -332,7 +283,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
         }
       }
       if (!ok) break;
-      const long long row0 = C::WGRAD ? static_cast<long long>(wk.e) * a.C + wk.c0 : wk.c0;
 #pragma unroll
       for (int i = 0; i < C::NCH; ++i) {
         if (i >= nch) continue;
@@ -342,9 +292,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const float2 d = acc[(4 * i + h) * 4 + g];
-            if (C::WGRAD || a.f32) {
+            if (a.f32) {
               const int f = f0 + 8 * h + (lane >> 2), cc = c + 2 * (lane & 3);
-              float* o = static_cast<float*>(a.out) + (row0 + cc) * a.F + f;
+              float* o = static_cast<float*>(a.out) + static_cast<long long>(wk.c0 + cc) * a.F + f;
               if (f < a.F && cc < wk.n) o[0] = d.x;
               if (f < a.F && cc + 1 < wk.n) o[a.F] = d.y;
             } else {
@@ -353,7 +303,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
               const uint32_t u = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p));
               const int f = f0 + 8 * h + 2 * (lane & 3), cc = c + (lane >> 2);
               if (f < a.F && cc < wk.n)
-                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row0 + cc) * a.F + f) = u;
+                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(wk.c0 + cc) * a.F + f) = u;
             }
           }
         }
@@ -380,25 +330,16 @@ static cudaError_t launch_cfg(const Fp8Maps& maps, const Fp8Args& a, int sms, cu
     set[dev] = true;
   }
   // no more CTAs than there can be items
-  const long long units = C::WGRAD ? static_cast<long long>(a.E) * a.CT
-                                   : static_cast<long long>(a.M) / C::BN + (a.M < a.E ? a.M : a.E);
+  const long long units = static_cast<long long>(a.M) / C::BN + (a.M < a.E ? a.M : a.E);
   const long long items = units * a.FT;
   return launch_chained(fp8_gemm_kernel<C>, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(C::THREADS),
                         C::SMEM, st, true, maps, a);
 }
 
-template <Fp8Kind KIND>
-static cudaError_t launch_rows(const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
-  return fp8_tile_columns(a.M, a.E) == 32 ? launch_cfg<Fp8Cfg<KIND, 32>>(maps, a, sms, st)
-                                          : launch_cfg<Fp8Cfg<KIND, 128>>(maps, a, sms, st);
-}
-
-cudaError_t launch_fp8_gemm(Fp8Kind kind, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
-  switch (kind) {
-    case FP8_WEIGHT_GRAD: return launch_cfg<Fp8Cfg<FP8_WEIGHT_GRAD, kWeightGradColumns>>(maps, a, sms, st);
-    case FP8_ROWS_GRAD: return launch_rows<FP8_ROWS_GRAD>(maps, a, sms, st);
-    default: return launch_rows<FP8_ROWS>(maps, a, sms, st);
-  }
+cudaError_t launch_fp8_gemm(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
+  if (fp8_tile_columns(a.M, a.E) == 32)
+    return back ? launch_cfg<Fp8Cfg<true, 32>>(maps, a, sms, st) : launch_cfg<Fp8Cfg<false, 32>>(maps, a, sms, st);
+  return back ? launch_cfg<Fp8Cfg<true, 128>>(maps, a, sms, st) : launch_cfg<Fp8Cfg<false, 128>>(maps, a, sms, st);
 }
 
 }  // namespace kmoe

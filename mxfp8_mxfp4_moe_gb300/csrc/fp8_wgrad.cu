@@ -1,0 +1,291 @@
+// The weights' gradient of the block-scaled products, dense or by expert:
+//
+//   dw[e, n, k] = sum over e's blocks b of 128 rows:
+//                   sy[b, n] sx[b, k] sum_{m in b} dy[m, n] x[m, k]
+//
+// Both scales are powers of two (kmoe_quantize_fp8_cols writes no others), so
+// the tensor core applies them (tcgen05.mma kind::mxf8f6f4, one UE8M0 scale for
+// 32 of the sum, the same four times) and all of an expert's blocks add up in
+// one TMEM accumulator: no pass over the accumulator for each block.  A scale
+// that is no power of two makes its row or column NaN.
+//
+// A tile is 128 features k (the MMA's M) x 240 features n; both operands are
+// read as they lie in memory, MN-major.  Two accumulators: a tile's stores
+// overlap the next one's products.  An expert has few blocks (1024 rows are
+// eight), so the fp32 stores weigh as much as the products.
+//
+// The scales of four blocks are one 32-bit word a feature; warp 2 gathers them
+// into the 32 x 16 byte order that tcgen05.cp copies into TMEM, and a block's
+// MMAs select their byte.
+//
+// Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues),
+// warp 2 the scales, warps 4 .. 11 the stores.  Every wait is bounded.
+#include "fp8_dev.cuh"
+
+namespace kmoe {
+
+struct WgradCfg {
+  static constexpr int BN = kWeightGradColumns;
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = 2 * 128 * 128;  // whole 128-column boxes
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 4;
+  static constexpr int CTRL_WARPS = 4, EPI_WARPS = 8;
+  static constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
+  static constexpr int NACC = 2;
+  static constexpr int SF_SLOTS = 3;        // of four blocks' scales in shared memory
+  static constexpr int SF_BYTES = 3 * 512;  // 128 features k, 256 features n
+  static constexpr int SF_COL = NACC * BN;  // in TMEM: two slots of 12 columns
+  static constexpr int SF_OFF = STAGES * STAGE;
+  static constexpr int BAR_OFF = SF_OFF + SF_SLOTS * SF_BYTES;
+  static constexpr int TAB_OFF = BAR_OFF + 256;
+  static constexpr int TAB_INTS = kMaxE + 1;
+  static constexpr int SMEM = 1024 + TAB_OFF + (2 * TAB_INTS + 40) * 4;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(SF_COL + 24 <= 512, "TMEM columns");
+  static_assert((2 * STAGES + 2 * NACC + 2 * SF_SLOTS + 1) * 8 + 8 <= 256, "barriers");
+};
+
+__device__ __forceinline__ Fp8Item wgrad_item(const Fp8Args& a, const int32_t* unit, int w) {
+  Fp8Item it;
+  const int per = a.FT * a.CT;
+  it.e = w / per;
+  const int r = w - it.e * per;
+  it.f0 = r / a.CT * 128;
+  it.c0 = r % a.CT * WgradCfg::BN;
+  it.n = min(WgradCfg::BN, a.C - it.c0);
+  it.kb = min(unit[it.e], a.KB);
+  it.kn = min(unit[it.e + 1], a.KB) - it.kb;
+  return it;
+}
+
+// The UE8M0 byte of a scale: its exponent, NaN for anything but a normal power of two.
+__device__ __forceinline__ uint32_t ue8m0_of(float s) {
+  const uint32_t u = __float_as_uint(s), e = u >> 23;
+  return (u & 0x807FFFFFu) != 0u || e == 0u ? 0xFFu : e;
+}
+
+__global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const __grid_constant__ Fp8Maps maps,
+                                                                        const Fp8Args a) {
+  using C = WgradCfg;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + C::NACC;
+  uint64_t* sf_full = acc_empty + C::NACC;
+  uint64_t* sf_empty = sf_full + C::SF_SLOTS;
+  uint64_t* done = sf_empty + C::SF_SLOTS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* first = reinterpret_cast<int32_t*>(smem + C::TAB_OFF);
+  int32_t* unit = first + C::TAB_INTS;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < C::NACC; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], C::EPI_WARPS);
+    }
+    for (int s = 0; s < C::SF_SLOTS; ++s) {
+      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  chain_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;  // long before any wait can give up
+  tc_fence_before();
+  segment_prefix(a.seg, a.E, a.M, kScaleBlock, first, unit, unit + C::TAB_INTS);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int total = a.E * a.FT * a.CT;
+  const uint64_t budget = a.budget_ns;
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- loads
+    const uint64_t pol = policy_evict_last();
+    uint32_t it = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+      const Fp8Item wk = wgrad_item(a, unit, w);
+      const int boxes = wk.n > 128 ? 2 : 1;
+      const uint32_t tx = C::A_BYTES + boxes * 16384;
+      for (int kb = 0; kb < wk.kn; ++kb, ++it) {
+        const int s = it % C::STAGES;
+        if (!wait_warp(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, budget, a.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + s * C::STAGE;
+        const int k0 = (wk.kb + kb) * kScaleBlock;
+        mbar_arrive_expect_tx_el(&full[s], tx);
+        tma_load_2d_el(sa, &maps.a, &full[s], wk.f0, k0, pol);
+        for (int i = 0; i < boxes; ++i)
+          tma_load_2d_el(sa + C::A_BYTES + i * 16384, &maps.b, &full[s], wk.c0 + i * 128, k0, pol);
+      }
+    }
+    if (!ok) {
+      // let the copies already issued land before the CTA can exit
+      const uint32_t from = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
+      for (uint32_t i = from; i < it; ++i)
+        mbar_wait_warp(&full[i % C::STAGES], (i / C::STAGES) & 1u, 20000000ull, nullptr, nullptr);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMA
+    // 32 of the sum are 32 rows of 128 bytes of an MN-major operand (8-row
+    // groups 1024 bytes apart, the next 128 columns 16 KB on).
+    const uint64_t adesc0 = make_sdesc(smem_u32(smem), 16384, 1024, 2);
+    const uint64_t bdesc0 = make_sdesc(smem_u32(smem + C::A_BYTES), 16384, 1024, 2);
+    const uint64_t sfdesc0 = sdesc_sf_32x16(smem_u32(smem + C::SF_OFF));
+    uint32_t it = 0, li = 0, grp = 0;  // blocks, items with rows, groups of four blocks
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+      const Fp8Item wk = wgrad_item(a, unit, w);
+      if (wk.kn <= 0) continue;
+      const uint32_t b = li % C::NACC;
+      if (!wait_warp(&acc_empty[b], ((li / C::NACC) & 1u) ^ 1u, budget, a.err, abort_flag)) break;
+      ++li;
+      const uint32_t d = tmem + b * C::BN;
+      const uint32_t idesc =
+          idesc_mxf8f6f4(128, (wk.n + 15) & ~15, MX_E4M3, MX_E4M3, 0, 0) | (1u << 15) | (1u << 16);
+      for (int kb = 0; kb < wk.kn; ++kb, ++it) {
+        const uint32_t sf = tmem + C::SF_COL + (grp & 1u) * 12;
+        if ((kb & 3) == 0) {
+          const uint32_t sl = grp % C::SF_SLOTS;
+          if (!wait_warp(&sf_full[sl], (grp / C::SF_SLOTS) & 1u, budget, a.err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t sd = sfdesc0 + sl * (C::SF_BYTES >> 4);
+          tc_cp_32x128b_warpx4_el(sf, sd);
+          tc_cp_32x128b_warpx4_el(sf + 4, sd + 32);
+          if (wk.n > 128) tc_cp_32x128b_warpx4_el(sf + 8, sd + 64);
+          tc_commit_el(&sf_empty[sl]);
+        }
+        const int s = it % C::STAGES;
+        if (!wait_warp(&full[s], (it / C::STAGES) & 1u, budget, a.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t so = static_cast<uint64_t>(s) * (C::STAGE >> 4);
+        const uint32_t id = idesc | (static_cast<uint32_t>(kb & 3) << 4) | (static_cast<uint32_t>(kb & 3) << 29);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mma_mxf8f6f4_el(d, adesc0 + so + i * 256, bdesc0 + so + i * 256, id, sf, sf + 4, (kb | i) != 0);
+        tc_commit_el(&empty[s]);
+        if ((kb & 3) == 3 || kb == wk.kn - 1) ++grp;
+      }
+      if (!ok) break;
+      tc_commit_el(&acc_full[b]);
+    }
+    tc_commit_el(done);
+    mbar_wait_warp(done, 0, budget, a.err, nullptr);
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- scales
+    uint32_t grp = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+      const Fp8Item wk = wgrad_item(a, unit, w);
+      for (int kb = 0; kb < wk.kn; kb += 4, ++grp) {
+        // features 32 j + lane: four of k, then eight of n; past an edge the last
+        // one's (no product that is stored uses those), all loads in flight at once
+        const int last = min(4, wk.kn - kb) - 1;
+        const long long b0 = wk.kb + kb;
+        float v[12][4];
+#pragma unroll
+        for (int j = 0; j < 12; ++j) {
+          const int at = j < 4 ? min(wk.f0 + 32 * j + lane, a.F - 1) : wk.c0 + min(32 * (j - 4) + lane, wk.n - 1);
+          const float* src = j < 4 ? a.a_sf : a.b_sf;
+          const int cols = j < 4 ? a.F : a.C;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[j][i] = __ldg(src + (b0 + min(i, last)) * cols + at);
+        }
+        const uint32_t sl = grp % C::SF_SLOTS;
+        if (!wait_warp(&sf_empty[sl], ((grp / C::SF_SLOTS) & 1u) ^ 1u, budget, a.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = smem + C::SF_OFF + sl * C::SF_BYTES + lane * 16;
+#pragma unroll
+        for (int j = 0; j < 12; ++j)
+          *reinterpret_cast<uint32_t*>(dst + (j >> 2) * 512 + (j & 3) * 4) =
+              ue8m0_of(v[j][0]) | ue8m0_of(v[j][1]) << 8 | ue8m0_of(v[j][2]) << 16 | ue8m0_of(v[j][3]) << 24;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sf_full[sl]);
+      }
+    }
+  } else if (warp >= C::CTRL_WARPS) {
+    // -------------------------------------------------------------- stores
+    const int q = warp & 3;
+    const int half = (warp - C::CTRL_WARPS) >> 2;  // of the tile's 16-column chunks, in turn
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    uint32_t li = 0;
+    for (int w = blockIdx.x; w < total; w += gridDim.x) {
+      const Fp8Item wk = wgrad_item(a, unit, w);
+      const int f = wk.f0 + q * 32 + lane;
+      float* out = static_cast<float*>(a.out) + (static_cast<long long>(wk.e) * a.C + wk.c0) * a.F + f;
+      if (wk.kn <= 0) {  // no rows: zeros
+        if (f < a.F)
+          for (int c = half; c < wk.n; c += 2) __stcs(out + static_cast<long long>(c) * a.F, 0.f);
+        continue;
+      }
+      const uint32_t b = li % C::NACC;
+      if (!wait_warp(&acc_full[b], (li / C::NACC) & 1u, budget, a.err, abort_flag)) break;
+      ++li;
+      tc_fence_after();
+      const uint32_t t = tmem + lanes + b * C::BN;
+      for (int c = 16 * half; c < wk.n; c += 32) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(t + c, r);
+        tmem_ld_wait_for16(r);
+        // (n is a multiple of 16) 32 features of one n a store
+        if (f < a.F)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) __stcs(out + static_cast<long long>(c + j) * a.F, __uint_as_float(r[j]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[b]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+cudaError_t launch_fp8_wgrad(const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
+  static bool set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!set[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(fp8_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WgradCfg::SMEM);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
+  }
+  const long long items = static_cast<long long>(a.E) * a.FT * a.CT;
+  return launch_chained(fp8_wgrad_kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)),
+                        dim3(WgradCfg::THREADS), WgradCfg::SMEM, st, true, maps, a);
+}
+
+}  // namespace kmoe
