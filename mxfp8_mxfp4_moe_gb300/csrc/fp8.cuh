@@ -40,8 +40,8 @@ constexpr int fp8_box_rows(int tile_columns) { return tile_columns == 0 ? 128 : 
 
 cudaError_t launch_fp8_gemm(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
 cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
-constexpr int kWeightGradColumns = 240;  // n of a tile of the weights' gradient
-cudaError_t launch_fp8_wgrad(const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
+constexpr int kWeightGradColumns = 224;  // n of a tile of the weights' gradient
+cudaError_t launch_fp8_wgrad(const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st);
 
 cudaError_t launch_fp8_quant_rows(const void* x, int rows, int cols, uint8_t* codes, float* scales, cudaStream_t st);
 cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, const int32_t* row_of_slot, uint8_t* codes,

@@ -9,30 +9,35 @@
 // one TMEM accumulator: no pass over the accumulator for each block.  A scale
 // that is no power of two makes its row or column NaN.
 //
-// A tile is 128 features k (the MMA's M) x 240 features n; both operands are
-// read as they lie in memory, MN-major.  Two accumulators: a tile's stores
-// overlap the next one's products.  An expert has few blocks (1024 rows are
-// eight), so the fp32 stores weigh as much as the products.
+// A cluster of two CTAs computes a tile of 256 features k (the MMA's M, 128 a
+// CTA) x 224 features n with tcgen05.mma.cta_group::2: each CTA loads its
+// features k and half of the features n, and holds the accumulator of its
+// features k.  Both operands are read as they lie in memory, MN-major.  Two
+// accumulators: a tile's stores overlap the next one's products.  An expert has
+// few blocks (1024 rows are eight), so the fp32 stores weigh as much as the
+// products.
 //
-// The scales of four blocks are one 32-bit word a feature; warp 2 gathers them
-// into the 32 x 16 byte order that tcgen05.cp copies into TMEM, and a block's
-// MMAs select their byte.
+// The scales of four blocks are one 32-bit word a feature; warps 2 and 3 gather
+// them into the 32 x 16 byte order that tcgen05.cp copies into TMEM (each CTA its
+// own features k and all n), and a block's MMAs select their byte.
 //
-// Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues),
-// warp 2 the scales, warps 4 .. 11 the stores.  Every wait is bounded.
+// Roles in each CTA: warp 0 TMA, warp 1 MMA (the even CTA's, for both), warps 2
+// and 3 the scales, warps 4 .. 11 the stores.  Loads complete on the even CTA's
+// barriers, commits arrive at both CTAs'.  Every wait is bounded.
 #include "fp8_dev.cuh"
 
 namespace kmoe {
 
 struct WgradCfg {
   static constexpr int BN = kWeightGradColumns;
-  static constexpr int A_BYTES = 128 * 128, B_BYTES = 2 * 128 * 128;  // whole 128-column boxes
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 4;
+  static constexpr int KPS = 2;  // blocks a stage
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // a block's 128 features k, and a box of n
+  static constexpr int STAGE = KPS * (A_BYTES + B_BYTES);
+  static constexpr int STAGES = 192 * 1024 / STAGE;
   static constexpr int CTRL_WARPS = 4, EPI_WARPS = 8;
   static constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
   static constexpr int NACC = 2;
-  static constexpr int SF_SLOTS = 3;        // of four blocks' scales in shared memory
+  static constexpr int SF_SLOTS = 4;        // of four blocks' scales in shared memory
   static constexpr int SF_BYTES = 3 * 512;  // 128 features k, 256 features n
   static constexpr int SF_COL = NACC * BN;  // in TMEM: two slots of 12 columns
   static constexpr int SF_OFF = STAGES * STAGE;
@@ -50,13 +55,16 @@ __device__ __forceinline__ Fp8Item wgrad_item(const Fp8Args& a, const int32_t* u
   const int per = a.FT * a.CT;
   it.e = w / per;
   const int r = w - it.e * per;
-  it.f0 = r / a.CT * 128;
-  it.c0 = r % a.CT * WgradCfg::BN;
+  it.f0 = r % a.FT * 256;
+  it.c0 = r / a.FT * WgradCfg::BN;
   it.n = min(WgradCfg::BN, a.C - it.c0);
   it.kb = min(unit[it.e], a.KB);
   it.kn = min(unit[it.e + 1], a.KB) - it.kb;
   return it;
 }
+
+// Columns that each CTA of a pair loads and multiplies for a tile of n.
+__device__ __forceinline__ int wgrad_half(int n) { return (n + 31) / 32 * 16; }
 
 // The UE8M0 byte of a scale: its exponent, NaN for anything but a normal power of two.
 __device__ __forceinline__ uint32_t ue8m0_of(float s) {
@@ -83,6 +91,8 @@ __global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const _
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool lead = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -90,10 +100,10 @@ __global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const _
     }
     for (int b = 0; b < C::NACC; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], C::EPI_WARPS);
+      mbar_init(&acc_empty[b], 2 * C::EPI_WARPS);  // of both CTAs
     }
     for (int s = 0; s < C::SF_SLOTS; ++s) {
-      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_full[s], 2);  // both CTAs' scales
       mbar_init(&sf_empty[s], 1);
     }
     mbar_init(done, 1);
@@ -103,106 +113,124 @@ __global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const _
     prefetch_tmap(&maps.b);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
   }
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;  // long before any wait can give up
   tc_fence_before();
   segment_prefix(a.seg, a.E, a.M, kScaleBlock, first, unit, unit + C::TAB_INTS);
+  cluster_sync();  // both CTAs' barriers and TMEM are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = a.E * a.FT * a.CT;
+  const int w0 = blockIdx.x >> 1, dw = gridDim.x >> 1;
   const uint64_t budget = a.budget_ns;
 
   if (warp == 0) {
     // -------------------------------------------------------------- loads
     const uint64_t pol = policy_evict_last();
+    const uint32_t lead_full = cluster_map(full, 0);
     uint32_t it = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+    for (int w = w0; ok && w < total; w += dw) {
       const Fp8Item wk = wgrad_item(a, unit, w);
-      const int boxes = wk.n > 128 ? 2 : 1;
-      const uint32_t tx = C::A_BYTES + boxes * 16384;
-      for (int kb = 0; kb < wk.kn; ++kb, ++it) {
+      // this CTA's half of the MMA's columns starts on a multiple of 16 bytes
+      const int c0 = wk.c0 + rank * wgrad_half(wk.n), f0 = wk.f0 + rank * 128;
+      for (int kb = 0; kb < wk.kn; kb += C::KPS, ++it) {
         const int s = it % C::STAGES;
         if (!wait_warp(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, budget, a.err, abort_flag)) {
           ok = false;
           break;
         }
-        uint8_t* sa = smem + s * C::STAGE;
-        const int k0 = (wk.kb + kb) * kScaleBlock;
-        mbar_arrive_expect_tx_el(&full[s], tx);
-        tma_load_2d_el(sa, &maps.a, &full[s], wk.f0, k0, pol);
-        for (int i = 0; i < boxes; ++i)
-          tma_load_2d_el(sa + C::A_BYTES + i * 16384, &maps.b, &full[s], wk.c0 + i * 128, k0, pol);
+        const int blocks = min(C::KPS, wk.kn - kb);
+        uint8_t* st = smem + s * C::STAGE;
+        if (lead) mbar_arrive_expect_tx_el(&full[s], 2u * blocks * (C::A_BYTES + C::B_BYTES));
+        for (int i = 0; i < blocks; ++i) {
+          const int k0 = (wk.kb + kb + i) * kScaleBlock;
+          tma_load_2d_pair_el(st + i * C::A_BYTES, &maps.a, lead_full + 8u * s, f0, k0, pol);
+          tma_load_2d_pair_el(st + C::KPS * C::A_BYTES + i * C::B_BYTES, &maps.b, lead_full + 8u * s, c0, k0, pol);
+        }
       }
     }
     if (!ok) {
       // let the copies already issued land before the CTA can exit
-      const uint32_t from = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
-      for (uint32_t i = from; i < it; ++i)
-        mbar_wait_warp(&full[i % C::STAGES], (i / C::STAGES) & 1u, 20000000ull, nullptr, nullptr);
+      if (lead) {
+        const uint32_t from = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
+        for (uint32_t i = from; i < it; ++i)
+          mbar_wait_warp(&full[i % C::STAGES], (i / C::STAGES) & 1u, 20000000ull, nullptr, nullptr);
+      } else {
+        spin_ns(100000ull);
+      }
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA
-    // 32 of the sum are 32 rows of 128 bytes of an MN-major operand (8-row
-    // groups 1024 bytes apart, the next 128 columns 16 KB on).
-    const uint64_t adesc0 = make_sdesc(smem_u32(smem), 16384, 1024, 2);
-    const uint64_t bdesc0 = make_sdesc(smem_u32(smem + C::A_BYTES), 16384, 1024, 2);
-    const uint64_t sfdesc0 = sdesc_sf_32x16(smem_u32(smem + C::SF_OFF));
-    uint32_t it = 0, li = 0, grp = 0;  // blocks, items with rows, groups of four blocks
-    bool ok = true;
-    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-      const Fp8Item wk = wgrad_item(a, unit, w);
-      if (wk.kn <= 0) continue;
-      const uint32_t b = li % C::NACC;
-      if (!wait_warp(&acc_empty[b], ((li / C::NACC) & 1u) ^ 1u, budget, a.err, abort_flag)) break;
-      ++li;
-      const uint32_t d = tmem + b * C::BN;
-      const uint32_t idesc =
-          idesc_mxf8f6f4(128, (wk.n + 15) & ~15, MX_E4M3, MX_E4M3, 0, 0) | (1u << 15) | (1u << 16);
-      for (int kb = 0; kb < wk.kn; ++kb, ++it) {
-        const uint32_t sf = tmem + C::SF_COL + (grp & 1u) * 12;
-        if ((kb & 3) == 0) {
-          const uint32_t sl = grp % C::SF_SLOTS;
-          if (!wait_warp(&sf_full[sl], (grp / C::SF_SLOTS) & 1u, budget, a.err, abort_flag)) {
+    if (lead) {
+      // 32 of the sum are 32 rows of 128 bytes of an MN-major operand (8-row
+      // groups 1024 bytes apart).
+      const uint64_t adesc0 = make_sdesc(smem_u32(smem), 16384, 1024, 2);
+      const uint64_t bdesc0 = make_sdesc(smem_u32(smem + C::KPS * C::A_BYTES), 16384, 1024, 2);
+      const uint64_t sfdesc0 = sdesc_sf_32x16(smem_u32(smem + C::SF_OFF));
+      uint32_t it = 0, li = 0, grp = 0;  // stages, items with rows, groups of four blocks
+      bool ok = true;
+      for (int w = w0; ok && w < total; w += dw) {
+        const Fp8Item wk = wgrad_item(a, unit, w);
+        if (wk.kn <= 0) continue;
+        const uint32_t b = li % C::NACC;
+        if (!mbar_wait_warp<true>(&acc_empty[b], ((li / C::NACC) & 1u) ^ 1u, budget, a.err, abort_flag)) break;
+        ++li;
+        const uint32_t d = tmem + b * C::BN;
+        const int nmma = 2 * wgrad_half(wk.n);
+        const uint32_t idesc = idesc_mxf8f6f4(256, nmma, MX_E4M3, MX_E4M3, 0, 0) | (1u << 15) | (1u << 16);
+        for (int kb = 0; kb < wk.kn; kb += C::KPS, ++it) {
+          const int s = it % C::STAGES;
+          if (!wait_warp(&full[s], (it / C::STAGES) & 1u, budget, a.err, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t sd = sfdesc0 + sl * (C::SF_BYTES >> 4);
-          tc_cp_32x128b_warpx4_el(sf, sd);
-          tc_cp_32x128b_warpx4_el(sf + 4, sd + 32);
-          if (wk.n > 128) tc_cp_32x128b_warpx4_el(sf + 8, sd + 64);
-          tc_commit_el(&sf_empty[sl]);
-        }
-        const int s = it % C::STAGES;
-        if (!wait_warp(&full[s], (it / C::STAGES) & 1u, budget, a.err, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t so = static_cast<uint64_t>(s) * (C::STAGE >> 4);
-        const uint32_t id = idesc | (static_cast<uint32_t>(kb & 3) << 4) | (static_cast<uint32_t>(kb & 3) << 29);
+          const int blocks = min(C::KPS, wk.kn - kb);
+          for (int i = 0; ok && i < blocks; ++i) {
+            const int k = kb + i;
+            const uint32_t sf = tmem + C::SF_COL + (grp & 1u) * 12;
+            if ((k & 3) == 0) {
+              const uint32_t sl = grp % C::SF_SLOTS;
+              ok = mbar_wait_warp<true>(&sf_full[sl], (grp / C::SF_SLOTS) & 1u, budget, a.err, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t sd = sfdesc0 + sl * (C::SF_BYTES >> 4);
+              tc_cp_32x128b_warpx4_pair_el(sf, sd);
+              tc_cp_32x128b_warpx4_pair_el(sf + 4, sd + 32);
+              if (nmma > 128) tc_cp_32x128b_warpx4_pair_el(sf + 8, sd + 64);
+              tc_commit_pair_el(&sf_empty[sl]);
+            }
+            const uint64_t ad = adesc0 + static_cast<uint64_t>(s) * (C::STAGE >> 4) + i * (C::A_BYTES >> 4);
+            const uint64_t bd = bdesc0 + static_cast<uint64_t>(s) * (C::STAGE >> 4) + i * (C::B_BYTES >> 4);
+            const uint32_t id = idesc | (static_cast<uint32_t>(k & 3) << 4) | (static_cast<uint32_t>(k & 3) << 29);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma_mxf8f6f4_el(d, adesc0 + so + i * 256, bdesc0 + so + i * 256, id, sf, sf + 4, (kb | i) != 0);
-        tc_commit_el(&empty[s]);
-        if ((kb & 3) == 3 || kb == wk.kn - 1) ++grp;
+            for (int j = 0; j < 4; ++j)
+              mma_mxf8f6f4_pair_el(d, ad + j * 256, bd + j * 256, id, sf, sf + 4, (k | j) != 0);
+            if ((k & 3) == 3 || k == wk.kn - 1) ++grp;
+          }
+          if (!ok) break;
+          tc_commit_pair_el(&empty[s]);
+        }
+        if (!ok) break;
+        tc_commit_pair_el(&acc_full[b]);
       }
-      if (!ok) break;
-      tc_commit_el(&acc_full[b]);
+      tc_commit_pair_el(done);
+      mbar_wait_warp(done, 0, budget, a.err, nullptr);
     }
-    tc_commit_el(done);
-    mbar_wait_warp(done, 0, budget, a.err, nullptr);
-  } else if (warp == 2) {
+  } else if (warp < C::CTRL_WARPS) {
     // -------------------------------------------------------------- scales
+    // (groups of four blocks by the two warps in turn)
+    const uint32_t lead_sf_full = cluster_map(sf_full, 0);
     uint32_t grp = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
+    for (int w = w0; ok && w < total; w += dw) {
       const Fp8Item wk = wgrad_item(a, unit, w);
       for (int kb = 0; kb < wk.kn; kb += 4, ++grp) {
+        if ((grp & 1u) != (warp & 1u)) continue;
         // features 32 j + lane: four of k, then eight of n; past an edge the last
         // one's (no product that is stored uses those), all loads in flight at once
         const int last = min(4, wk.kn - kb) - 1;
@@ -210,7 +238,7 @@ __global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const _
         float v[12][4];
 #pragma unroll
         for (int j = 0; j < 12; ++j) {
-          const int at = j < 4 ? min(wk.f0 + 32 * j + lane, a.F - 1) : wk.c0 + min(32 * (j - 4) + lane, wk.n - 1);
+          const int at = j < 4 ? min(wk.f0 + rank * 128 + 32 * j + lane, a.F - 1) : wk.c0 + min(32 * (j - 4) + lane, wk.n - 1);
           const float* src = j < 4 ? a.a_sf : a.b_sf;
           const int cols = j < 4 ? a.F : a.C;
 #pragma unroll
@@ -228,7 +256,12 @@ __global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const _
               ue8m0_of(v[j][0]) | ue8m0_of(v[j][1]) << 8 | ue8m0_of(v[j][2]) << 16 | ue8m0_of(v[j][3]) << 24;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_full[sl]);
+        if (lane == 0) {
+          if (lead)
+            mbar_arrive(&sf_full[sl]);
+          else
+            mbar_arrive_remote(lead_sf_full + 8u * sl);
+        }
       }
     }
   } else if (warp >= C::CTRL_WARPS) {
@@ -236,10 +269,11 @@ __global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const _
     const int q = warp & 3;
     const int half = (warp - C::CTRL_WARPS) >> 2;  // of the tile's 16-column chunks, in turn
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t lead_acc_empty = cluster_map(acc_empty, 0);
     uint32_t li = 0;
-    for (int w = blockIdx.x; w < total; w += gridDim.x) {
+    for (int w = w0; w < total; w += dw) {
       const Fp8Item wk = wgrad_item(a, unit, w);
-      const int f = wk.f0 + q * 32 + lane;
+      const int f = wk.f0 + rank * 128 + q * 32 + lane;
       float* out = static_cast<float*>(a.out) + (static_cast<long long>(wk.e) * a.C + wk.c0) * a.F + f;
       if (wk.kn <= 0) {  // no rows: zeros
         if (f < a.F)
@@ -262,30 +296,57 @@ __global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const _
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[b]);
+      if (lane == 0) {
+        if (lead)
+          mbar_arrive(&acc_empty[b]);
+        else
+          mbar_arrive_remote(lead_acc_empty + 8u * b);
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // no MMA of the pair and no remote arrive is outstanding past here
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
-cudaError_t launch_fp8_wgrad(const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
-  static bool set[kMaxDevices] = {};
+cudaError_t launch_fp8_wgrad(const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st) {
+  static int pairs_of[kMaxDevices] = {};  // co-resident clusters of two, per device
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
-  if (!set[dev]) {
-    const cudaError_t e =
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see chain_wait
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(2 * (sms / 2));
+  cfg.blockDim = dim3(WgradCfg::THREADS);
+  cfg.dynamicSmemBytes = WgradCfg::SMEM;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int& pairs = pairs_of[dev];
+  if (pairs == 0) {
+    cudaError_t e =
         cudaFuncSetAttribute(fp8_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WgradCfg::SMEM);
     if (e != cudaSuccess) return e;
-    set[dev] = true;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, fp8_wgrad_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n <= 0) return cudaErrorInvalidConfiguration;
+    pairs = n < sms / 2 ? n : sms / 2;
   }
+  a.FT = (a.F + 255) / 256;
   const long long items = static_cast<long long>(a.E) * a.FT * a.CT;
-  return launch_chained(fp8_wgrad_kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)),
-                        dim3(WgradCfg::THREADS), WgradCfg::SMEM, st, true, maps, a);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs)));
+  cfg.stream = st;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, fp8_wgrad_kernel, maps, a);
 }
 
 }  // namespace kmoe
