@@ -27,6 +27,7 @@ struct Fp8Args {
   int KB;          // blocks of the sum (weight gradient: blocks there are)
   int ldb;
   int f32;         // out is fp32, else bf16
+  int split;       // CTAs of a cluster that share an item's blocks (fp8_gemm.cu; set at the launch)
 };
 
 // The kernel for M rows of E experts, by the rows an expert has on average:
@@ -35,8 +36,9 @@ inline int fp8_tile_columns(int M, int E) {
   const int avg = (M + E - 1) / E;
   return avg <= 32 ? 32 : (avg <= 128 ? 128 : 0);
 }
-// Rows of a TMA box of such tiles.
-constexpr int fp8_box_rows(int tile_columns) { return tile_columns == 0 ? 128 : (tile_columns < 64 ? tile_columns : 64); }
+// Rows of a TMA box of such tiles: a copy takes the time of its rows, and tiles
+// are cut to multiples of 16.
+constexpr int fp8_box_rows(int tile_columns) { return tile_columns == 0 ? 128 : (tile_columns == 32 ? 8 : 32); }
 
 cudaError_t launch_fp8_gemm(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
 cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);

@@ -14,9 +14,17 @@
 // K-major; transposed weights are read as they lie in memory, MN-major
 // (128-byte swizzle either way).
 //
-// Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues),
-// the others the epilogue: groups of four warps (one per TMEM lane quarter)
-// that take the 32-column chunks in turn.  Every wait is bounded.
+// Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues), warp
+// 2 the scales (a ring in shared memory, some blocks ahead of their use: with
+// few rows a block takes less time than a read of global memory), the others
+// the epilogue: groups of four warps (one per TMEM lane quarter) that take
+// the 32-column chunks in turn.  Every wait is bounded.
+//
+// Where there are too few items for the SMs, a cluster of `split` CTAs takes
+// one item: each sums a part of the blocks, and the parts are added in order
+// through distributed shared memory, each CTA a share of the accumulators.
+#include <type_traits>
+
 #include "fp8_dev.cuh"
 
 namespace kmoe {
@@ -39,6 +47,12 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   return r;
 }
 
+__device__ __forceinline__ float2 ld_shared_cluster_f2(uint32_t cluster_addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 template <bool BACK_, int BN_>
 struct Fp8Cfg {
   static constexpr bool BACK = BACK_;  // the weights transposed, read MN-major
@@ -46,30 +60,35 @@ struct Fp8Cfg {
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int BOX = fp8_box_rows(BN);
   static constexpr int STAGE = A_BYTES + BN * 128;
-  static constexpr int STAGES = 200 * 1024 / STAGE < 10 ? 200 * 1024 / STAGE : 10;
+  // BN = 32: two CTAs fit on an SM, so that one can start while another ends
+  static constexpr int STAGES = (BN == 32 ? 100 : 200) * 1024 / STAGE;
   // an epilogue warp holds up to 64 columns of 32 features (a TMEM quarter), and
   // in as many registers the block being read
   static constexpr int CW = BN < 64 ? BN : 64;
   static constexpr int NCH = CW / 32;  // 32-column chunks
   static constexpr int NG = BN / CW;   // groups of four warps
   static constexpr int EPI_WARPS = 4 * NG;
-  static constexpr int CTRL_WARPS = 2;
+  static constexpr int CTRL_WARPS = 3;
   static constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
   static constexpr int NACC = 512 / BN < 4 ? 512 / BN : 4;
   static constexpr int TMEM_COLS = BN * NACC <= 128 ? 128 : 512;
+  // ring of scales: a block's BN rows and its features'
+  static constexpr int RING = 16, AHEAD = RING - NACC - 1;  // slots, and blocks loaded ahead
+  static constexpr int SLOT = BN + 4;                       // floats
   static constexpr int SC_OFF = STAGES * STAGE;
-  static constexpr int SC_BYTES = EPI_WARPS * 2 * CW * 4;
-  static constexpr int BAR_OFF = SC_OFF + SC_BYTES;
+  static constexpr int BAR_OFF = SC_OFF + RING * SLOT * 4;
   static constexpr int TAB_OFF = BAR_OFF + 256;
   static constexpr int TAB_INTS = kMaxE + 1;
   static constexpr int SMEM = 1024 + TAB_OFF + (2 * TAB_INTS + 40) * 4;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert((2 * STAGES + 2 * NACC + 1) * 8 + 8 <= 256, "barriers");
   static_assert(BN * NACC <= TMEM_COLS, "TMEM columns");
+  static_assert(EPI_WARPS * 32 * CW * 4 <= STAGES * STAGE, "a cluster's parts go where the stages were");
 };
 
 template <class C>
-__device__ __forceinline__ Fp8Item fp8_item(const Fp8Args& a, const int32_t* first, const int32_t* unit, int w) {
+__device__ __forceinline__ Fp8Item fp8_item(const Fp8Args& a, const int32_t* first, const int32_t* unit, int w,
+                                            int rank) {
   Fp8Item it;
   it.e = segment_of_unit(unit, a.E, w / a.FT);
   const int u0 = unit[it.e], nt = unit[it.e + 1] - u0;
@@ -81,13 +100,14 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8Args& a, const int32_t* fir
   const int at = r % nt * per;
   it.c0 = first[it.e] + at;
   it.n = min(per, rows - at);
-  it.kb = 0;
-  it.kn = a.KB;
+  const int per_cta = (a.KB + a.split - 1) / a.split;
+  it.kb = min(rank * per_cta, a.KB);
+  it.kn = min(per_cta, a.KB - it.kb);
   return it;
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps,
+__global__ void __launch_bounds__(C::THREADS, C::BN == 32 ? 2 : 1) fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps,
                                                                 const Fp8Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -103,13 +123,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());  // 0 without a cluster
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < C::NACC; ++b) {
-      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_full[b], 2);  // the block's products, and its scales
       mbar_init(&acc_empty[b], C::EPI_WARPS);
     }
     mbar_init(done, 1);
@@ -130,6 +151,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
   const uint32_t tmem = *tmem_slot;
   const int total = a.FT * unit[a.E];
   const uint64_t budget = a.budget_ns;
+  const int w0 = blockIdx.x / a.split, dw = gridDim.x / a.split;
 
   if (warp < C::CTRL_WARPS) {
     if (warp == 0) {
@@ -137,8 +159,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
       const uint64_t pol_a = policy_evict_normal(), pol_b = policy_evict_last();
       uint32_t it = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-        const Fp8Item wk = fp8_item<C>(a, first, unit, w);
+      for (int w = w0; ok && w < total; w += dw) {
+        const Fp8Item wk = fp8_item<C>(a, first, unit, w, rank);
         const int boxes = (wk.n + C::BOX - 1) / C::BOX;
         const uint32_t tx = C::A_BYTES + boxes * C::BOX * 128;
         for (int kb = 0; kb < wk.kn; ++kb, ++it) {
@@ -149,7 +171,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
           }
           uint8_t* sa = smem + s * C::STAGE;
           uint8_t* sb = sa + C::A_BYTES;
-          const int k0 = kb * kScaleBlock;
+          const int k0 = (wk.kb + kb) * kScaleBlock;
           mbar_arrive_expect_tx_el(&full[s], tx);
           tma_load_3d_el(sa, &maps.a, &full[s], C::BACK ? wk.f0 : k0, C::BACK ? k0 : wk.f0, wk.e, pol_a);
           for (int i = 0; i < boxes; ++i)
@@ -172,8 +194,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
       const uint64_t bdesc0 = sdesc_kmajor_sw128(smem_u32(smem + C::A_BYTES));
       uint32_t it = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-        const Fp8Item wk = fp8_item<C>(a, first, unit, w);
+      for (int w = w0; ok && w < total; w += dw) {
+        const Fp8Item wk = fp8_item<C>(a, first, unit, w, rank);
         const uint32_t idesc = idesc_f8(128, (wk.n + 15) & ~15, C::BACK, false);
         for (int kb = 0; kb < wk.kn; ++kb, ++it) {
           const int s = it % C::STAGES;
@@ -196,54 +218,81 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
       tc_commit_el(done);
       mbar_wait_warp(done, 0, budget, a.err, nullptr);
     }
+    else {
+      // ------------------------------------------------------------ scales
+      // A chunk's lie in the order in which the eight that a thread needs are
+      // two 16-byte pieces: columns 8g + 2q + {0, 1}, g even and the g after it.
+      const uint32_t ring =
+          smem_u32(smem + C::SC_OFF) +
+          ((lane >> 4) * 16 + ((lane & 7) >> 1) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1)) * 4;
+      const uint32_t ring_w = smem_u32(smem + C::SC_OFF) + C::BN * 4;
+      int w = w0 - dw, kb = 0, kn = 0, n = 0;  // the block that is loaded next
+      const float *x_sf = nullptr, *w_sf = nullptr;
+      bool more = true;
+      uint32_t issued = 0;
+      auto issue = [&] {
+        while (more && kb >= kn) {  // the next item
+          w += dw;
+          more = w < total;
+          if (more) {
+            const Fp8Item wk = fp8_item<C>(a, first, unit, w, rank);
+            kb = 0;
+            kn = wk.kn;
+            n = wk.n;
+            x_sf = a.b_sf + static_cast<long long>(wk.kb) * a.ldb + wk.c0;
+            w_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm + wk.kb * a.a_sk;
+          }
+        }
+        if (more) {
+          const uint32_t slot = (issued & (C::RING - 1)) * (C::SLOT * 4);
+#pragma unroll
+          for (int j = 0; j < C::BN / 32; ++j)
+            if (32 * j < n) cp_async4(ring + slot + j * 128, x_sf + min(32 * j + lane, n - 1));
+          if (lane == 0) cp_async4(ring_w + slot, w_sf);
+          x_sf += a.ldb;
+          w_sf += a.a_sk;
+          ++kb;
+          ++issued;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll 1
+      for (int i = 0; i < C::AHEAD; ++i) issue();
+#pragma unroll 1
+      for (uint32_t it = 0;; ++it) {
+        const uint32_t b = it % C::NACC;
+        if (it < issued && !wait_warp(&acc_empty[b], ((it / C::NACC) & 1u) ^ 1u, budget, a.err, abort_flag)) break;
+        issue();  // the slot's last block was read before the accumulator above was released
+        if (it >= issued) break;
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_full[b]);
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    if (a.split > 1) {  // (the epilogue's exchange)
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     const int ew = warp - C::CTRL_WARPS;
     const int grp = ew >> 2;
-    float* const ring = reinterpret_cast<float*>(smem + C::SC_OFF) + ew * 2 * C::CW;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
-    // A chunk's scales lie in the order in which the eight that a thread needs
-    // are two 16-byte pieces: columns 8g + 2q + {0, 1}, g even and the g after it.
-    float* const my_scale = ring + (lane >> 4) * 16 + ((lane & 7) >> 1) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1);
     uint32_t it = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-      const Fp8Item wk = fp8_item<C>(a, first, unit, w);
+    bool ok = true, exchanged = false;
+    for (int w = w0; ok && w < total; w += dw) {
+      const Fp8Item wk = fp8_item<C>(a, first, unit, w, rank);
       const int f0 = wk.f0 + q * 32;  // the warp's first feature
       // the group's 32-column chunks start at column(0), column(1)
       auto column = [&](int i) { return (i * C::NG + grp) * 32; };
       const int nch = (wk.n - grp * 32 + C::NG * 32 - 1) / (C::NG * 32);  // chunks with columns of the tile
-      const float* b_sf = a.b_sf + wk.c0 + lane;
-      const float* a_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm;
-      // a block's scales: this lane's column of each chunk (0 past the tile), and the weights'
-      struct Scales {
-        float b[C::NCH], a;
-      };
-      auto load = [&](int kb, Scales& s) {
-        if (kb >= wk.kn) return;
-#pragma unroll
-        for (int j = 0; j < C::NCH; ++j) {
-          s.b[j] = 0.f;
-          if (column(j) + lane < wk.n) s.b[j] = __ldg(b_sf + column(j));
-        }
-        s.a = __ldg(a_sf);
-        b_sf += a.ldb;
-        a_sf += a.a_sk;
-      };
       float2 acc[C::CW / 2];
 #pragma unroll
       for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      Scales s0{}, s1{};
-      load(0, s0);
-      load(1, s1);
       for (int kb = 0; kb < wk.kn; ++kb, ++it) {
         const uint32_t b = it % C::NACC;
-        float* const mine = my_scale + (kb & 1) * C::CW;
-#pragma unroll
-        for (int j = 0; j < C::NCH; ++j) mine[32 * j] = s0.b[j] * s0.a;
-        s0 = s1;
-        load(kb + 2, s1);
         if (!wait_warp(&acc_full[b], (it / C::NACC) & 1u, budget, a.err, abort_flag)) {
           ok = false;
           break;
@@ -251,63 +300,95 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
         __syncwarp();
         tc_fence_after();
         const uint32_t t = tmem + lanes + b * C::BN;
-        uint32_t r[C::NCH][32];
-#pragma unroll
-        for (int i = 0; i < C::NCH; ++i)
-          if (i < nch) {
-            tmem_ld_16x256b_x4(t + column(i), r[i]);
-            tmem_ld_16x256b_x4(t + (16u << 16) + column(i), r[i] + 16);
-          }
-#pragma unroll
-        for (int i = 0; i < C::NCH; ++i) tmem_ld_wait_for(r[i]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[b]);
-        const float* const scale = ring + (kb & 1) * C::CW + (lane & 3) * 4;
+        const float* const scale = reinterpret_cast<const float*>(smem + C::SC_OFF) + (it & (C::RING - 1)) * C::SLOT;
+        const float sw = scale[C::BN];
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+        };
 #pragma unroll
         for (int i = 0; i < C::NCH; ++i) {
           if (i >= nch) continue;
+          uint32_t r[32];
+          tmem_ld_16x256b_x4(t + column(i), r);
+          tmem_ld_16x256b_x4(t + (16u << 16) + column(i), r + 16);
+          tmem_ld_wait_for(r);
+          if (i == nch - 1) release();
 #pragma unroll
           for (int g = 0; g < 4; g += 2) {
-            const float4 sv = *reinterpret_cast<const float4*>(scale + 32 * i + 8 * g);
+            const float4 sv = *reinterpret_cast<const float4*>(scale + column(i) + 8 * g + (lane & 3) * 4);
+            const float2 s0 = make_float2(sv.x * sw, sv.y * sw), s1 = make_float2(sv.z * sw, sv.w * sw);
 #pragma unroll
             for (int h = 0; h < 4; ++h) {  // features lane / 4 + 8 h
-              const uint32_t* v = r[i] + (h >> 1) * 16 + 4 * g + (h & 1) * 2;
+              const uint32_t* v = r + (h >> 1) * 16 + 4 * g + (h & 1) * 2;
               const float2 x0 = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
               const float2 x1 = make_float2(__uint_as_float(v[4]), __uint_as_float(v[5]));
               float2* d = acc + (4 * i + h) * 4 + g;
-              d[0] = __ffma2_rn(x0, make_float2(sv.x, sv.y), d[0]);
-              d[1] = __ffma2_rn(x1, make_float2(sv.z, sv.w), d[1]);
+              d[0] = __ffma2_rn(x0, s0, d[0]);
+              d[1] = __ffma2_rn(x1, s1, d[1]);
             }
           }
         }
+        if (nch <= 0) release();
       }
       if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < C::NCH; ++i) {
-        if (i >= nch) continue;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = column(i) + 8 * g;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const float2 d = acc[(4 * i + h) * 4 + g];
-            if (a.f32) {
-              const int f = f0 + 8 * h + (lane >> 2), cc = c + 2 * (lane & 3);
-              float* o = static_cast<float*>(a.out) + static_cast<long long>(wk.c0 + cc) * a.F + f;
-              if (f < a.F && cc < wk.n) o[0] = d.x;
-              if (f < a.F && cc + 1 < wk.n) o[a.F] = d.y;
-            } else {
-              // two features of one row a lane
-              const __nv_bfloat162 p = __floats2bfloat162_rn(d.x, d.y);
-              const uint32_t u = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p));
-              const int f = f0 + 8 * h + 2 * (lane & 3), cc = c + (lane >> 2);
-              if (f < a.F && cc < wk.n)
-                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(wk.c0 + cc) * a.F + f) = u;
-            }
-          }
+      // accumulator j: rows c, c + 1 of features f0 + 8 h + lane / 4
+      auto store = [&](int j, float2 d) {
+        const int c = column(j >> 4) + 8 * (j & 3), h = (j >> 2) & 3;
+        if (c >= wk.n) return;
+        if (a.f32) {
+          const int f = f0 + 8 * h + (lane >> 2), cc = c + 2 * (lane & 3);
+          float* o = static_cast<float*>(a.out) + static_cast<long long>(wk.c0 + cc) * a.F + f;
+          if (f < a.F && cc < wk.n) o[0] = d.x;
+          if (f < a.F && cc + 1 < wk.n) o[a.F] = d.y;
+        } else {
+          // two features of one row a lane
+          const __nv_bfloat162 p = __floats2bfloat162_rn(d.x, d.y);
+          const uint32_t u = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p));
+          const int f = f0 + 8 * h + 2 * (lane & 3), cc = c + (lane >> 2);
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(wk.c0 + cc) * a.F + f;
+          if (f < a.F && cc < wk.n) *reinterpret_cast<uint32_t*>(o) = u;
         }
+      };
+      // the parts of S CTAs: each adds up every S-th accumulator, all its reads in flight at once
+      auto exchange = [&](auto clusters) {
+        constexpr int S = decltype(clusters)::value, NJ = C::CW / 2 / S;
+        // every load of this CTA has been used: its stages are free
+        constexpr int kStride = C::EPI_WARPS * 32;
+        float2* const part = reinterpret_cast<float2*>(smem) + ew * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < C::CW / 2; ++j) part[j * kStride] = acc[j];
+        cluster_sync();
+        exchanged = true;
+        float2 v[NJ][S];
+#pragma unroll
+        for (int i = 0; i < NJ; ++i)
+#pragma unroll
+          for (int r = 0; r < S; ++r) v[i][r] = ld_shared_cluster_f2(cluster_map(part + (i * S + rank) * kStride, r));
+#pragma unroll
+        for (int i = 0; i < NJ; ++i) {
+#pragma unroll
+          for (int r = 1; r < S; ++r) {
+            v[i][0].x += v[i][r].x;
+            v[i][0].y += v[i][r].y;
+          }
+          store(i * S + rank, v[i][0]);
+        }
+      };
+      switch (a.split) {
+        case 1:
+#pragma unroll
+          for (int j = 0; j < C::CW / 2; ++j) store(j, acc[j]);
+          break;
+        case 2: exchange(std::integral_constant<int, 2>{}); break;
+        case 4: exchange(std::integral_constant<int, 4>{}); break;
+        default: exchange(std::integral_constant<int, 8>{}); break;
       }
+    }
+    if (a.split > 1) {
+      if (!exchanged) cluster_sync();
+      cluster_sync();  // the other CTAs have read this one's part
     }
   }
   tc_fence_before();
@@ -319,7 +400,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_kernel(const __grid_co
 }
 
 template <class C>
-static cudaError_t launch_cfg(const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
+static cudaError_t launch_cfg(const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st) {
   static bool set[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
@@ -329,11 +410,28 @@ static cudaError_t launch_cfg(const Fp8Maps& maps, const Fp8Args& a, int sms, cu
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  // no more CTAs than there can be items
-  const long long units = static_cast<long long>(a.M) / C::BN + (a.M < a.E ? a.M : a.E);
-  const long long items = units * a.FT;
-  return launch_chained(fp8_gemm_kernel<C>, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(C::THREADS),
-                        C::SMEM, st, true, maps, a);
+  // no more CTAs than there can be items, or clusters that share them
+  const long long with = a.M < a.E ? a.M : a.E;  // experts that can have rows
+  const long long items = (a.M + (C::BN - 1) * with) / C::BN * a.FT;
+  const int resident = sms * (C::BN == 32 ? 2 : 1);
+  a.split = 1;
+  while (a.split < 8 && items * a.split * 2 <= resident && a.KB >= 8 * a.split) a.split *= 2;
+  const long long ctas = items * a.split;  // a cluster has one item: its CTAs meet once
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see chain_wait
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = a.split;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < resident ? ctas : resident));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<C>, maps, a);
 }
 
 cudaError_t launch_fp8_gemm(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {

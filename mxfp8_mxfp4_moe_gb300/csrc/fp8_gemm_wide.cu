@@ -353,7 +353,8 @@ static cudaError_t launch_cfg(const Fp8Maps& maps, Fp8Args a, int sms, cudaStrea
   }
   a.FT = (a.F + C::BN - 1) / C::BN;
   // no more CTAs than there can be items
-  const long long items = (static_cast<long long>(a.M) / C::BM + (a.M < a.E ? a.M : a.E)) * a.FT;
+  const long long with = a.M < a.E ? a.M : a.E;  // experts that can have rows
+  const long long items = (a.M + (C::BM - 1) * with) / C::BM * a.FT;
   return launch_chained(fp8_gemm_wide_kernel<C>, dim3(static_cast<unsigned>(items < sms ? items : sms)),
                         dim3(C::THREADS), C::SMEM, st, true, maps, a);
 }
