@@ -200,14 +200,14 @@ int kmoe_gemm_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, con
   a.KB = back ? nb : kb;
   a.ldb = M;
   a.f32 = f32;
+  const bool few = fp8_few_rows(M, E);
   Fp8Maps m;
   if (!make_weights_map(&m.a, w, E, N, K) ||
-      !make_codes_map(&m.b, x, M, back ? N : K, fp8_box_rows(fp8_tile_columns(M, E))))
+      !make_codes_map(&m.b, x, M, back ? N : K, few ? kFp8BoxRows : kFp8WideBoxRows))
     return KMOE_ERR_CUDA;
   const int sms = num_sms();
   if (sms <= 0) return KMOE_ERR_CUDA;
-  KMOE_CK(fp8_tile_columns(M, E) == 0 ? launch_fp8_gemm_wide(back, m, a, sms, stream)
-                                      : launch_fp8_gemm(back, m, a, sms, stream));
+  KMOE_CK(few ? launch_fp8_gemm(back, m, a, sms, stream) : launch_fp8_gemm_wide(back, m, a, sms, stream));
   return KMOE_OK;
 }
 

@@ -9,7 +9,7 @@ constexpr int kScaleBlock = 128;  // values a scale
 
 struct Fp8Maps {
   CUtensorMap a;  // weights in boxes of 128 x 128 (weight gradient: x)
-  CUtensorMap b;  // rows in boxes of fp8_box_rows (weight gradient: dy)
+  CUtensorMap b;  // boxes of 128 x kFp8BoxRows rows (weight gradient: dy)
 };
 
 struct Fp8Args {
@@ -30,18 +30,20 @@ struct Fp8Args {
   int split;       // CTAs of a cluster that share an item's blocks (fp8_gemm.cu; set at the launch)
 };
 
-// The kernel for M rows of E experts, by the rows an expert has on average:
-// fp8_gemm.cu with tiles of 32 or 128 rows, or (0) fp8_gemm_wide.cu.
-inline int fp8_tile_columns(int M, int E) {
-  const int avg = (M + E - 1) / E;
-  return avg <= 32 ? 32 : (avg <= 128 ? 128 : 0);
+// Tiles of up to `per` rows that M rows of E experts can have, whatever the
+// counts.
+__host__ inline long long fp8_most_tiles(long long M, int E, int per) {
+  const long long with = M < E ? M : E;  // experts that can have rows
+  return (M + (per - 1) * with) / per;
 }
-// Rows of a TMA box of such tiles: a copy takes the time of its rows, and tiles
-// are cut to multiples of 16.
-constexpr int fp8_box_rows(int tile_columns) { return tile_columns == 0 ? 128 : (tile_columns == 32 ? 8 : 32); }
+// Whether M rows of E experts are few for each, fp8_gemm.cu's; else fp8_gemm_wide.cu's.
+__host__ inline bool fp8_few_rows(int M, int E) { return (M + E - 1) / E <= 32; }
+// Rows of a TMA box of the rows: tiles of up to 32 are cut to multiples of 16
+// (a copy takes the time of its rows), those of many are 128.
+constexpr int kFp8BoxRows = 8, kFp8WideBoxRows = 128;
 
 cudaError_t launch_fp8_gemm(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
-cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st);
+cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st);
 constexpr int kWeightGradColumns = 224;  // n of a tile of the weights' gradient
 cudaError_t launch_fp8_wgrad(const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st);
 

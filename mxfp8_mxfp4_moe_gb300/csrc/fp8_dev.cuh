@@ -57,6 +57,44 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
+__device__ __forceinline__ float2 ld_shared_cluster_f2(uint32_t cluster_addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// CTAs of a cluster that share an item where `items` (at most) are too few for
+// the CTAs that can run at once: up to eight, with `least` blocks of the sum for
+// each.  Such a cluster has one item, and its CTAs meet once.
+__host__ inline int product_split(long long items, int resident, int KB, int least) {
+  int split = 1;
+  while (split < 8 && items * split * 2 <= resident && KB >= 2 * least * split) split *= 2;
+  return split;
+}
+
+// Launches a product's kernel for at most `items` work items on up to
+// `resident` CTAs; a.split is product_split's.
+template <typename Kernel>
+__host__ inline cudaError_t launch_product(Kernel kernel, int threads, int smem, long long items, int resident,
+                                           const Fp8Maps& maps, const Fp8Args& a, cudaStream_t st) {
+  const long long ctas = items * a.split;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see chain_wait
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = a.split;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < resident ? ctas : resident));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
 // A work item: features f0 .. of expert e for the columns (rows of the batch)
 // c0 .. c0 + n, over blocks kb .. kb + kn of the sum.
 struct Fp8Item {

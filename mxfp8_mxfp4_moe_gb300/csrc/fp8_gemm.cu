@@ -16,9 +16,8 @@
 //
 // Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues), warp
 // 2 the scales (a ring in shared memory, some blocks ahead of their use: with
-// few rows a block takes less time than a read of global memory), the others
-// the epilogue: groups of four warps (one per TMEM lane quarter) that take
-// the 32-column chunks in turn.  Every wait is bounded.
+// few rows a block takes less time than a read of global memory), warps 3 .. 6
+// the epilogue, one per TMEM lane quarter.  Every wait is bounded.
 //
 // Where there are too few items for the SMs, a cluster of `split` CTAs takes
 // one item: each sums a part of the blocks, and the parts are added in order
@@ -47,31 +46,21 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ float2 ld_shared_cluster_f2(uint32_t cluster_addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr) : "memory");
-  return v;
-}
-
-template <bool BACK_, int BN_>
+template <bool BACK_>
 struct Fp8Cfg {
   static constexpr bool BACK = BACK_;  // the weights transposed, read MN-major
-  static constexpr int BN = BN_;       // columns of a tile
+  static constexpr int BN = 32;        // rows of a tile
   static constexpr int A_BYTES = 128 * 128;
-  static constexpr int BOX = fp8_box_rows(BN);
+  static constexpr int BOX = kFp8BoxRows;
   static constexpr int STAGE = A_BYTES + BN * 128;
-  // BN = 32: two CTAs fit on an SM, so that one can start while another ends
-  static constexpr int STAGES = (BN == 32 ? 100 : 200) * 1024 / STAGE;
-  // an epilogue warp holds up to 64 columns of 32 features (a TMEM quarter), and
-  // in as many registers the block being read
-  static constexpr int CW = BN < 64 ? BN : 64;
-  static constexpr int NCH = CW / 32;  // 32-column chunks
-  static constexpr int NG = BN / CW;   // groups of four warps
-  static constexpr int EPI_WARPS = 4 * NG;
+  // two CTAs on an SM, so that one can start while another ends
+  static constexpr int CTAS_PER_SM = 2;
+  static constexpr int STAGES = 100 * 1024 / STAGE;
+  static constexpr int EPI_WARPS = 4;
   static constexpr int CTRL_WARPS = 3;
   static constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
-  static constexpr int NACC = 512 / BN < 4 ? 512 / BN : 4;
-  static constexpr int TMEM_COLS = BN * NACC <= 128 ? 128 : 512;
+  static constexpr int NACC = 4;
+  static constexpr int TMEM_COLS = NACC * BN;
   // ring of scales: a block's BN rows and its features'
   static constexpr int RING = 16, AHEAD = RING - NACC - 1;  // slots, and blocks loaded ahead
   static constexpr int SLOT = BN + 4;                       // floats
@@ -82,8 +71,7 @@ struct Fp8Cfg {
   static constexpr int SMEM = 1024 + TAB_OFF + (2 * TAB_INTS + 40) * 4;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert((2 * STAGES + 2 * NACC + 1) * 8 + 8 <= 256, "barriers");
-  static_assert(BN * NACC <= TMEM_COLS, "TMEM columns");
-  static_assert(EPI_WARPS * 32 * CW * 4 <= STAGES * STAGE, "a cluster's parts go where the stages were");
+  static_assert(EPI_WARPS * 32 * BN * 4 <= STAGES * STAGE, "a cluster's parts go where the stages were");
 };
 
 template <class C>
@@ -107,7 +95,7 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8Args& a, const int32_t* fir
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, C::BN == 32 ? 2 : 1) fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps,
+__global__ void __launch_bounds__(C::THREADS, C::CTAS_PER_SM) fp8_gemm_kernel(const __grid_constant__ Fp8Maps maps,
                                                                 const Fp8Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -220,11 +208,10 @@ __global__ void __launch_bounds__(C::THREADS, C::BN == 32 ? 2 : 1) fp8_gemm_kern
     }
     else {
       // ------------------------------------------------------------ scales
-      // A chunk's lie in the order in which the eight that a thread needs are
-      // two 16-byte pieces: columns 8g + 2q + {0, 1}, g even and the g after it.
-      const uint32_t ring =
-          smem_u32(smem + C::SC_OFF) +
-          ((lane >> 4) * 16 + ((lane & 7) >> 1) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1)) * 4;
+      // The rows' lie in the order in which the eight that a thread needs are two
+      // 16-byte pieces: rows 8g + 2q + {0, 1}, g even and the g after it.
+      const uint32_t ring = smem_u32(smem + C::SC_OFF) +
+                            ((lane >> 4) * 16 + ((lane & 7) >> 1) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1)) * 4;
       const uint32_t ring_w = smem_u32(smem + C::SC_OFF) + C::BN * 4;
       int w = w0 - dw, kb = 0, kn = 0, n = 0;  // the block that is loaded next
       const float *x_sf = nullptr, *w_sf = nullptr;
@@ -245,9 +232,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BN == 32 ? 2 : 1) fp8_gemm_kern
         }
         if (more) {
           const uint32_t slot = (issued & (C::RING - 1)) * (C::SLOT * 4);
-#pragma unroll
-          for (int j = 0; j < C::BN / 32; ++j)
-            if (32 * j < n) cp_async4(ring + slot + j * 128, x_sf + min(32 * j + lane, n - 1));
+          cp_async4(ring + slot, x_sf + min(lane, n - 1));
           if (lane == 0) cp_async4(ring_w + slot, w_sf);
           x_sf += a.ldb;
           w_sf += a.a_sk;
@@ -278,19 +263,15 @@ __global__ void __launch_bounds__(C::THREADS, C::BN == 32 ? 2 : 1) fp8_gemm_kern
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     const int ew = warp - C::CTRL_WARPS;
-    const int grp = ew >> 2;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     uint32_t it = 0;
     bool ok = true, exchanged = false;
     for (int w = w0; ok && w < total; w += dw) {
       const Fp8Item wk = fp8_item<C>(a, first, unit, w, rank);
       const int f0 = wk.f0 + q * 32;  // the warp's first feature
-      // the group's 32-column chunks start at column(0), column(1)
-      auto column = [&](int i) { return (i * C::NG + grp) * 32; };
-      const int nch = (wk.n - grp * 32 + C::NG * 32 - 1) / (C::NG * 32);  // chunks with columns of the tile
-      float2 acc[C::CW / 2];
+      float2 acc[16];
 #pragma unroll
-      for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < 16; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < wk.kn; ++kb, ++it) {
         const uint32_t b = it % C::NACC;
         if (!wait_warp(&acc_full[b], (it / C::NACC) & 1u, budget, a.err, abort_flag)) {
@@ -300,42 +281,35 @@ __global__ void __launch_bounds__(C::THREADS, C::BN == 32 ? 2 : 1) fp8_gemm_kern
         __syncwarp();
         tc_fence_after();
         const uint32_t t = tmem + lanes + b * C::BN;
+        uint32_t r[32];
+        tmem_ld_16x256b_x4(t, r);
+        tmem_ld_16x256b_x4(t + (16u << 16), r + 16);
         const float* const scale = reinterpret_cast<const float*>(smem + C::SC_OFF) + (it & (C::RING - 1)) * C::SLOT;
         const float sw = scale[C::BN];
-        auto release = [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[b]);
-        };
+        float2 s[4];  // of rows 8 g + 2 q + {0, 1}
 #pragma unroll
-        for (int i = 0; i < C::NCH; ++i) {
-          if (i >= nch) continue;
-          uint32_t r[32];
-          tmem_ld_16x256b_x4(t + column(i), r);
-          tmem_ld_16x256b_x4(t + (16u << 16) + column(i), r + 16);
-          tmem_ld_wait_for(r);
-          if (i == nch - 1) release();
-#pragma unroll
-          for (int g = 0; g < 4; g += 2) {
-            const float4 sv = *reinterpret_cast<const float4*>(scale + column(i) + 8 * g + (lane & 3) * 4);
-            const float2 s0 = make_float2(sv.x * sw, sv.y * sw), s1 = make_float2(sv.z * sw, sv.w * sw);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {  // features lane / 4 + 8 h
-              const uint32_t* v = r + (h >> 1) * 16 + 4 * g + (h & 1) * 2;
-              const float2 x0 = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-              const float2 x1 = make_float2(__uint_as_float(v[4]), __uint_as_float(v[5]));
-              float2* d = acc + (4 * i + h) * 4 + g;
-              d[0] = __ffma2_rn(x0, s0, d[0]);
-              d[1] = __ffma2_rn(x1, s1, d[1]);
-            }
-          }
+        for (int g = 0; g < 4; g += 2) {
+          const float4 v = *reinterpret_cast<const float4*>(scale + 8 * g + (lane & 3) * 4);
+          s[g] = make_float2(v.x * sw, v.y * sw);
+          s[g + 1] = make_float2(v.z * sw, v.w * sw);
         }
-        if (nch <= 0) release();
+        tmem_ld_wait_for(r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[b]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h)  // features lane / 4 + 8 h
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t* v = r + (h >> 1) * 16 + 4 * g + (h & 1) * 2;
+            acc[4 * h + g] =
+                __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), s[g], acc[4 * h + g]);
+          }
       }
       if (!ok) break;
       // accumulator j: rows c, c + 1 of features f0 + 8 h + lane / 4
       auto store = [&](int j, float2 d) {
-        const int c = column(j >> 4) + 8 * (j & 3), h = (j >> 2) & 3;
+        const int c = 8 * (j & 3), h = j >> 2;
         if (c >= wk.n) return;
         if (a.f32) {
           const int f = f0 + 8 * h + (lane >> 2), cc = c + 2 * (lane & 3);
@@ -353,12 +327,12 @@ __global__ void __launch_bounds__(C::THREADS, C::BN == 32 ? 2 : 1) fp8_gemm_kern
       };
       // the parts of S CTAs: each adds up every S-th accumulator, all its reads in flight at once
       auto exchange = [&](auto clusters) {
-        constexpr int S = decltype(clusters)::value, NJ = C::CW / 2 / S;
+        constexpr int S = decltype(clusters)::value, NJ = 16 / S;
         // every load of this CTA has been used: its stages are free
         constexpr int kStride = C::EPI_WARPS * 32;
         float2* const part = reinterpret_cast<float2*>(smem) + ew * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < C::CW / 2; ++j) part[j * kStride] = acc[j];
+        for (int j = 0; j < 16; ++j) part[j * kStride] = acc[j];
         cluster_sync();
         exchanged = true;
         float2 v[NJ][S];
@@ -379,7 +353,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BN == 32 ? 2 : 1) fp8_gemm_kern
       switch (a.split) {
         case 1:
 #pragma unroll
-          for (int j = 0; j < C::CW / 2; ++j) store(j, acc[j]);
+          for (int j = 0; j < 16; ++j) store(j, acc[j]);
           break;
         case 2: exchange(std::integral_constant<int, 2>{}); break;
         case 4: exchange(std::integral_constant<int, 4>{}); break;
@@ -410,34 +384,13 @@ static cudaError_t launch_cfg(const Fp8Maps& maps, Fp8Args a, int sms, cudaStrea
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  // no more CTAs than there can be items, or clusters that share them
-  const long long with = a.M < a.E ? a.M : a.E;  // experts that can have rows
-  const long long items = (a.M + (C::BN - 1) * with) / C::BN * a.FT;
-  const int resident = sms * (C::BN == 32 ? 2 : 1);
-  a.split = 1;
-  while (a.split < 8 && items * a.split * 2 <= resident && a.KB >= 8 * a.split) a.split *= 2;
-  const long long ctas = items * a.split;  // a cluster has one item: its CTAs meet once
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see chain_wait
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = a.split;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas < resident ? ctas : resident));
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = a.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<C>, maps, a);
+  const long long items = fp8_most_tiles(a.M, a.E, C::BN) * a.FT;
+  a.split = product_split(items, C::CTAS_PER_SM * sms, a.KB, 4);
+  return launch_product(fp8_gemm_kernel<C>, C::THREADS, C::SMEM, items, C::CTAS_PER_SM * sms, maps, a, st);
 }
 
 cudaError_t launch_fp8_gemm(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
-  if (fp8_tile_columns(a.M, a.E) == 32)
-    return back ? launch_cfg<Fp8Cfg<true, 32>>(maps, a, sms, st) : launch_cfg<Fp8Cfg<false, 32>>(maps, a, sms, st);
-  return back ? launch_cfg<Fp8Cfg<true, 128>>(maps, a, sms, st) : launch_cfg<Fp8Cfg<false, 128>>(maps, a, sms, st);
+  return back ? launch_cfg<Fp8Cfg<true>>(maps, a, sms, st) : launch_cfg<Fp8Cfg<false>>(maps, a, sms, st);
 }
 
 }  // namespace kmoe

@@ -8,18 +8,23 @@
 // one multiply-add a value; with the rows in the MMA's N it needs a factor a
 // column, from shared memory that the tensor core is reading.
 //
+// Where there are too few items for the SMs, a cluster of `split` CTAs takes
+// one item, as in fp8_gemm.cu.
+//
 // Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues),
 // warp 2 the scales (a ring in shared memory, some blocks ahead of their use),
-// warps 4 .. 15 the epilogue: three groups of four (one warp per TMEM lane
-// quarter) that take the eight 32-column chunks in turn.  Every wait is
-// bounded.
+// warps 4 .. 11 the epilogue: two groups of four (one warp per TMEM lane
+// quarter), each with 128 features of the tile.  Every wait is bounded.
+#include <type_traits>
+
 #include "fp8_dev.cuh"
 
 namespace kmoe {
 
-template <bool BACK_>
+template <bool BACK_, bool SPLIT_>
 struct Fp8WideCfg {
-  static constexpr bool BACK = BACK_;  // the weights transposed, read MN-major
+  static constexpr bool BACK = BACK_;    // the weights transposed, read MN-major
+  static constexpr bool SPLIT = SPLIT_;  // a cluster shares an item (its exchange costs the others registers)
   static constexpr int BM = 128, BN = 256;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
@@ -44,11 +49,13 @@ struct Fp8WideCfg {
   static constexpr int SMEM = 1024 + TAB_OFF + (2 * TAB_INTS + 40) * 4;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(RING >= AHEAD + NACC + 1, "a slot is written again when its block has been read");
+  static_assert(EPI_WARPS * 32 * NCH * 8 * 8 <= STAGES * STAGE, "a cluster's parts go where the stages were");
   static_assert(128 * CTRL_REGS + 32 * EPI_WARPS * EPI_REGS <= THREADS * 168, "register split");
 };
 
 template <class C>
-__device__ __forceinline__ Fp8Item wide_item(const Fp8Args& a, const int32_t* first, const int32_t* unit, int w) {
+__device__ __forceinline__ Fp8Item wide_item(const Fp8Args& a, const int32_t* first, const int32_t* unit, int w,
+                                             int rank) {
   Fp8Item it;
   it.e = segment_of_unit(unit, a.E, w / a.FT);
   const int u0 = unit[it.e], nt = unit[it.e + 1] - u0;
@@ -57,8 +64,14 @@ __device__ __forceinline__ Fp8Item wide_item(const Fp8Args& a, const int32_t* fi
   const int at = r % nt * C::BM;
   it.c0 = first[it.e] + at;
   it.n = min(C::BM, first[it.e + 1] - it.c0);
-  it.kb = 0;
-  it.kn = a.KB;
+  if constexpr (C::SPLIT) {
+    const int per_cta = (a.KB + a.split - 1) / a.split;
+    it.kb = min(rank * per_cta, a.KB);
+    it.kn = min(per_cta, a.KB - it.kb);
+  } else {
+    it.kb = 0;
+    it.kn = a.KB;
+  }
   return it;
 }
 
@@ -79,6 +92,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = C::SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -106,6 +120,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
   const uint32_t tmem = *tmem_slot;
   const int total = a.FT * unit[a.E];
   const uint64_t budget = a.budget_ns;
+  const int ctas = C::SPLIT ? a.split : 1;
+  const int w0 = blockIdx.x / ctas, dw = gridDim.x / ctas;
 
   if (warp < C::CTRL_WARPS) {
     // (of the registers that the block was launched with)
@@ -115,8 +131,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
       const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_last();
       uint32_t it = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-        const Fp8Item wk = wide_item<C>(a, first, unit, w);
+      for (int w = w0; ok && w < total; w += dw) {
+        const Fp8Item wk = wide_item<C>(a, first, unit, w, rank);
         const int boxes = a.F - wk.f0 > 128 ? 2 : 1;  // of 128 features
         const uint32_t tx = C::A_BYTES + boxes * 16384;
         for (int kb = 0; kb < wk.kn; ++kb, ++it) {
@@ -126,7 +142,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
             break;
           }
           uint8_t* sa = smem + s * C::STAGE;
-          const int k0 = kb * kScaleBlock;
+          const int k0 = (wk.kb + kb) * kScaleBlock;
           mbar_arrive_expect_tx_el(&full[s], tx);
           tma_load_2d_el(sa, &maps.b, &full[s], k0, wk.c0, pol_x);
           for (int i = 0; i < boxes; ++i) {
@@ -150,8 +166,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
                                       : sdesc_kmajor_sw128(smem_u32(smem + C::A_BYTES));
       uint32_t it = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-        const Fp8Item wk = wide_item<C>(a, first, unit, w);
+      for (int w = w0; ok && w < total; w += dw) {
+        const Fp8Item wk = wide_item<C>(a, first, unit, w, rank);
         const uint32_t idesc = idesc_f8(128, min(C::BN, a.F - wk.f0), false, C::BACK);  // F is a multiple of 16
         for (int kb = 0; kb < wk.kn; ++kb, ++it) {
           const int s = it % C::STAGES;
@@ -176,22 +192,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
       // ------------------------------------------------------------ scales
       const uint32_t ring = smem_u32(smem + C::SC_OFF);
       // the block that is loaded next: the issued-th of this CTA's
-      int w = blockIdx.x - gridDim.x, kb = 0, kn = 0;
+      int w = w0 - dw, kb = 0, kn = 0;
       const float *x_sf = nullptr, *w_sf = nullptr;
       bool more = true;
       uint32_t issued = 0;
       int n = 0, second = 0;
       auto issue = [&] {
-        if (kb == kn) {  // the next item
-          w += gridDim.x;
+        while (more && kb >= kn) {  // the next item
+          w += dw;
           more = w < total;
           if (more) {
-            const Fp8Item wk = wide_item<C>(a, first, unit, w);
+            const Fp8Item wk = wide_item<C>(a, first, unit, w, rank);
             kb = 0;
             kn = wk.kn;
             n = wk.n;
-            x_sf = a.b_sf + wk.c0;
-            w_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm;
+            x_sf = a.b_sf + static_cast<long long>(wk.kb) * a.ldb + wk.c0;
+            w_sf = a.a_sf + wk.e * a.a_se + static_cast<long long>(wk.f0 >> 7) * a.a_sm + wk.kb * a.a_sk;
             second = a.F - wk.f0 > 128 ? a.a_sm : 0;
           }
         }
@@ -221,6 +237,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
+    if constexpr (C::SPLIT) {  // (the epilogue's exchange)
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::EPI_REGS));
     // ------------------------------------------------------------ epilogue
@@ -229,9 +249,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     uint8_t* const out_smem = smem + C::OUT_OFF + (warp - C::CTRL_WARPS) * 2048;
     uint32_t it = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-      const Fp8Item wk = wide_item<C>(a, first, unit, w);
+    bool ok = true, exchanged = false;
+    for (int w = w0; ok && w < total; w += dw) {
+      const Fp8Item wk = wide_item<C>(a, first, unit, w, rank);
       const int row = q * 32 + lane;
       const int g0 = wk.f0 + grp * 128;  // the group's first feature
       const int ng = a.F - g0;           // and how many there are from there (128 used)
@@ -307,29 +327,84 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
         }
         __syncwarp();
       };
+      // 16 features of a row as fp32
+      auto pieces_f32 = [&](const float2* d) {
 #pragma unroll
-      for (int i = 0; i < C::NCH; ++i) {
-        const float2* d = acc[i];
-        if (a.f32) {
-          if (16 * i < ng) {
+        for (int j = 0; j < 4; ++j)
+          out_piece(j, make_uint4(__float_as_uint(d[2 * j].x), __float_as_uint(d[2 * j].y),
+                                  __float_as_uint(d[2 * j + 1].x), __float_as_uint(d[2 * j + 1].y)));
+      };
+      // and as bf16, pieces p and p + 1
+      auto pieces_bf16 = [&](const float2* d, int p) {
+        uint32_t u[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              out_piece(j, make_uint4(__float_as_uint(d[2 * j].x), __float_as_uint(d[2 * j].y),
-                                      __float_as_uint(d[2 * j + 1].x), __float_as_uint(d[2 * j + 1].y)));
+        for (int j = 0; j < 8; ++j) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(d[j].x, d[j].y);
+          u[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        out_piece(p, make_uint4(u[0], u[1], u[2], u[3]));
+        out_piece(p + 1, make_uint4(u[4], u[5], u[6], u[7]));
+      };
+      // the parts of S CTAs: each adds up and stores an S-th of the chunks
+      auto exchange = [&](auto clusters) {
+        constexpr int S = decltype(clusters)::value, NJ = C::NCH / S;
+        // every load of this CTA has been used: its stages are free
+        constexpr int kStride = C::EPI_WARPS * 32;
+        float2* const part = reinterpret_cast<float2*>(smem) + (warp - C::CTRL_WARPS) * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < C::NCH; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) part[(8 * i + j) * kStride] = acc[i][j];
+        cluster_sync();
+        exchanged = true;
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) {
+          const int i = rank * NJ + n;
+          float2 v[S][8];
+#pragma unroll
+          for (int r = 0; r < S; ++r)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[r][j] = ld_shared_cluster_f2(cluster_map(part + (8 * i + j) * kStride, r));
+#pragma unroll
+          for (int r = 1; r < S; ++r)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              v[0][j].x += v[r][j].x;
+              v[0][j].y += v[r][j].y;
+            }
+          if (16 * i >= ng) continue;
+          if (a.f32) {
+            pieces_f32(v[0]);
             flush((g0 + 16 * i) * 4LL, a.F * 4LL, 4);
+          } else {
+            pieces_bf16(v[0], 0);
+            flush((g0 + 16 * i) * 2LL, a.F * 2LL, 2);
           }
-        } else {
-          uint32_t u[8];
+        }
+      };
+      if constexpr (C::SPLIT) {
+        switch (a.split) {
+          case 2: exchange(std::integral_constant<int, 2>{}); break;
+          case 4: exchange(std::integral_constant<int, 4>{}); break;
+          default: exchange(std::integral_constant<int, 8>{}); break;
+        }
+      } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(d[j].x, d[j].y);
-            u[j] = *reinterpret_cast<const uint32_t*>(&p);
+        for (int i = 0; i < C::NCH; ++i) {
+          if (a.f32) {
+            if (16 * i >= ng) continue;
+            pieces_f32(acc[i]);
+            flush((g0 + 16 * i) * 4LL, a.F * 4LL, 4);
+          } else {
+            pieces_bf16(acc[i], (i & 1) * 2);
+            if ((i & 1) && 16 * (i - 1) < ng) flush((g0 + 16 * (i - 1)) * 2LL, a.F * 2LL, 16 * i < ng ? 4 : 2);
           }
-          out_piece((i & 1) * 2, make_uint4(u[0], u[1], u[2], u[3]));
-          out_piece((i & 1) * 2 + 1, make_uint4(u[4], u[5], u[6], u[7]));
-          if ((i & 1) && 16 * (i - 1) < ng) flush((g0 + 16 * (i - 1)) * 2LL, a.F * 2LL, 16 * i < ng ? 4 : 2);
         }
       }
+    }
+    if constexpr (C::SPLIT) {
+      if (!exchanged) cluster_sync();
+      cluster_sync();  // the other CTAs have read this one's part
     }
   }
   tc_fence_before();
@@ -341,7 +416,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
 }
 
 template <class C>
-static cudaError_t launch_cfg(const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st) {
+static cudaError_t launch_cfg(const Fp8Maps& maps, const Fp8Args& a, long long items, int sms, cudaStream_t st) {
   static bool set[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
@@ -351,16 +426,19 @@ static cudaError_t launch_cfg(const Fp8Maps& maps, Fp8Args a, int sms, cudaStrea
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  a.FT = (a.F + C::BN - 1) / C::BN;
-  // no more CTAs than there can be items
-  const long long with = a.M < a.E ? a.M : a.E;  // experts that can have rows
-  const long long items = (a.M + (C::BM - 1) * with) / C::BM * a.FT;
-  return launch_chained(fp8_gemm_wide_kernel<C>, dim3(static_cast<unsigned>(items < sms ? items : sms)),
-                        dim3(C::THREADS), C::SMEM, st, true, maps, a);
+  return launch_product(fp8_gemm_wide_kernel<C>, C::THREADS, C::SMEM, items, sms, maps, a, st);
 }
 
-cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
-  return back ? launch_cfg<Fp8WideCfg<true>>(maps, a, sms, st) : launch_cfg<Fp8WideCfg<false>>(maps, a, sms, st);
+cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st) {
+  using C = Fp8WideCfg<false, false>;
+  a.FT = (a.F + C::BN - 1) / C::BN;
+  const long long items = fp8_most_tiles(a.M, a.E, C::BM) * a.FT;
+  a.split = product_split(items, sms, a.KB, 8);
+  if (a.split > 1)
+    return back ? launch_cfg<Fp8WideCfg<true, true>>(maps, a, items, sms, st)
+                : launch_cfg<Fp8WideCfg<false, true>>(maps, a, items, sms, st);
+  return back ? launch_cfg<Fp8WideCfg<true, false>>(maps, a, items, sms, st)
+              : launch_cfg<Fp8WideCfg<false, false>>(maps, a, items, sms, st);
 }
 
 }  // namespace kmoe

@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 import mxfp8_mxfp4_moe_gb300 as _k
-from mxfp8_mxfp4_moe_gb300 import (_F32_OR_BF16, _arg, _args, _check, _gpu, _nbytes, _new, _raw_stream, _rows,
+from mxfp8_mxfp4_moe_gb300 import (_F32_OR_BF16, _arg, _args, _check, _gpu, _new, _raw_stream, _rows,
                                    _rows_on, _type_of)
 
 PRODUCT_EXPORTS = ("kmoe_sort_workspace_size", "kmoe_sort_tokens", "kmoe_permute", "kmoe_unpermute",
@@ -177,10 +177,14 @@ def kmoe_quantize_fp8(x, row_of_slot=None, codes=None, scales=None, stream=None)
 
 def _weights(w, name):
     """(E, N, K) of weights [E, N, K], or [N, K] for a dense projection, and their scales' shape."""
-    if w is None or w.dim() not in (2, 3):
+    s = () if w is None else w.shape
+    if len(s) == 3:
+        E, N, K = s
+        return s, (E, (N + 127) // 128, (K + 127) // 128)
+    if len(s) != 2:
         raise ValueError(f"{name} must be a tensor [E, N, K] or [N, K]")
-    s = tuple(w.shape)
-    return (1, *s)[-3:], s[:-2] + (-(-s[-2] // _BLOCK), -(-s[-1] // _BLOCK))
+    N, K = s
+    return (1, N, K), ((N + 127) // 128, (K + 127) // 128)
 
 
 def kmoe_quantize_fp8_weights(w, codes=None, scales=None, stream=None):
@@ -232,12 +236,13 @@ def kmoe_quantize_fp8_cols(x, seg_start=None, codes=None, scales=None, stream=No
     return codes, scales
 
 
-def _product_workspace(workspace, dev, stream):
+def _workspace_entry(workspace):
+    """A product's workspace, for _args."""
     if workspace is None:
-        return _new(GEMM_FP8_WORKSPACE_BYTES, _U8, dev, stream)
-    _arg(workspace, "workspace", _U8, min_bytes=GEMM_FP8_WORKSPACE_BYTES)
-    _gpu(stream, workspace=workspace)
-    return workspace
+        return "workspace", None, _U8, None
+    if workspace.numel() < GEMM_FP8_WORKSPACE_BYTES:
+        _arg(workspace, "workspace", _U8, min_bytes=GEMM_FP8_WORKSPACE_BYTES)
+    return "workspace", workspace, _U8, workspace.shape
 
 
 def kmoe_gemm_fp8(x, x_scales, w, w_scales, seg_start=None, transpose=False, out=None, out_dtype=torch.bfloat16,
@@ -256,14 +261,17 @@ def kmoe_gemm_fp8(x, x_scales, w, w_scales, seg_start=None, transpose=False, out
     wide, F = (N, K) if transpose else (K, N)
     to = _out_type(out, out_dtype)
     at = _args(stream, dev, (("x", x, _U8, (M, wide)), ("x_scales", x_scales, _F32, (-(-wide // _BLOCK), M)),
-                             ("w", w, _U8, w.shape), ("w_scales", w_scales, _F32, sf), seg, ("out", out, to, (M, F))))
-    workspace = _product_workspace(workspace, dev, stream)
+                             ("w", w, _U8, w.shape), ("w_scales", w_scales, _F32, sf), seg, ("out", out, to, (M, F)),
+                             _workspace_entry(workspace)))
+    if workspace is None:
+        workspace = _new(GEMM_FP8_WORKSPACE_BYTES, _U8, dev, stream)
+        at[6] = workspace.data_ptr()
     if out is None:
         out = _new((M, F), to, dev, stream)
         at[5] = out.data_ptr()
     flags = (KMOE_GEMM_TRANSPOSE if transpose else 0) | (KMOE_GEMM_OUT_F32 if to is _F32 else 0)
     _check("kmoe_gemm_fp8", _k._lib.kmoe_gemm_fp8(at[0], at[1], at[2], at[3], at[4], M, N, K, E, flags, at[5],
-                                                  workspace.data_ptr(), _nbytes(workspace), _raw_stream(dev, stream)))
+                                                  at[6], workspace.numel(), _raw_stream(dev, stream)))
     return out, workspace
 
 
@@ -276,12 +284,14 @@ def kmoe_gemm_fp8_wgrad(dy, dy_scales, x, x_scales, seg_start=None, dw=None, wor
     E, seg = _experts(seg_start)
     at = _args(stream, dev, (("dy", dy, _U8, (P, N)), ("dy_scales", dy_scales, _F32, (P // _BLOCK, N)),
                              ("x", x, _U8, (P, K)), ("x_scales", x_scales, _F32, (P // _BLOCK, K)), seg,
-                             ("dw", dw, _F32, (E, N, K))))
-    workspace = _product_workspace(workspace, dev, stream)
+                             ("dw", dw, _F32, (E, N, K)), _workspace_entry(workspace)))
+    if workspace is None:
+        workspace = _new(GEMM_FP8_WORKSPACE_BYTES, _U8, dev, stream)
+        at[6] = workspace.data_ptr()
     if dw is None:
         dw = _new((E, N, K), _F32, dev, stream)
         at[5] = dw.data_ptr()
     _check("kmoe_gemm_fp8_wgrad", _k._lib.kmoe_gemm_fp8_wgrad(
-        at[0], at[1], at[2], at[3], at[4], P, N, K, E, at[5], workspace.data_ptr(), _nbytes(workspace),
+        at[0], at[1], at[2], at[3], at[4], P, N, K, E, at[5], at[6], workspace.numel(),
         _raw_stream(dev, stream)))
     return dw, workspace
