@@ -81,9 +81,12 @@ int kmoe_unpermute_backward(const void* d_out, const void* y, const int32_t* row
  * kmoe_gemm_fp8 reads them.  With row_of_slot [rows, k] (kmoe_sort_tokens')
  * row t goes to the sorted rows of its k slots instead: codes [rows * k, cols],
  * scales [ceil(cols/128), rows * k]; rows without a slot keep their contents.
- * Without it k is 1. */
+ * Without it k is 1.
+ *   workspace: kmoe_quantize_fp8_workspace_size bytes (0: none is used), 4-byte
+ *   aligned, or null: many sorted rows' scales are then stored more slowly. */
+size_t kmoe_quantize_fp8_workspace_size(int rows, int cols, int k);
 int kmoe_quantize_fp8(const void* x_bf16, int rows, int cols, const int32_t* row_of_slot, int k, uint8_t* codes,
-                      float* scales, cudaStream_t stream);
+                      float* scales, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Weights [E, N, K]: blocks of 128 x 128 of an expert.  codes [E, N, K], scales
  * [E, ceil(N/128), ceil(K/128)] float.  E <= 1024. */

@@ -48,8 +48,9 @@ constexpr int kWeightGradColumns = 224;  // n of a tile of the weights' gradient
 cudaError_t launch_fp8_wgrad(const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st);
 
 cudaError_t launch_fp8_quant_rows(const void* x, int rows, int cols, uint8_t* codes, float* scales, cudaStream_t st);
+// workspace: scales by token and a slot a row, or null.
 cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, const int32_t* row_of_slot, uint8_t* codes,
-                                     float* scales, cudaStream_t st);
+                                     float* scales, void* workspace, cudaStream_t st);
 cudaError_t launch_fp8_quant_weights(const void* w, int E, int N, int K, uint8_t* codes, float* scales,
                                      cudaStream_t st);
 cudaError_t launch_fp8_quant_cols(const void* x, int rows, int cols, const int32_t* seg, int E, uint8_t* codes,

@@ -9,6 +9,7 @@
 //   fp8_quant_rows_kernel     128 columns of one row: the sum of rows x weights
 //   fp8_quant_scatter_kernel  the same, each token's row once, written to the
 //                             expert-sorted rows of its k slots
+//   fp8_sort_scales_kernel    the scales of those rows, where they are many
 //   fp8_quant_tile_kernel     128 rows of one column (the sum of the weights'
 //                             gradient; every expert's rows from a multiple of
 //                             128 on, zeros behind them), or 128 x 128 weights
@@ -81,16 +82,22 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const __nv_bfloat16
   }
 }
 
+// A row's scales are a line apart, so storing them here is a partial sector a
+// value; LATER keeps them by token (`scales` [T][groups]) and notes each row's
+// slot for fp8_sort_scales_kernel.
+template <bool LATER>
 __global__ void __launch_bounds__(512) fp8_quant_scatter_kernel(const __nv_bfloat16* __restrict__ x, int cols, int k,
                                                                 long long R, const int32_t* __restrict__ row_of_slot,
-                                                                uint8_t* __restrict__ codes,
-                                                                float* __restrict__ scales) {
+                                                                uint8_t* __restrict__ codes, float* __restrict__ scales,
+                                                                int32_t* __restrict__ slot_of_row) {
   chain_wait();
   __shared__ int s_row[kMaxK];
   const long long t = blockIdx.x;
   if (threadIdx.x < k) {
     const int r = row_of_slot[t * k + threadIdx.x];
-    s_row[threadIdx.x] = r >= 0 && r < R ? r : -1;
+    const bool in = r >= 0 && r < R;
+    s_row[threadIdx.x] = in ? r : -1;
+    if (LATER && in) slot_of_row[r] = static_cast<int>(t * k + threadIdx.x);
   }
   __syncthreads();
   const int step = blockDim.x * 16 * gridDim.y;
@@ -105,12 +112,45 @@ __global__ void __launch_bounds__(512) fp8_quant_scatter_kernel(const __nv_bfloa
     const uint2 lo = e4m3_chunk(v.a, byte), hi = e4m3_chunk(v.b, byte);
     const uint4 out = make_uint4(lo.x, lo.y, hi.x, hi.y);
     const float scale = fp8_scale(byte);
+    if (LATER && (threadIdx.x & 7) == 0) scales[t * ((cols + 127) / 128) + (col >> 7)] = scale;
     for (int j = 0; j < k; ++j) {
       const int r = s_row[j];
       if (r < 0) continue;
       *reinterpret_cast<uint4*>(codes + static_cast<long long>(r) * cols + col) = out;
-      if ((threadIdx.x & 7) == 0) scales[(col >> 7) * R + r] = scale;
+      if (!LATER && (threadIdx.x & 7) == 0) scales[(col >> 7) * R + r] = scale;
     }
+  }
+}
+
+// The scales by token [T][groups] into the sorted rows' lines [groups][R]: 32
+// rows a block, 64 groups at a time, turned in shared memory.  slot_of_row may
+// hold anything for rows without a slot, which are left out.
+__global__ void __launch_bounds__(256) fp8_sort_scales_kernel(const float* __restrict__ by_token, int groups, int k,
+                                                              long long R, const int32_t* __restrict__ row_of_slot,
+                                                              const int32_t* __restrict__ slot_of_row,
+                                                              float* __restrict__ scales) {
+  chain_wait();
+  __shared__ float s_tile[32][65];
+  __shared__ int s_token[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long r0 = blockIdx.x * 32LL;
+  if (warp == 0) {
+    const long long r = r0 + lane;
+    const int s = r < R ? slot_of_row[r] : -1;
+    s_token[lane] = s >= 0 && s < R && row_of_slot[s] == r ? s / k : -1;
+  }
+  __syncthreads();
+  for (int g0 = 0; g0 < groups; g0 += 64) {
+    for (int i = warp; i < 32; i += 8) {
+      const int t = s_token[i];
+      if (t < 0) continue;
+      for (int g = lane; g < min(64, groups - g0); g += 32)
+        s_tile[i][g] = __ldg(by_token + static_cast<long long>(t) * groups + g0 + g);
+    }
+    __syncthreads();
+    if (s_token[lane] >= 0)
+      for (int g = warp; g < min(64, groups - g0); g += 8) scales[(g0 + g) * R + r0 + lane] = s_tile[lane][g];
+    __syncthreads();
   }
 }
 
@@ -149,30 +189,32 @@ __global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const __nv_bfloat16
   for (int c0 = blockIdx.y * 128; c0 < cols; c0 += gridDim.y * 128) {
     const int col = c0 + cg * 8;
     uint4 v[8];
-    uint32_t m[4] = {0, 0, 0, 0};  // largest magnitudes of the columns, two a word
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = r0 + 16 * i;
       v[i] = make_uint4(0, 0, 0, 0);
       if (r < n && col < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(x + (src + r) * cols + col));
     }
+    // largest magnitudes of the thread's columns, two a word, then over the two rows of a warp
+    __nv_bfloat162 m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = __float2bfloat162_rn(0.f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (bf16_amax_nan(v[i]) > 0x7F80u) v[i] = bf16_drop_nan(v[i]);
-      m[0] = __vmaxu2(m[0], v[i].x & 0x7FFF7FFFu);
-      m[1] = __vmaxu2(m[1], v[i].y & 0x7FFF7FFFu);
-      m[2] = __vmaxu2(m[2], v[i].z & 0x7FFF7FFFu);
-      m[3] = __vmaxu2(m[3], v[i].w & 0x7FFF7FFFu);
-    }
-    // over the two rows of a warp, then over the warps
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = __vmaxu2(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+      for (int j = 0; j < 4; ++j) m[j] = __hmax2(m[j], __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = __hmax2(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
     __syncthreads();
     if (lane < 16)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s_max[warp][cg * 8 + 2 * j] = m[j] & 0xFFFFu;
-        s_max[warp][cg * 8 + 2 * j + 1] = m[j] >> 16;
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&m[j]);
+        s_max[warp][cg * 8 + 2 * j] = u & 0xFFFFu;
+        s_max[warp][cg * 8 + 2 * j + 1] = u >> 16;
       }
     __syncthreads();
     if (threadIdx.x < 128) {
@@ -197,17 +239,20 @@ __global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const __nv_bfloat16
     } else if (col < cols) {
       // eight columns with scales of their own
       uint32_t byte[8];
+      float inv[8];  // 1 / s: a power of two, so x / s is exact
 #pragma unroll
-      for (int j = 0; j < 8; ++j) byte[j] = fp8_scale_byte(s_max[0][cg * 8 + j]);
+      for (int j = 0; j < 8; ++j) {
+        byte[j] = fp8_scale_byte(s_max[0][cg * 8 + j]);
+        inv[j] = exp2i(127 - static_cast<int>(byte[j]));
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         uint32_t pair[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          // x / s: exact, s = 2^(byte - 127)
-          const float lo = __uint_as_float(w[j] << 16) * exp2i(127 - static_cast<int>(byte[2 * j]));
-          const float hi = __uint_as_float(w[j] & 0xFFFF0000u) * exp2i(127 - static_cast<int>(byte[2 * j + 1]));
+          const float lo = __uint_as_float(w[j] << 16) * inv[2 * j];
+          const float hi = __uint_as_float(w[j] & 0xFFFF0000u) * inv[2 * j + 1];
           pair[j] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
         }
         *reinterpret_cast<uint2*>(codes + (dst + r0 + 16 * i) * cols + col) =
@@ -228,14 +273,25 @@ cudaError_t launch_fp8_quant_rows(const void* x, int rows, int cols, uint8_t* co
 }
 
 cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, const int32_t* row_of_slot, uint8_t* codes,
-                                     float* scales, cudaStream_t st) {
+                                     float* scales, void* workspace, cudaStream_t st) {
   const int chunks = (cols / 16 + 31) / 32;  // warps a row takes
   // few tokens: a warp a block, so that their stores spread over the SMs
   const int threads = T < 304 ? 32 : 32 * (chunks < 16 ? chunks : 16);
-  const int split = T < 304 ? chunks : 1;
-  return launch_chained(fp8_quant_scatter_kernel, dim3(T, split), dim3(threads), 0, st, true,
-                        static_cast<const __nv_bfloat16*>(x), cols, k, static_cast<long long>(T) * k, row_of_slot,
-                        codes, scales);
+  const dim3 grid(T, T < 304 ? chunks : 1);
+  const long long R = static_cast<long long>(T) * k;
+  const auto* rows = static_cast<const __nv_bfloat16*>(x);
+  if (workspace == nullptr)
+    return launch_chained(fp8_quant_scatter_kernel<false>, grid, dim3(threads), 0, st, true, rows, cols, k, R,
+                          row_of_slot, codes, scales, static_cast<int32_t*>(nullptr));
+  const int groups = (cols + 127) / 128;
+  float* by_token = static_cast<float*>(workspace);
+  int32_t* slot_of_row = static_cast<int32_t*>(workspace) + static_cast<long long>(T) * groups;
+  const cudaError_t e = launch_chained(fp8_quant_scatter_kernel<true>, grid, dim3(threads), 0, st, true, rows, cols, k,
+                                       R, row_of_slot, codes, by_token, slot_of_row);
+  if (e != cudaSuccess) return e;
+  return launch_chained(fp8_sort_scales_kernel, dim3(static_cast<unsigned>((R + 31) / 32)), dim3(256), 0, st, true,
+                        static_cast<const float*>(by_token), groups, k, R, row_of_slot,
+                        static_cast<const int32_t*>(slot_of_row), scales);
 }
 
 cudaError_t launch_fp8_quant_weights(const void* w, int E, int N, int K, uint8_t* codes, float* scales,

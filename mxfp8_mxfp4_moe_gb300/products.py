@@ -16,8 +16,9 @@ from mxfp8_mxfp4_moe_gb300 import (_F32_OR_BF16, _arg, _args, _check, _gpu, _new
                                    _rows_on, _type_of)
 
 PRODUCT_EXPORTS = ("kmoe_sort_workspace_size", "kmoe_sort_tokens", "kmoe_permute", "kmoe_unpermute",
-                   "kmoe_unpermute_backward", "kmoe_quantize_fp8", "kmoe_quantize_fp8_weights",
-                   "kmoe_fp8_padded_rows", "kmoe_quantize_fp8_cols", "kmoe_gemm_fp8", "kmoe_gemm_fp8_wgrad")
+                   "kmoe_unpermute_backward", "kmoe_quantize_fp8_workspace_size", "kmoe_quantize_fp8",
+                   "kmoe_quantize_fp8_weights", "kmoe_fp8_padded_rows", "kmoe_quantize_fp8_cols", "kmoe_gemm_fp8",
+                   "kmoe_gemm_fp8_wgrad")
 
 __all__ = ["PRODUCT_EXPORTS", "KMOE_ROWS_F32", "KMOE_OUT_F32", "KMOE_GEMM_TRANSPOSE", "KMOE_GEMM_OUT_F32",
            "GEMM_FP8_WORKSPACE_BYTES", *PRODUCT_EXPORTS]
@@ -38,7 +39,8 @@ def _declare(lib):
                        ("kmoe_permute", [P, P, I, I, I, U, P, V]),
                        ("kmoe_unpermute", [P, P, P, I, I, I, U, P, V]),
                        ("kmoe_unpermute_backward", [P, P, P, P, I, I, I, U, P, P, V]),
-                       ("kmoe_quantize_fp8", [P, I, I, P, I, P, P, V]),
+                       ("kmoe_quantize_fp8_workspace_size", [I, I, I]),
+                       ("kmoe_quantize_fp8", [P, I, I, P, I, P, P, P, S, V]),
                        ("kmoe_quantize_fp8_weights", [P, I, I, I, P, P, V]),
                        ("kmoe_fp8_padded_rows", [I, I]),
                        ("kmoe_quantize_fp8_cols", [P, I, I, P, I, P, P, V]),
@@ -155,7 +157,11 @@ def kmoe_unpermute_backward(d_out, y, row_of_slot, topk_w, d_y=None, d_w=None, s
     return d_y, d_w
 
 
-def kmoe_quantize_fp8(x, row_of_slot=None, codes=None, scales=None, stream=None):
+def kmoe_quantize_fp8_workspace_size(rows: int, cols: int, k: int = 1) -> int:
+    return _k._lib.kmoe_quantize_fp8_workspace_size(rows, cols, k)
+
+
+def kmoe_quantize_fp8(x, row_of_slot=None, codes=None, scales=None, workspace=None, stream=None):
     """E4M3 codes [rows, cols] and fp32 power-of-two scales [ceil(cols/128), rows]
     of bf16 rows, one scale for 128 columns of a row.  With row_of_slot [T, k]
     token t's row goes to the sorted rows of its slots: codes [T * k, cols]."""
@@ -164,14 +170,25 @@ def kmoe_quantize_fp8(x, row_of_slot=None, codes=None, scales=None, stream=None)
     sf = (-(-H // _BLOCK), T * k)
     at = _args(stream, dev, (("x", x, _BF16, (T, H)), ("row_of_slot", row_of_slot, _I32, (T, k)),
                              ("codes", codes, _U8, (T * k, H)), ("scales", scales, _F32, sf)))
+    n = 0 if row_of_slot is None else _k._lib.kmoe_quantize_fp8_workspace_size(T, H, k)
+    if workspace is not None:
+        _arg(workspace, "workspace", _U8, min_bytes=n)
+        _gpu(stream, workspace=workspace)
     if codes is None:
         codes = _new((T * k, H), _U8, dev, stream)
         at[2] = codes.data_ptr()
     if scales is None:
         scales = _new(sf, _F32, dev, stream)
         at[3] = scales.data_ptr()
-    _check("kmoe_quantize_fp8", _k._lib.kmoe_quantize_fp8(at[0], T, H, at[1], k, at[2], at[3],
-                                                          _raw_stream(dev, stream)))
+    raw = _raw_stream(dev, stream)
+    # freed when the launches are queued: the memory's next user on this stream comes after them
+    scratch = _k._scratch_alloc(n, raw) if n and workspace is None else 0
+    try:
+        _check("kmoe_quantize_fp8", _k._lib.kmoe_quantize_fp8(
+            at[0], T, H, at[1], k, at[2], at[3], scratch or (workspace.data_ptr() if n else None), n, raw))
+    finally:
+        if scratch:
+            _k._scratch_free(scratch)
     return codes, scales
 
 

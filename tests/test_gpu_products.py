@@ -219,7 +219,8 @@ def test_quantize_rows(K, rows, cols):
     same(scales.double(), ref_s, "scales")
 
 
-@pytest.mark.parametrize("T,cols,E,k", [(1, 16, 1, 1), (5, 7168, 8, 4), (33, 528, 7, 3), (400, 144, 9, 2)])
+@pytest.mark.parametrize("T,cols,E,k", [(1, 16, 1, 1), (5, 7168, 8, 4), (33, 528, 7, 3), (400, 144, 9, 2),
+                                        (2049, 144, 40, 16), (1024, 8400, 40, 32)])
 def test_quantize_into_sorted_rows(K, T, cols, E, k):
     x = special(T, T, cols)
     _, row, seg = sorted_rows(T, E, k)
