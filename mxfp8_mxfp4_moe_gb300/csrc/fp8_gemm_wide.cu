@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
           const float f = slot[row] * slot[128 + grp];
 #pragma unroll
           for (int i = 0; i < C::NCH; ++i) {
-            tmem_ld_wait_for16(r[i & 1]);
+            tmem_ld_wait_for(r[i & 1]);
             if (i + 1 < C::NCH)
               tmem_ld_32x32b_x16(t + 16 * (i + 1), r[(i + 1) & 1]);
             else
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
             if (16 * i >= ng) continue;
             uint32_t v[16];
             tmem_ld_32x32b_x16(t + 16 * i, v);
-            tmem_ld_wait_for16(v);
+            tmem_ld_wait_for(v);
             add(i, v, make_float2(f, f));
           }
           release();

@@ -294,20 +294,24 @@ cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, cons
                         static_cast<const int32_t*>(slot_of_row), scales);
 }
 
+// Blocks along the columns for `tiles_down` tiles of rows: about eight an SM.
+static int column_split(int tiles_down, int cols) {
+  const int tiles = (cols + 127) / 128, split = (1216 + tiles_down - 1) / tiles_down;
+  return split < 1 ? 1 : (split < tiles ? split : tiles);
+}
+
 cudaError_t launch_fp8_quant_weights(const void* w, int E, int N, int K, uint8_t* codes, float* scales,
                                      cudaStream_t st) {
-  return launch_chained(fp8_quant_tile_kernel<true>, dim3(E * ((N + 127) / 128), 1), dim3(256), 0, st, true,
+  const int down = E * ((N + 127) / 128);
+  return launch_chained(fp8_quant_tile_kernel<true>, dim3(down, column_split(down, K)), dim3(256), 0, st, true,
                         static_cast<const __nv_bfloat16*>(w), N, K, E, static_cast<const int32_t*>(nullptr), codes,
                         scales);
 }
 
 cudaError_t launch_fp8_quant_cols(const void* x, int rows, int cols, const int32_t* seg, int E, uint8_t* codes,
                                   float* scales, cudaStream_t st) {
-  const int blocks = static_cast<int>(fp8_padded_rows(rows, E) / 128);
-  const int tiles = (cols + 127) / 128;
-  int split = (1216 + blocks - 1) / blocks;  // about eight blocks an SM
-  split = split < 1 ? 1 : (split < tiles ? split : tiles);
-  return launch_chained(fp8_quant_tile_kernel<false>, dim3(blocks, split), dim3(256), 0, st, true,
+  const int down = static_cast<int>(fp8_padded_rows(rows, E) / 128);
+  return launch_chained(fp8_quant_tile_kernel<false>, dim3(down, column_split(down, cols)), dim3(256), 0, st, true,
                         static_cast<const __nv_bfloat16*>(x), rows, cols, E, seg, codes, scales);
 }
 

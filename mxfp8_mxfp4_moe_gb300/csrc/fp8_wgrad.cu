@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(WgradCfg::THREADS, 1) fp8_wgrad_kernel(const _
       for (int c = 16 * half; c < wk.n; c += 32) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(t + c, r);
-        tmem_ld_wait_for16(r);
+        tmem_ld_wait_for(r);
         // (n is a multiple of 16) 32 features of one n a store
         if (f < a.F)
 #pragma unroll

@@ -219,18 +219,25 @@ def test_quantize_rows(K, rows, cols):
     same(scales.double(), ref_s, "scales")
 
 
+# the last two have rows enough for the scales' own pass, of one and of two 64-group chunks
 @pytest.mark.parametrize("T,cols,E,k", [(1, 16, 1, 1), (5, 7168, 8, 4), (33, 528, 7, 3), (400, 144, 9, 2),
-                                        (2049, 144, 40, 16), (1024, 8400, 40, 32)])
+                                        (4100, 144, 40, 16), (2048, 8400, 40, 32)])
 def test_quantize_into_sorted_rows(K, T, cols, E, k):
     x = special(T, T, cols)
     _, row, seg = sorted_rows(T, E, k)
     codes = torch.full((T * k, cols), 99, dtype=U8, device="cuda")
     scales = torch.full((-(-cols // 128), T * k), -3.0, device="cuda")
     K.kmoe_quantize_fp8(x.cuda(), torch.from_numpy(row).cuda(), codes=codes, scales=scales)
-    ref_c, ref_s = P.quantize_rows(f64(x))
+    assert (K.kmoe_quantize_fp8_workspace_size(T, cols, k) > 0) == (T >= 2048)
+    few = slice(None) if T < 2048 else np.r_[0:40, T - 40:T]  # the oracle's loops are slow
+    ref_c, ref_s = P.quantize_rows(f64(x)[few])
+    plain_c, plain_s = K.kmoe_quantize_fp8(x.cuda())  # checked row by row in the test above, and here where `few` says
+    same(plain_c[few], ref_c, "codes by token")
+    same(plain_s.double()[:, few], ref_s, "scales by token")
     want_c, want_s = np.full((T * k, cols), 99, np.uint8), np.full(scales.shape, -3.0)
+    plain_c, plain_s = plain_c.cpu().numpy(), f64(plain_s)
     for t, j in np.argwhere(row >= 0):
-        want_c[row[t, j]], want_s[:, row[t, j]] = ref_c[t], ref_s[:, t]
+        want_c[row[t, j]], want_s[:, row[t, j]] = plain_c[t], plain_s[:, t]
     same(codes, want_c, "codes")
     same(scales.double(), want_s, "scales")
 
@@ -303,7 +310,10 @@ def product_tolerance(ref, mag, n, to):
 PRODUCTS = [(1, 16, 16, 1), (1, 128, 128, 1), (1, 528, 7168, 1), (16, 144, 144, 1), (17, 272, 400, 1), (32, 128, 1024, 1),
             (33, 256, 256, 1), (128, 640, 272, 1), (129, 128, 512, 1), (257, 400, 384, 1), (600, 144, 640, 1),
             (1000, 1040, 256, 1), (1, 144, 144, 5), (40, 272, 400, 8), (200, 144, 528, 3), (333, 256, 128, 64),
-            (700, 128, 272, 2), (1500, 400, 144, 5), (3, 16, 32, 1000)]
+            (700, 128, 272, 2), (1500, 400, 144, 5), (3, 16, 32, 1000),
+            # shared by clusters of 2, 4 and 8; several items a CTA; blocks that leave a cluster's last CTA fewer
+            (5, 2048, 1040, 1), (32, 640, 4112, 1), (20, 4112, 528, 1), (64, 1024, 4096, 1), (200, 3600, 2064, 1),
+            (129, 272, 2176, 1), (2600, 4112, 144, 1), (70, 6160, 144, 40), (4000, 2064, 272, 9)]
 
 
 @pytest.mark.parametrize("transpose", [False, True])
