@@ -248,6 +248,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
     const int grp = (warp - C::CTRL_WARPS) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     uint8_t* const out_smem = smem + C::OUT_OFF + (warp - C::CTRL_WARPS) * 2048;
+    auto release = [&](uint32_t b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[b]);
+    };
     uint32_t it = 0;
     bool ok = true, exchanged = false;
     for (int w = w0; ok && w < total; w += dw) {
@@ -260,51 +265,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
       for (int i = 0; i < C::NCH; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < wk.kn; ++kb, ++it) {
-        const uint32_t b = it % C::NACC;
-        if (!wait_warp(&acc_full[b], (it / C::NACC) & 1u, budget, a.err, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t t = tmem + lanes + b * C::BN + grp * 128;
-        const float* slot = reinterpret_cast<const float*>(smem + C::SC_OFF) + (it & (C::RING - 1)) * C::SLOT;
-        auto add = [&](int i, const uint32_t(&v)[16], float2 f) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[i][j] = __ffma2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f, acc[i][j]);
-        };
-        auto release = [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[b]);
-        };
-        if (ng >= 128) {  // without branches: the values read stay where they are
+      // The blocks of the sum, for whole groups and for ones with fewer features:
+      // two loops, so that neither's registers follow the other's.
+      auto blocks = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        for (int kb = 0; kb < wk.kn; ++kb, ++it) {
+          const uint32_t b = it % C::NACC;
+          if (!wait_warp(&acc_full[b], (it / C::NACC) & 1u, budget, a.err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t t = tmem + lanes + b * C::BN + grp * 128;
+          const float* slot = reinterpret_cast<const float*>(smem + C::SC_OFF) + (it & (C::RING - 1)) * C::SLOT;
           uint32_t r[2][16];
           tmem_ld_32x32b_x16(t, r[0]);
           const float f = slot[row] * slot[128 + grp];
 #pragma unroll
           for (int i = 0; i < C::NCH; ++i) {
+            if (!WHOLE && 16 * i >= ng) continue;
+            if (!WHOLE && i > 0) tmem_ld_32x32b_x16(t + 16 * i, r[i & 1]);
             tmem_ld_wait_for(r[i & 1]);
-            if (i + 1 < C::NCH)
-              tmem_ld_32x32b_x16(t + 16 * (i + 1), r[(i + 1) & 1]);
-            else
-              release();
-            add(i, r[i & 1], make_float2(f, f));
-          }
-        } else {
-          const float f = slot[row] * slot[128 + grp];
+            if (WHOLE && i + 1 < C::NCH) tmem_ld_32x32b_x16(t + 16 * (i + 1), r[(i + 1) & 1]);
+            if (WHOLE && i + 1 == C::NCH) release(b);
 #pragma unroll
-          for (int i = 0; i < C::NCH; ++i) {
-            if (16 * i >= ng) continue;
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(t + 16 * i, v);
-            tmem_ld_wait_for(v);
-            add(i, v, make_float2(f, f));
+            for (int j = 0; j < 8; ++j)
+              acc[i][j] = __ffma2_rn(make_float2(__uint_as_float(r[i & 1][2 * j]), __uint_as_float(r[i & 1][2 * j + 1])),
+                                     make_float2(f, f), acc[i][j]);
           }
-          release();
+          if (!WHOLE) {
+            tmem_ld_wait_for(r[0]);
+            release(b);
+          }
         }
-      }
+      };
+      if (ng >= 128)
+        blocks(std::true_type{});
+      else
+        blocks(std::false_type{});
       if (!ok) break;
       // Rows go out by way of shared memory, 64 bytes of each at a time: a
       // store covers eight rows' pieces instead of 32 rows' 16 bytes.  The
