@@ -36,7 +36,10 @@ __host__ inline long long fp8_most_tiles(long long M, int E, int per) {
   const long long with = M < E ? M : E;  // experts that can have rows
   return (M + (per - 1) * with) / per;
 }
-// Whether M rows of E experts are few for each, fp8_gemm.cu's; else fp8_gemm_wide.cu's.
+// Whether M rows of E experts are few for each, fp8_gemm.cu's; else
+// fp8_gemm_wide.cu's.  On the GPU, weights of 7168 x 7168: 32 rows of one take
+// 11.4 us there (33 to 64: 16.5 in tiles of 128); 256 rows of 8 experts of
+// 7168 x 3584 39, 320 rows 42 in tiles of 128.
 __host__ inline bool fp8_few_rows(int M, int E) { return (M + E - 1) / E <= 32; }
 // Rows of a TMA box of the rows: tiles of up to 32 are cut to multiples of 16
 // (a copy takes the time of its rows), those of many are 128.

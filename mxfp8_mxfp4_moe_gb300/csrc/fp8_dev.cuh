@@ -65,7 +65,10 @@ __device__ __forceinline__ float2 ld_shared_cluster_f2(uint32_t cluster_addr) {
 
 // CTAs of a cluster that share an item where `items` (at most) are too few for
 // the CTAs that can run at once: up to eight, with `least` blocks of the sum for
-// each.  Such a cluster has one item, and its CTAs meet once.
+// each.  Such a cluster has one item, and its CTAs meet once.  One row, 7168 x
+// 7168: clusters of 1, 2 and 4 take 21.5, 13.8 and 10.6 us.  fp8_gemm.cu's tiles
+// want four blocks for each CTA, fp8_gemm_wide.cu's eight: their exchange is
+// eight times larger (128 rows, 4096 x 4096: four blocks each 25 us, eight 12.5).
 __host__ inline int product_split(long long items, int resident, int KB, int least) {
   int split = 1;
   while (split < 8 && items * split * 2 <= resident && KB >= 2 * least * split) split *= 2;
@@ -93,6 +96,14 @@ __host__ inline cudaError_t launch_product(Kernel kernel, int threads, int smem,
   cfg.attrs = at;
   cfg.numAttrs = a.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
+// Work items of the segments' tiles for `clusters` clusters.  A table whose
+// segments overlap can hold more than the launch counted on; a cluster that
+// shares an item takes one even then, as its CTAs meet once.
+__device__ __forceinline__ int product_items(const Fp8Args& a, const int32_t* unit, int clusters) {
+  const int total = a.FT * unit[a.E];
+  return a.split > 1 ? min(total, clusters) : total;
 }
 
 // A work item: features f0 .. of expert e for the columns (rows of the batch)

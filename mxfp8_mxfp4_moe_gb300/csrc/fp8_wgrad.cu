@@ -24,13 +24,18 @@
 // Roles in each CTA: warp 0 TMA, warp 1 MMA (the even CTA's, for both), warps 2
 // and 3 the scales, warps 4 .. 11 the stores.  Loads complete on the even CTA's
 // barriers, commits arrive at both CTAs'.  Every wait is bounded.
+//
+// 16384 rows of 16 experts, 7168 x 3584: 463 us, 1820 TFLOP/s and 1.6 GB of
+// stores; without the stores 360, without the loads 347, without both 283 (the
+// products and the scales' copies).  One CTA a tile 569, the accumulators read
+// and scaled for each block instead 1411.
 #include "fp8_dev.cuh"
 
 namespace kmoe {
 
 struct WgradCfg {
   static constexpr int BN = kWeightGradColumns;
-  static constexpr int KPS = 2;  // blocks a stage
+  static constexpr int KPS = 1;  // blocks a stage (two: 473 us where one takes 463)
   static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // a block's 128 features k, and a box of n
   static constexpr int STAGE = KPS * (A_BYTES + B_BYTES);
   static constexpr int STAGES = 192 * 1024 / STAGE;

@@ -397,6 +397,84 @@ def test_segment_tables_that_lie_stay_inside(K):
         no_error(K, work)
 
 
+@pytest.mark.parametrize("M,N,Kd,E", [(100, 128, 4096, 512), (300, 256, 4096, 8)])
+def test_overlapping_segments_end(K, M, N, Kd, E):
+    """More tiles than any ascending table gives, where clusters share items."""
+    x, xs = K.kmoe_quantize_fp8(randn(1, M, Kd).to(BF).cuda())
+    w, ws = K.kmoe_quantize_fp8_weights(randn(2, 1, N, Kd).to(BF).cuda())
+    seg = torch.tensor([0, M] * E, dtype=I32, device="cuda")[:E + 1].contiguous()
+    out, work = K.kmoe_gemm_fp8(x, xs, w.repeat(E, 1, 1), ws.repeat(E, 1, 1), seg, out_dtype=F32)
+    no_error(K, work)
+    # every expert has the same weights, and the first one's tiles come first
+    ref, mag = P.gemm(P.values_rows(x.cpu().numpy(), xs.cpu().numpy()),
+                      P.values_weights(w.cpu().numpy(), ws.cpu().numpy()), [0, M])
+    within(out, ref, product_tolerance(ref, mag, Kd, F32), "out")
+
+
+def test_weight_gradient_of_many_rows(K):
+    rows, N, Kd = 65536, 144, 128
+    dy, x = randn(1, rows, N).to(BF).cuda(), randn(2, rows, Kd).to(BF).cuda()
+    qd, qx = K.kmoe_quantize_fp8_cols(dy), K.kmoe_quantize_fp8_cols(x)
+    dw, work = K.kmoe_gemm_fp8_wgrad(*qd, *qx)
+    no_error(K, work)
+    ref, mag = P.wgrad(*(P.values_cols(c.cpu().numpy(), s.cpu().numpy()) for c, s in (qd, qx)), [0, rows])
+    within(dw, ref, product_tolerance(ref, mag, rows, F32), "dw")
+
+
+def test_products_past_2_31_elements(K):
+    M, N, Kd = 140000, 16384, 128  # M * N > 2^31
+    last = M // 64 * 64  # these rows are the first ones again
+    x = randn(1, 64, Kd).to(BF).cuda().repeat(-(-M // 64), 1)[:M].contiguous()
+    w, ws = K.kmoe_quantize_fp8_weights(randn(2, 1, N, Kd).to(BF).cuda())
+    wv = P.values_weights(w.cpu().numpy(), ws.cpu().numpy())
+    xc, xs = K.kmoe_quantize_fp8(x)
+    out, work = K.kmoe_gemm_fp8(xc, xs, w, ws)
+    no_error(K, work)
+    assert torch.equal(out[last:last + 16], out[:16])
+    ref, mag = P.gemm(P.values_rows(xc[:16].cpu().numpy(), xs[:, :16].cpu().numpy()), wv, [0, 16])
+    within(out[:16], ref, product_tolerance(ref, mag, Kd, BF), "out")
+    # and back: rows of codes past 2^31
+    fc, fs = K.kmoe_quantize_fp8(out[:16].contiguous())
+    oc, osc = K.kmoe_quantize_fp8(out)
+    del out
+    for at in (0, last):
+        assert torch.equal(oc[at:at + 16], fc) and torch.equal(osc[:, at:at + 16], fs)
+    back, work = K.kmoe_gemm_fp8(oc, osc, w, ws, transpose=True, out_dtype=F32, workspace=work)
+    no_error(K, work)
+    assert torch.equal(back[last:last + 16], back[:16])
+    ref, mag = P.gemm(P.values_rows(fc.cpu().numpy(), fs.cpu().numpy()), wv, [0, 16], transpose=True)
+    within(back[:16], ref, product_tolerance(ref, mag, N, F32), "back")
+
+
+@pytest.mark.parametrize("rows", [900, 30000])
+def test_weights_past_2_31_elements(K, rows):
+    E, N, Kd = 300, 4096, 2048  # E * N * K > 2^31
+    seg = segments(rows, rows, E, behind=0)
+    w = torch.randint(0, 0x7F, (E, N, Kd), dtype=U8, device="cuda")  # no NaN codes
+    ws = torch.rand(E, N // 128, Kd // 128, device="cuda")
+    xc, xs = K.kmoe_quantize_fp8(randn(1, rows, Kd).to(BF).cuda())
+    out, work = K.kmoe_gemm_fp8(xc, xs, w, ws, torch.from_numpy(seg).cuda(), out_dtype=F32)
+    no_error(K, work)
+    for e in np.flatnonzero(np.diff(seg))[[0, -1]]:
+        a, b = seg[e], min(seg[e + 1], seg[e] + 4)
+        v = P.values_rows(xc[a:b].cpu().numpy(), xs[:, a:b].cpu().numpy())
+        ref, mag = P.gemm(v, P.values_weights(w[e:e + 1].cpu().numpy(), ws[e:e + 1].cpu().numpy()), [0, b - a])
+        within(out[a:b], ref, product_tolerance(ref, mag, Kd, F32), f"expert {e}")
+    del out
+    # and their gradient, as large
+    dc, ds = K.kmoe_quantize_fp8_cols(randn(2, rows, N).to(BF).cuda(), torch.from_numpy(seg).cuda())
+    qc, qs = K.kmoe_quantize_fp8_cols(randn(3, rows, Kd).to(BF).cuda(), torch.from_numpy(seg).cuda())
+    dw, work = K.kmoe_gemm_fp8_wgrad(dc, ds, qc, qs, seg_start=torch.from_numpy(seg).cuda())
+    no_error(K, work)
+    blocks = np.concatenate([[0], np.cumsum(-(-np.diff(seg) // 128))])
+    for e in np.flatnonzero(np.diff(seg))[[0, -1]]:
+        at, sb = slice(blocks[e] * 128, blocks[e + 1] * 128), slice(blocks[e], blocks[e + 1])
+        vd = P.values_cols(dc[at, :256].cpu().numpy(), ds[sb, :256].cpu().numpy())
+        vx = P.values_cols(qc[at].cpu().numpy(), qs[sb].cpu().numpy())
+        ref, mag = P.wgrad(vd, vx, [0, seg[e + 1] - seg[e]])
+        within(dw[e:e + 1, :256], ref, product_tolerance(ref, mag, seg[e + 1] - seg[e] + 128, F32), f"dw {e}")
+
+
 # ---------------------------------------------------------------- together
 
 
