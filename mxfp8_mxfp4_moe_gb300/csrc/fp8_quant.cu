@@ -10,13 +10,14 @@
 //   fp8_quant_scatter_kernel  the same, each token's row once, written to the
 //                             expert-sorted rows of its k slots
 //   fp8_sort_scales_kernel    the scales of those rows, where they are many
-//   fp8_quant_tile_kernel     128 rows of one column (the sum of the weights'
+//   fp8_quant_cols_kernel     128 rows of one column (the sum of the weights'
 //                             gradient; every expert's rows from a multiple of
-//                             128 on, zeros behind them), or 128 x 128 weights
+//                             128 on, zeros behind them)
+//   fp8_quant_weights_kernel  128 x 128 weights
 //
 // Bound by HBM where rows are many: 32768 x 7168 rows 104 us (6.8 TB/s), 8192
-// tokens into 16 rows each 174 us (6.2 TB/s), 16384 x 7168 by columns 73 us
-// (4.8 TB/s), weights 4 x 7168 x 7168 97 us (6.4 TB/s).
+// tokens into 16 rows each 174 us (6.2 TB/s), 16384 x 7168 by columns 60 us
+// (5.9 TB/s), weights 4 x 7168 x 7168 92 us (6.7 TB/s).
 #include "fp8.cuh"
 #include "mx_dev.cuh"
 
@@ -158,38 +159,20 @@ __global__ void __launch_bounds__(256) fp8_sort_scales_kernel(const float* __res
   }
 }
 
-// One tile of 128 rows x 128 columns a step: 16 lanes of 8 columns by 16 rows,
-// eight rows a thread.  WEIGHTS: one scale for the tile, blockIdx.x = expert
-// and row tile; else one for each column, blockIdx.x = a block of 128 rows of
-// the padded order.
-template <bool WEIGHTS>
-__global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const __nv_bfloat16* __restrict__ x, int rows, int cols,
-                                                             int E, const int32_t* __restrict__ seg,
-                                                             uint8_t* __restrict__ codes,
-                                                             float* __restrict__ scales) {
+// One tile of 128 rows x 128 columns of weights a step, with one scale: 16 lanes
+// of 8 columns by 16 rows, eight rows a thread.  blockIdx.x = expert and row
+// tile.
+__global__ void __launch_bounds__(256) fp8_quant_weights_kernel(const __nv_bfloat16* __restrict__ w, int rows, int cols,
+                                                                uint8_t* __restrict__ codes,
+                                                                float* __restrict__ scales) {
   chain_wait();
-  __shared__ int32_t first[WEIGHTS ? 1 : kMaxE + 1], unit[WEIGHTS ? 1 : kMaxE + 1], tmp[33];
-  __shared__ uint32_t s_max[8][128];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ uint32_t s_max[8];
+  const int warp = threadIdx.x >> 5;
   const int cg = threadIdx.x & 15, r0 = threadIdx.x >> 4;
-  long long src, dst;  // first row of the tile in x and in codes
-  int n, nd;           // rows it has in x, and in codes
-  if constexpr (WEIGHTS) {
-    const int tiles = (rows + 127) / 128;
-    const int e = blockIdx.x / tiles, i = blockIdx.x % tiles;
-    src = dst = static_cast<long long>(e) * rows + i * 128;
-    n = nd = min(128, rows - i * 128);
-  } else {
-    segment_prefix(seg, E, rows, 128, first, unit, tmp);
-    const int b = blockIdx.x;
-    if (b >= unit[E]) return;
-    const int e = segment_of_unit(unit, E, b);
-    const int at = (b - unit[e]) * 128;
-    src = first[e] + at;
-    dst = static_cast<long long>(b) * 128;
-    n = min(128, first[e + 1] - first[e] - at);
-    nd = 128;
-  }
+  const int tiles = (rows + 127) / 128;
+  const int e = blockIdx.x / tiles, i0 = blockIdx.x % tiles * 128;
+  const long long src = static_cast<long long>(e) * rows + i0;
+  const int n = min(128, rows - i0);
   for (int c0 = blockIdx.y * 128; c0 < cols; c0 += gridDim.y * 128) {
     const int col = c0 + cg * 8;
     uint4 v[8];
@@ -197,76 +180,118 @@ __global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const __nv_bfloat16
     for (int i = 0; i < 8; ++i) {
       const int r = r0 + 16 * i;
       v[i] = make_uint4(0, 0, 0, 0);
-      if (r < n && col < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(x + (src + r) * cols + col));
+      if (r < n && col < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(w + (src + r) * cols + col));
     }
-    // largest magnitudes of the thread's columns, two a word, then over the two rows of a warp
-    __nv_bfloat162 m[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = __float2bfloat162_rn(0.f);
+    uint32_t a = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (bf16_amax_nan(v[i]) > 0x7F80u) v[i] = bf16_drop_nan(v[i]);
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m[j] = __hmax2(m[j], __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
+      uint32_t m = bf16_amax_nan(v[i]);
+      if (m > 0x7F80u) {
+        v[i] = bf16_drop_nan(v[i]);
+        m = bf16x2_amax(v[i]);
+      }
+      a = max(a, m);
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = __hmax2(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+    a = __reduce_max_sync(0xffffffffu, a);
     __syncthreads();
-    if (lane < 16)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(&m[j]);
-        s_max[warp][cg * 8 + 2 * j] = u & 0xFFFFu;
-        s_max[warp][cg * 8 + 2 * j + 1] = u >> 16;
-      }
+    if ((threadIdx.x & 31) == 0) s_max[warp] = a;
     __syncthreads();
-    if (threadIdx.x < 128) {
-      uint32_t a = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) a = max(a, s_max[w][threadIdx.x]);
-      if constexpr (WEIGHTS) a = __reduce_max_sync(0xffffffffu, a);
-      s_max[0][threadIdx.x] = a;
+    for (int u = 0; u < 8; ++u) a = max(a, s_max[u]);
+    const uint32_t byte = fp8_scale_byte(a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 16 * i;
+      if (r < n && col < cols)
+        *reinterpret_cast<uint2*>(codes + (src + r) * cols + col) = e4m3_chunk(v[i], byte);
     }
-    __syncthreads();
-    if constexpr (WEIGHTS) {
-      const uint32_t a = max(max(s_max[0][0], s_max[0][32]), max(s_max[0][64], s_max[0][96]));
-      const uint32_t byte = fp8_scale_byte(a);
+    if (threadIdx.x == 0)
+      scales[static_cast<long long>(blockIdx.x) * ((cols + 127) / 128) + c0 / 128] = fp8_scale(byte);
+  }
+}
+
+// A block takes 128 rows x 128 columns a step, a scale for each column: a lane
+// four columns, a warp kColRows rows, all of them in registers and in flight at
+// once; one exchange of the columns' largest stands between loads and stores.
+// blockIdx.x = a block of 128 rows of the padded order.  Eight warps of 16 rows,
+// four blocks an SM; 4095 x 7168: 13.7 us, 16384 x 7168: 60 (four warps of 32
+// rows 14.4 and 69, sixteen of eight 19.6 and 73; 64 rows of 64 columns a half
+// warp, without the barrier, 15.7 and 67).
+constexpr int kColWarps = 8, kColRows = 128 / kColWarps;
+__global__ void __launch_bounds__(32 * kColWarps, 4) fp8_quant_cols_kernel(
+    const __nv_bfloat16* __restrict__ x, int rows, int cols, int E, const int32_t* __restrict__ seg,
+    uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  chain_wait();
+  __shared__ int32_t first[kMaxE + 1], unit[kMaxE + 1], tmp[33];
+  __shared__ uint2 s_max[2][kColWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  segment_prefix(seg, E, rows, 128, first, unit, tmp);
+  const int b = blockIdx.x;
+  if (b >= unit[E]) return;
+  const int e = segment_of_unit(unit, E, b);
+  const int at = (b - unit[e]) * 128, r0 = kColRows * warp;
+  const int n = min(128, first[e + 1] - first[e] - at) - r0;  // rows that are there from r0 on
+  const long long src = first[e] + at + r0, dst = static_cast<long long>(b) * 128 + r0;
+  int turn = 0;
+  for (int c0 = blockIdx.y * 128; c0 < cols; c0 += gridDim.y * 128) {
+    const int col = c0 + lane * 4;
+    const bool in = col < cols;
+    uint2 v[kColRows];
+    const __nv_bfloat16* p = x + src * cols + col;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        if (r < nd && col < cols)
-          *reinterpret_cast<uint2*>(codes + (dst + r) * cols + col) = e4m3_chunk(v[i], byte);
+    for (int i = 0; i < kColRows; ++i) {
+      v[i] = make_uint2(0, 0);
+      if (in && i < n) v[i] = __ldg(reinterpret_cast<const uint2*>(p + static_cast<long long>(i) * cols));
+    }
+    // largest magnitudes of the four columns, two a word (as integers, so that NaN shows)
+    auto largest = [&] {
+      uint2 m = make_uint2(0, 0);
+#pragma unroll
+      for (int i = 0; i < kColRows; ++i) {
+        m.x = __vmaxu2(m.x, v[i].x & 0x7FFF7FFFu);
+        m.y = __vmaxu2(m.y, v[i].y & 0x7FFF7FFFu);
       }
-      if (threadIdx.x == 0)
-        scales[static_cast<long long>(blockIdx.x) * ((cols + 127) / 128) + c0 / 128] = fp8_scale(byte);
-    } else if (col < cols) {
-      // eight columns with scales of their own
-      uint32_t byte[8];
-      float inv[8];  // 1 / s: a power of two, so x / s is exact
+      turn ^= 1;  // the other half of s_max was read before the last barrier
+      s_max[turn][warp][lane] = m;
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        byte[j] = fp8_scale_byte(s_max[0][cg * 8 + j]);
-        inv[j] = exp2i(127 - static_cast<int>(byte[j]));
+      for (int w = 0; w < kColWarps; ++w) {
+        const uint2 o = s_max[turn][w][lane];
+        m.x = __vmaxu2(m.x, o.x);
+        m.y = __vmaxu2(m.y, o.y);
       }
+      return m;
+    };
+    uint2 m = largest();
+    const uint32_t top = __vmaxu2(m.x, m.y);
+    if (__any_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16) > 0x7F80u)) {  // the same in every warp
+      auto drop = [](uint32_t w) {
+        return ((w & 0x7FFFu) > 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7FFF0000u) > 0x7F800000u ? 0u : w & 0xFFFF0000u);
+      };
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t pair[4];
+      for (int i = 0; i < kColRows; ++i) v[i] = make_uint2(drop(v[i].x), drop(v[i].y));
+      m = largest();
+    }
+    if (!in) continue;
+    const uint32_t amax[4] = {m.x & 0xFFFFu, m.x >> 16, m.y & 0xFFFFu, m.y >> 16};
+    float inv[4];  // 1 / s: a power of two, so x / s is exact
+    float* s = scales + static_cast<long long>(b) * cols + col;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float lo = __uint_as_float(w[j] << 16) * inv[2 * j];
-          const float hi = __uint_as_float(w[j] & 0xFFFF0000u) * inv[2 * j + 1];
-          pair[j] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-        }
-        *reinterpret_cast<uint2*>(codes + (dst + r0 + 16 * i) * cols + col) =
-            make_uint2(pair[0] | (pair[1] << 16), pair[2] | (pair[3] << 16));
-      }
-      if (r0 == 0) {
-        float* s = scales + static_cast<long long>(blockIdx.x) * cols + col;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t byte = fp8_scale_byte(amax[j]);
+      inv[j] = exp2i(127 - static_cast<int>(byte));
+      if (warp == 0) s[j] = fp8_scale(byte);
+    }
+    uint8_t* q = codes + dst * cols + col;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = fp8_scale(byte[j]);
-      }
+    for (int i = 0; i < kColRows; ++i) {
+      auto two = [](uint32_t w, float lo, float hi) {
+        return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+            make_float2(__uint_as_float(w << 16) * lo, __uint_as_float(w & 0xFFFF0000u) * hi), __NV_SATFINITE,
+            __NV_E4M3));
+      };
+      *reinterpret_cast<uint32_t*>(q + static_cast<long long>(i) * cols) =
+          two(v[i].x, inv[0], inv[1]) | two(v[i].y, inv[2], inv[3]) << 16;
     }
   }
 }
@@ -299,7 +324,8 @@ cudaError_t launch_fp8_quant_scatter(const void* x, int T, int cols, int k, cons
 }
 
 // Blocks along the columns for `tiles_down` tiles of rows: about eight an SM
-// (weights 4 x 7168 x 7168: 97 us, with one for all of the columns 139).
+// (weights 4 x 7168 x 7168: 92 us, with one for all of the columns 139; 16384 x
+// 7168 by columns of 16 experts: 60 us, with four an SM 66, with sixteen 60).
 static int column_split(int tiles_down, int cols) {
   const int tiles = (cols + 127) / 128, split = (1216 + tiles_down - 1) / tiles_down;
   return split < 1 ? 1 : (split < tiles ? split : tiles);
@@ -308,16 +334,15 @@ static int column_split(int tiles_down, int cols) {
 cudaError_t launch_fp8_quant_weights(const void* w, int E, int N, int K, uint8_t* codes, float* scales,
                                      cudaStream_t st) {
   const int down = E * ((N + 127) / 128);
-  return launch_chained(fp8_quant_tile_kernel<true>, dim3(down, column_split(down, K)), dim3(256), 0, st, true,
-                        static_cast<const __nv_bfloat16*>(w), N, K, E, static_cast<const int32_t*>(nullptr), codes,
-                        scales);
+  return launch_chained(fp8_quant_weights_kernel, dim3(down, column_split(down, K)), dim3(256), 0, st, true,
+                        static_cast<const __nv_bfloat16*>(w), N, K, codes, scales);
 }
 
 cudaError_t launch_fp8_quant_cols(const void* x, int rows, int cols, const int32_t* seg, int E, uint8_t* codes,
                                   float* scales, cudaStream_t st) {
   const int down = static_cast<int>(fp8_padded_rows(rows, E) / 128);
-  return launch_chained(fp8_quant_tile_kernel<false>, dim3(down, column_split(down, cols)), dim3(256), 0, st, true,
-                        static_cast<const __nv_bfloat16*>(x), rows, cols, E, seg, codes, scales);
+  return launch_chained(fp8_quant_cols_kernel, dim3(down, column_split(down, cols)), dim3(32 * kColWarps), 0, st,
+                        true, static_cast<const __nv_bfloat16*>(x), rows, cols, E, seg, codes, scales);
 }
 
 }  // namespace kmoe
