@@ -331,6 +331,12 @@ def test_gemm(K, M, N, Kd, E, transpose):
         within(out, ref, product_tolerance(ref, mag, n, to), f"{to}")
 
 
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("M,N,Kd", [(1, 32, 131072), (2, 131072, 144), (40, 32, 65552), (130, 65552, 48)])
+def test_long_products(K, M, N, Kd, transpose):
+    test_gemm(K, M, N, Kd, 1, transpose)
+
+
 @pytest.mark.parametrize("rows,N,Kd,E", [(1, 16, 16, 1), (128, 128, 128, 1), (300, 272, 144, 1), (1000, 144, 400, 1),
                                          (129, 528, 128, 1), (300, 144, 272, 4), (77, 16, 144, 100), (900, 384, 256, 3)])
 def test_wgrad(K, rows, N, Kd, E):
@@ -558,3 +564,36 @@ def test_calls_on_a_stream_and_in_a_graph(K):
     torch.cuda.synchronize()
     for a, b in zip(captured, want):
         assert torch.equal(a, b)
+
+
+def test_calls_at_once(K):
+    """Products, gradients and moves on two streams, each call with its own workspace."""
+    x, d = randn(1, 600, 1040).to(BF).cuda(), randn(2, 600, 528).to(BF).cuda()
+    wc, ws = K.kmoe_quantize_fp8_weights(randn(3, 1, 528, 1040).to(BF).cuda())
+    ids = torch.from_numpy(routing(4, 600, 9, 4, 0.1)).cuda()
+    tw = torch.softmax(randn(5, 600, 4), 1).cuda()
+
+    def run():
+        xc, xs = K.kmoe_quantize_fp8(x)
+        few, w1 = K.kmoe_gemm_fp8(xc[:7].contiguous(), xs[:, :7].contiguous(), wc, ws)
+        many, w2 = K.kmoe_gemm_fp8(xc, xs, wc, ws)
+        dw, w3 = K.kmoe_gemm_fp8_wgrad(*K.kmoe_quantize_fp8_cols(d), *K.kmoe_quantize_fp8_cols(x))
+        row, _, _ = K.kmoe_sort_tokens(ids, 9)
+        xp = K.kmoe_permute(x, row, out=torch.zeros(2400, 1040, dtype=BF, device="cuda"))
+        return [few, many, dw, row, K.kmoe_unpermute(xp, row, tw)], [w1, w2, w3]
+
+    want, _ = run()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(run())
+    torch.cuda.synchronize()
+    for outs, works in got:
+        for w in works:
+            no_error(K, w)
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
