@@ -138,8 +138,9 @@ int kmoe_gemm_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, con
  * writes them for the same rows and seg_start, P a multiple of 128 (a scale that
  * is no normal power of two makes its row or column of dw NaN); dw [E, N, K]
  * float (out, every element: an expert without rows gets zeros, P = 0 included).
- * The tensor cores sum all of an expert's rows, in fp32 whose additions may
- * truncate.  Workspace as kmoe_gemm_fp8; the error word is cleared by every call. */
+ * The tensor cores sum up to 1024 rows, in fp32 whose additions may truncate;
+ * those sums are added in fp32, in order.  Workspace as kmoe_gemm_fp8; the error
+ * word is cleared by every call. */
 int kmoe_gemm_fp8_wgrad(const uint8_t* dy, const float* dy_scales, const uint8_t* x, const float* x_scales,
                         const int32_t* seg_start, int P, int N, int K, int E, float* dw, void* workspace,
                         size_t ws_bytes, cudaStream_t stream);
