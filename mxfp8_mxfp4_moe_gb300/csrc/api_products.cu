@@ -120,8 +120,8 @@ int kmoe_unpermute_backward(const void* d_out, const void* y, const int32_t* row
 
 size_t kmoe_quantize_fp8_workspace_size(int rows, int cols, int k) {
   if (check_slots(rows, k) != KMOE_OK || check_cols(cols) != KMOE_OK) return 0;
-  // from where the sorted scales in a pass of their own are worth its launch (7168 columns, without / with it: R = 131072
-  // 217 / 174 us, 65536 102 / 97, 32768 (k = 8, 16) 52 / 50 and 44 / 46, 16384 27 / 28, 8184 11.4 / 13.6)
+  // from where the sorted scales in a pass of their own are worth its launch (7168 columns, without / with it:
+  // R = 131072 217 / 174 us, 65536 102 / 97, 32768 (k = 8, 16) 52 / 50 and 44 / 46, 16384 27 / 28, 8184 11.4 / 13.6)
   const long long R = static_cast<long long>(rows) * k;
   if (k == 1 || R < 65536) return 0;
   return align_up((static_cast<size_t>(rows) * blocks_of(cols) + static_cast<size_t>(R)) * 4, 256);

@@ -597,3 +597,39 @@ def test_calls_at_once(K):
             no_error(K, w)
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
+
+
+def test_rows_that_are_none(K):
+    """Entries of row_of_slot outside the rows count as -1 in every call."""
+    T, H, E, k = 70, 144, 6, 3
+    _, row, _ = sorted_rows(T, E, k, 0.2)
+    bad = row.copy()
+    none = np.argwhere(row < 0)
+    assert len(none) >= 4
+    for (t, j), v in zip(none, [T * k, 2 ** 31 - 1, -2 ** 31, -7] * len(none)):
+        bad[t, j] = v
+    r, b = torch.from_numpy(row).cuda(), torch.from_numpy(bad).cuda()
+    x, y, w = randn(1, T, H).to(BF).cuda(), randn(2, T * k, H).to(BF).cuda(), randn(3, T, k).cuda()
+
+    def run(rows):
+        out = torch.zeros_like(y)
+        d_y = torch.zeros_like(y)
+        q = torch.zeros(T * k, H, dtype=U8, device="cuda"), torch.zeros(2, T * k, device="cuda")
+        K.kmoe_permute(x, rows, out=out)
+        K.kmoe_quantize_fp8(x, rows, codes=q[0], scales=q[1])
+        return [out, K.kmoe_unpermute(y, rows, w), *K.kmoe_unpermute_backward(x, y, rows, w, d_y=d_y), *q]
+
+    for got, want in zip(run(b), run(r)):
+        assert torch.equal(got, want)
+
+
+def test_quantize_into_many_sorted_rows_without_a_workspace(K):
+    T, cols, E, k = 4100, 144, 40, 16
+    x = special(T, T, cols).cuda()
+    _, row, seg = sorted_rows(T, E, k)
+    r, n = torch.from_numpy(row).cuda(), int(seg[E])
+    codes, scales = K.kmoe_quantize_fp8(x, r)
+    c2, s2 = torch.empty_like(codes), torch.empty_like(scales)
+    st = torch.cuda.current_stream().cuda_stream
+    assert K._lib.kmoe_quantize_fp8(x.data_ptr(), T, cols, r.data_ptr(), k, c2.data_ptr(), s2.data_ptr(), None, 0, st) == 0
+    assert torch.equal(c2[:n], codes[:n]) and torch.equal(s2[:, :n], scales[:, :n])
