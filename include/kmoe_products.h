@@ -117,7 +117,12 @@ int kmoe_quantize_fp8_cols(const void* x_bf16, int rows, int cols, const int32_t
  *   out[m, k] = sum_b x_scales[b, m] * w_scales[e, b, k/128] *
  *               sum_{n in block b of 128} x[m, n] * w[e, n, k].
  * A block's products are summed by the tensor cores, the scaled blocks in fp32
- * in the order of b; out is rounded once.  Scales are any fp32 values.
+ * in the order of b; out is rounded once.  Scales are any fp32 values whose
+ * product, which is taken first, is a normal fp32 number or 0.  Below 2^-126 it
+ * loses bits, by which a block is off by up to 2^-125 (kmoe_quantize_fp8's
+ * smallest scale, 2^-126, is that of zeros, which stay exact, and of values below
+ * 2^-117); from 2^128 on it is an infinity, and so is the block, or NaN where its
+ * sum is 0.
  *   x [M, K] (transposed: [M, N]) codes, x_scales [ceil(cols/128), M] float
  *   (kmoe_quantize_fp8's); w [E, N, K] codes, w_scales [E, ceil(N/128),
  *   ceil(K/128)] float (kmoe_quantize_fp8_weights', or a checkpoint's);

@@ -8,7 +8,12 @@
 //
 // A block's inner sum is four tcgen05.mma (kind::f8f6f4, K = 32) into a fresh
 // TMEM accumulator; the epilogue warps read it while the next block's runs in
-// another accumulator, multiply by the two scales and add in fp32 registers.
+// another accumulator, multiply by the product of the two scales and add in fp32
+// registers.  That product may leave fp32's normal range, which the header says;
+// finding such blocks in the epilogue and giving them their scales one after the
+// other was measured at 3 to 25 % of fp8_gemm_wide.cu's time for every call (each
+// read of shared memory, vote or register more lengthens the accumulators'
+// hand-over) and 1 to 4 % here.
 // The features f are the MMA's M, the rows its N (16 .. BN), so that a few
 // rows cost few columns.  Operands that are contiguous along the sum are
 // K-major; transposed weights are read as they lie in memory, MN-major
