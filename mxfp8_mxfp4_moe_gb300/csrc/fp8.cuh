@@ -27,7 +27,8 @@ struct Fp8Args {
   int KB;          // blocks of the sum (weight gradient: blocks there are)
   int ldb;
   int f32;         // out is fp32, else bf16
-  int split;       // CTAs of a cluster that share an item's blocks (fp8_gemm.cu; set at the launch)
+  int split;       // CTAs of a cluster that share an item's blocks (products; set at the launch, as is
+  int items;       // the most work items that an ascending table gives)
 };
 
 // Tiles of up to `per` rows that M rows of E experts can have, whatever the
@@ -72,15 +73,22 @@ __device__ __forceinline__ int segment_start(const int32_t* seg, int e, int M) {
   return seg == nullptr ? (e == 0 ? 0 : M) : min(max(__ldg(seg + e), 0), M);
 }
 
+// Units that are counted: more than an ascending table can have, and a sum of two
+// fits an int.  Tables whose segments overlap can hold more, which are left out.
+constexpr int kMaxUnits = (1 << 30) - 1;
+__host__ __device__ __forceinline__ int add_units(int a, int b) { return a + b < kMaxUnits ? a + b : kMaxUnits; }
+
 // Shared-memory prefixes over the experts, for all threads of a block:
-// first[e] = expert e's first row (held in [0, M]), unit[e] = units before it,
-// a unit being up to `per` rows; both with E + 1 entries.  `tmp` holds 33 ints.
+// first[e] = expert e's first row (held in [0, M]), unit[e] = units before it (at
+// most kMaxUnits), a unit being up to `per` rows, 32 at least; both with E + 1
+// entries.  `tmp` holds 33 ints.
 __device__ __forceinline__ void segment_prefix(const int32_t* seg, int E, int M, int per, int32_t* first,
                                                int32_t* unit, int32_t* tmp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   for (int e = threadIdx.x; e <= E; e += blockDim.x) first[e] = segment_start(seg, e, M);
   __syncthreads();
-  // chunks of 32 experts: prefixes inside, then over the (at most 32) chunks
+  // chunks of 32 experts: prefixes inside (of at most 2^30 / 32 units each), then
+  // over the (at most 32) chunks
   const int chunks = (E + 31) / 32;
   for (int c = warp; c < chunks; c += nw) {
     const int e = c * 32 + lane;
@@ -97,22 +105,22 @@ __device__ __forceinline__ void segment_prefix(const int32_t* seg, int E, int M,
   __syncthreads();
   if (warp == 0) {
     int v = lane < chunks ? tmp[lane] : 0;
-    const int own = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, v, off);
-      if (lane >= off) v += u;
+      if (lane >= off) v = add_units(v, u);
     }
-    if (lane < chunks) tmp[lane] = v - own;
+    v = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane < chunks) tmp[lane] = lane > 0 ? v : 0;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) unit[e + 1] += tmp[e >> 5];
+  for (int e = threadIdx.x; e < E; e += blockDim.x) unit[e + 1] = add_units(unit[e + 1], tmp[e >> 5]);
   if (threadIdx.x == 0) unit[0] = 0;
   __syncthreads();
 }
 
 // The expert whose units [unit[e], unit[e + 1]) hold u < unit[E].
-__device__ __forceinline__ int segment_of_unit(const int32_t* unit, int E, int u) {
+__host__ __device__ __forceinline__ int segment_of_unit(const int32_t* unit, int E, int u) {
   int lo = 0, hi = E;  // the largest e with unit[e] <= u has units
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;

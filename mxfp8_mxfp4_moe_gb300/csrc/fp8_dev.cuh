@@ -75,12 +75,12 @@ __host__ inline int product_split(long long items, int resident, int KB, int lea
   return split;
 }
 
-// Launches a product's kernel for at most `items` work items on up to
+// Launches a product's kernel for at most a.items work items on up to
 // `resident` CTAs; a.split is product_split's.
 template <typename Kernel>
-__host__ inline cudaError_t launch_product(Kernel kernel, int threads, int smem, long long items, int resident,
-                                           const Fp8Maps& maps, const Fp8Args& a, cudaStream_t st) {
-  const long long ctas = items * a.split;
+__host__ inline cudaError_t launch_product(Kernel kernel, int threads, int smem, int resident, const Fp8Maps& maps,
+                                           const Fp8Args& a, cudaStream_t st) {
+  const long long ctas = static_cast<long long>(a.items) * a.split;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see chain_wait
@@ -98,12 +98,13 @@ __host__ inline cudaError_t launch_product(Kernel kernel, int threads, int smem,
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
 
-// Work items of the segments' tiles for `clusters` clusters.  A table whose
-// segments overlap can hold more than the launch counted on; a cluster that
-// shares an item takes one even then, as its CTAs meet once.
-__device__ __forceinline__ int product_items(const Fp8Args& a, const int32_t* unit, int clusters) {
-  const int total = a.FT * unit[a.E];
-  return a.split > 1 ? min(total, clusters) : total;
+// Work items of `units` tiles of rows and `ft` of features, of which the launch
+// counted on at most `items`, which an ascending table keeps to.  One whose segments
+// overlap can hold more, beyond an int too; those are left out (a cluster that
+// shares an item takes one even then, as its CTAs meet once).
+__host__ __device__ __forceinline__ int product_items(int ft, int units, int items) {
+  const long long all = static_cast<long long>(ft) * units;
+  return all < items ? static_cast<int>(all) : items;
 }
 
 // A work item: features f0 .. of expert e for the columns (rows of the batch)

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS_PER_SM) fp8_gemm_kernel(co
   const uint32_t tmem = *tmem_slot;
   const uint64_t budget = a.budget_ns;
   const int w0 = blockIdx.x / a.split, dw = gridDim.x / a.split;
-  const int total = product_items(a, unit, dw);
+  const int total = product_items(a.FT, unit[a.E], a.items);
 
   if (warp < C::CTRL_WARPS) {
     if (warp == 0) {
@@ -394,9 +394,9 @@ static cudaError_t launch_cfg(const Fp8Maps& maps, Fp8Args a, int sms, cudaStrea
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  const long long items = fp8_most_tiles(a.M, a.E, C::BN) * a.FT;
-  a.split = product_split(items, C::CTAS_PER_SM * sms, a.KB, 4);
-  return launch_product(fp8_gemm_kernel<C>, C::THREADS, C::SMEM, items, C::CTAS_PER_SM * sms, maps, a, st);
+  a.items = static_cast<int>(fp8_most_tiles(a.M, a.E, C::BN) * a.FT);
+  a.split = product_split(a.items, C::CTAS_PER_SM * sms, a.KB, 4);
+  return launch_product(fp8_gemm_kernel<C>, C::THREADS, C::SMEM, C::CTAS_PER_SM * sms, maps, a, st);
 }
 
 cudaError_t launch_fp8_gemm(bool back, const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {

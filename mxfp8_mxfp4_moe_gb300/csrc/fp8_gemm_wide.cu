@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
   const uint64_t budget = a.budget_ns;
   const int ctas = C::SPLIT ? a.split : 1;
   const int w0 = blockIdx.x / ctas, dw = gridDim.x / ctas;
-  const int total = product_items(a, unit, dw);
+  const int total = product_items(a.FT, unit[a.E], a.items);
 
   if (warp < C::CTRL_WARPS) {
     // (of the registers that the block was launched with)
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) fp8_gemm_wide_kernel(const __gr
 }
 
 template <class C>
-static cudaError_t launch_cfg(const Fp8Maps& maps, const Fp8Args& a, long long items, int sms, cudaStream_t st) {
+static cudaError_t launch_cfg(const Fp8Maps& maps, const Fp8Args& a, int sms, cudaStream_t st) {
   static bool set[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
@@ -432,19 +432,19 @@ static cudaError_t launch_cfg(const Fp8Maps& maps, const Fp8Args& a, long long i
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  return launch_product(fp8_gemm_wide_kernel<C>, C::THREADS, C::SMEM, items, sms, maps, a, st);
+  return launch_product(fp8_gemm_wide_kernel<C>, C::THREADS, C::SMEM, sms, maps, a, st);
 }
 
 cudaError_t launch_fp8_gemm_wide(bool back, const Fp8Maps& maps, Fp8Args a, int sms, cudaStream_t st) {
   using C = Fp8WideCfg<false, false>;
   a.FT = (a.F + C::BN - 1) / C::BN;
-  const long long items = fp8_most_tiles(a.M, a.E, C::BM) * a.FT;
-  a.split = product_split(items, sms, a.KB, 8);
+  a.items = static_cast<int>(fp8_most_tiles(a.M, a.E, C::BM) * a.FT);
+  a.split = product_split(a.items, sms, a.KB, 8);
   if (a.split > 1)
-    return back ? launch_cfg<Fp8WideCfg<true, true>>(maps, a, items, sms, st)
-                : launch_cfg<Fp8WideCfg<false, true>>(maps, a, items, sms, st);
-  return back ? launch_cfg<Fp8WideCfg<true, false>>(maps, a, items, sms, st)
-              : launch_cfg<Fp8WideCfg<false, false>>(maps, a, items, sms, st);
+    return back ? launch_cfg<Fp8WideCfg<true, true>>(maps, a, sms, st)
+                : launch_cfg<Fp8WideCfg<false, true>>(maps, a, sms, st);
+  return back ? launch_cfg<Fp8WideCfg<true, false>>(maps, a, sms, st)
+              : launch_cfg<Fp8WideCfg<false, false>>(maps, a, sms, st);
 }
 
 }  // namespace kmoe
