@@ -131,7 +131,9 @@ int kmoe_quantize_fp8_cols(const void* x_bf16, int rows, int cols, const int32_t
  *   their contents.  N and K multiples of 16; x, w and out 16-byte aligned.
  *   workspace: KMOE_GEMM_FP8_WORKSPACE_BYTES, 256-byte aligned: its first word
  *   is the device error word (kmoe_device_error), cleared by every call that
- *   has rows.  Calls that can overlap on the GPU take a workspace each. */
+ *   has rows (one without leaves it as it is): what an earlier call in the same
+ *   workspace left there is gone, so it is read before, or each call has a
+ *   workspace of its own.  Calls that can overlap on the GPU take one each. */
 int kmoe_gemm_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
                   const int32_t* seg_start, int M, int N, int K, int E, uint32_t flags, void* out, void* workspace,
                   size_t ws_bytes, cudaStream_t stream);

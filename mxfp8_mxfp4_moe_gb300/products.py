@@ -269,7 +269,8 @@ def kmoe_gemm_fp8(x, x_scales, w, w_scales, seg_start=None, transpose=False, out
     and x_scales as kmoe_quantize_fp8 gives them, w_scales [E, ceil(N/128),
     ceil(K/128)] fp32.  Expert e's rows are [seg_start[e], seg_start[e+1]); rows
     outside are left as they were.  Returns (out, workspace); the workspace's
-    first word is the device error word."""
+    first word is the device error word, which the next product in it clears:
+    read it before (kmoe_device_error), or let each product have its own."""
     M, _, dev = _rows_on(x, "x", "cols")
     (E, N, K), sf = _weights(w, "w")
     experts, seg = _experts(seg_start)
@@ -283,6 +284,9 @@ def kmoe_gemm_fp8(x, x_scales, w, w_scales, seg_start=None, transpose=False, out
     if workspace is None:
         workspace = _new(GEMM_FP8_WORKSPACE_BYTES, _U8, dev, stream)
         at[6] = workspace.data_ptr()
+        if M == 0:  # a call without rows leaves the error word as it is
+            with torch.cuda.stream(stream):
+                workspace.zero_()
     if out is None:
         out = _new((M, F), to, dev, stream)
         at[5] = out.data_ptr()
