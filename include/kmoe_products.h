@@ -24,7 +24,7 @@ extern "C" {
  *   kmoe_gemm_fp8_wgrad (the weights'), ..., kmoe_unpermute without weights.
  * At most 2^30 rows (tokens times k) and 2^20 columns.  These kernels are
  * launched with programmatic stream serialization and wait for what is queued
- * before them. */
+ * before them.  Calls that can overlap on the GPU take a workspace each. */
 
 /* Tokens sorted by expert: a stable sort of the slots s = t * k + j by
  * topk_ids[s].
@@ -116,8 +116,11 @@ int kmoe_quantize_fp8_cols(const void* x_bf16, int rows, int cols, const int32_t
  * for m in [seg_start[e], seg_start[e+1]), or with KMOE_GEMM_TRANSPOSE
  *   out[m, k] = sum_b x_scales[b, m] * w_scales[e, b, k/128] *
  *               sum_{n in block b of 128} x[m, n] * w[e, n, k].
- * A block's products are summed by the tensor cores, the scaled blocks in fp32
- * in the order of b; out is rounded once.  Scales are any fp32 values whose
+ * A block's products are summed by the tensor cores, the scaled blocks in fp32,
+ * in the order of b; where there are few rows up to eight ranges of blocks are
+ * summed so, each by itself, and then the ranges in their order.  How many depends
+ * on the sizes of the call and the GPU's SMs: equal calls give equal bits, a row in
+ * a call of another size may differ in its last ones.  out is rounded once.  Scales are any fp32 values whose
  * product, which is taken first, is a normal fp32 number or 0.  Below 2^-126 it
  * loses bits, by which a block is off by up to 2^-125 (kmoe_quantize_fp8's
  * smallest scale, 2^-126, is that of zeros, which stay exact, and of values below
@@ -133,7 +136,7 @@ int kmoe_quantize_fp8_cols(const void* x_bf16, int rows, int cols, const int32_t
  *   is the device error word (kmoe_device_error), cleared by every call that
  *   has rows (one without leaves it as it is): what an earlier call in the same
  *   workspace left there is gone, so it is read before, or each call has a
- *   workspace of its own.  Calls that can overlap on the GPU take one each. */
+ *   workspace of its own. */
 int kmoe_gemm_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
                   const int32_t* seg_start, int M, int N, int K, int E, uint32_t flags, void* out, void* workspace,
                   size_t ws_bytes, cudaStream_t stream);

@@ -38,9 +38,13 @@ __host__ inline long long fp8_most_tiles(long long M, int E, int per) {
   return (M + (per - 1) * with) / per;
 }
 // Whether M rows of E experts are few for each, fp8_gemm.cu's; else
-// fp8_gemm_wide.cu's.  On the GPU, weights of 7168 x 7168: 32 rows of one take
-// 11.4 us there (33 to 64: 16.5 in tiles of 128); 256 rows of 8 experts of
-// 7168 x 3584 39, 320 rows 42 in tiles of 128.
+// fp8_gemm_wide.cu's.  One matrix of 7168 x 7168, from HBM: 8 to 32 rows take
+// 13.6 us there, 18.5 to 23 in tiles of 128.  8 experts of 7168 x 3584 with 4 to
+// 32 rows each 38 to 39 us, in tiles of 128 41 to 52 (transposed 34 to 35 and
+// 35 to 36).  64 experts: 246 to 265 us, in tiles of 128 245 to 253 (transposed
+// 248 to 270 and 233 to 237): the rule looks at the average alone and errs by up
+// to 12 % there, and by up to 16 % where half of the rows are one expert's (2048
+// rows: 327 and 275 us).
 __host__ inline bool fp8_few_rows(int M, int E) { return (M + E - 1) / E <= 32; }
 // Rows of a TMA box of the rows: tiles of up to 32 are cut to multiples of 16
 // (a copy takes the time of its rows), those of many are 128.

@@ -66,7 +66,8 @@ __device__ __forceinline__ float2 ld_shared_cluster_f2(uint32_t cluster_addr) {
 // CTAs of a cluster that share an item where `items` (at most) are too few for
 // the CTAs that can run at once: up to eight, with `least` blocks of the sum for
 // each.  Such a cluster has one item, and its CTAs meet once.  One row, 7168 x
-// 7168: clusters of 1, 2 and 4 take 21.5, 13.8 and 10.6 us.  fp8_gemm.cu's tiles
+// 7168, the same weights again and again: clusters of 1, 2 and 4 take 21.5, 13.8
+// and 10.6 us.  fp8_gemm.cu's tiles
 // want four blocks for each CTA, fp8_gemm_wide.cu's eight: their exchange is
 // eight times larger (128 rows, 4096 x 4096: four blocks each 25 us, eight 12.5).
 __host__ inline int product_split(long long items, int resident, int KB, int least) {

@@ -11,7 +11,7 @@
 // another accumulator, multiply by the product of the two scales and add in fp32
 // registers.  That product may leave fp32's normal range, which the header says;
 // finding such blocks in the epilogue and giving them their scales one after the
-// other was measured at 3 to 25 % of fp8_gemm_wide.cu's time for every call (each
+// other was measured at 2 to 28 % of fp8_gemm_wide.cu's time for every call (each
 // read of shared memory, vote or register more lengthens the accumulators'
 // hand-over) and 1 to 4 % here.
 // The features f are the MMA's M, the rows its N (16 .. BN), so that a few
@@ -22,7 +22,8 @@
 // Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues), warp
 // 2 the scales (a ring in shared memory, some blocks ahead of their use: with
 // few rows a block takes less time than a read of global memory), warps 3 .. 6
-// the epilogue, one per TMEM lane quarter.  Every wait is bounded.
+// the epilogue, one per TMEM lane quarter.  Every wait on an mbarrier is bounded;
+// the cluster's barriers, which are not, are reached by every warp after its own.
 //
 // Where there are too few items for the SMs, a cluster of `split` CTAs takes
 // one item: each sums a part of the blocks, and the parts are added in order
@@ -31,7 +32,9 @@
 // Bound by HBM's reads of the weights where they are many (2048 rows of 64
 // experts, 7168 x 3584: 256-264 us, 6.2-6.4 TB/s), by the chain of launch,
 // first load, blocks and exchange where they are one matrix: one row 7168 x
-// 7168 10.6 us (51 MB: 4.8 TB/s), 16 rows 2048 x 7168 7.4 us.
+// 7168 13.3 us with the 51 MB of weights from HBM (3.9 TB/s; eight matrices in
+// turn), 10.7 with one matrix again and again, part of which stays in L2; 16 rows
+// 2048 x 7168 7.4 us.  Transposed the same (13.2; 2048 rows of 64 experts 260-271).
 #include <type_traits>
 
 #include "fp8_dev.cuh"

@@ -14,15 +14,18 @@
 // Roles: warp 0 TMA, warp 1 MMA (both converged, one elected lane issues),
 // warp 2 the scales (a ring in shared memory, some blocks ahead of their use),
 // warps 4 .. 11 the epilogue: two groups of four (one warp per TMEM lane
-// quarter), each with 128 features of the tile.  Every wait is bounded.
+// quarter), each with 128 features of the tile.  Every wait on an mbarrier is
+// bounded; the clusters' barriers are reached by every warp after its own waits.
 //
 // A block of the sum takes 584 cycles of the tensor core, at least 520 of the
 // epilogue (TMEM reads and multiply-adds of 128 x 256 values) and 880 of its
 // 48 KB through TMA; with the two accumulators' handshake it comes to about
 // 1030.  8192 rows, 7168 x 7168: 336 us, 2500 TFLOP/s (1.30 of the bf16 peak,
-// 0.65 of twice it); 64 experts with 512 rows each 1394 us.  Measured there:
-// the rows in the MMA's N 708-1048, CTA pairs with a handshake a block 775 and
-// more, 12 or 16 epilogue warps 354-432, accumulators in halves 429.
+// 0.65 of twice it); 64 experts with 512 rows each 1394 us; 896 experts with 146
+// rows each on average, 2048 x 2048, 1100-1140 (bytes: 683), whose second tiles are
+// mostly empty.  Measured at 8192 rows: the rows in the MMA's N 708-1048, CTA pairs
+// 1038 (a pair's accumulators handed over without any loads 775, one CTA's 304), 12
+// or 16 epilogue warps 354-432, accumulators in halves 429.
 #include <type_traits>
 
 #include "fp8_dev.cuh"

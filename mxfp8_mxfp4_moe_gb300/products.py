@@ -3,7 +3,9 @@ expert and summed back with their weights, quantisation to E4M3 with a scale for
 each block of 128, products of such operands, and the gradients of each.
 
 Part of the package's binding, whose rules for arguments, streams and memory
-hold here; the functions are the package's own (kmoe_gemm_fp8 and so on).
+hold here; the functions are the package's own (kmoe_gemm_fp8 and so on).  Codes
+are torch.uint8: a checkpoint's torch.float8_e4m3fn tensor goes in as its
+.view(torch.uint8), and codes are values as .view(torch.float8_e4m3fn).
 """
 from __future__ import annotations
 
