@@ -120,12 +120,12 @@ int kmoe_quantize_fp8_cols(const void* x_bf16, int rows, int cols, const int32_t
  * in the order of b; where there are few rows up to eight ranges of blocks are
  * summed so, each by itself, and then the ranges in their order.  How many depends
  * on the sizes of the call and the GPU's SMs: equal calls give equal bits, a row in
- * a call of another size may differ in its last ones.  out is rounded once.  Scales are any fp32 values whose
- * product, which is taken first, is a normal fp32 number or 0.  Below 2^-126 it
- * loses bits, by which a block is off by up to 2^-125 (kmoe_quantize_fp8's
- * smallest scale, 2^-126, is that of zeros, which stay exact, and of values below
- * 2^-117); from 2^128 on it is an infinity, and so is the block, or NaN where its
- * sum is 0.
+ * a call of another size may differ in its last ones.  out is rounded once.
+ *   Scales are any fp32 values whose product, which is taken first, is a normal
+ * fp32 number or 0.  Below 2^-126 it loses bits, by which a block is off by up to
+ * 2^-125 (kmoe_quantize_fp8's smallest scale, 2^-126, is that of zeros, which stay
+ * exact, and of values below 2^-117); from 2^128 on it is an infinity, and so is
+ * the block, or NaN where its sum is 0.
  *   x [M, K] (transposed: [M, N]) codes, x_scales [ceil(cols/128), M] float
  *   (kmoe_quantize_fp8's); w [E, N, K] codes, w_scales [E, ceil(N/128),
  *   ceil(K/128)] float (kmoe_quantize_fp8_weights', or a checkpoint's);
