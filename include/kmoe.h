@@ -57,7 +57,7 @@ extern "C" {
 enum kmoe_status {
   KMOE_OK = 0,
   KMOE_ERR_ARG = 1,        /* null pointer, k > E, non-positive size, bad enum */
-  KMOE_ERR_SHAPE = 2,      /* H or I not a multiple of 128, FC1 width != 2 x FC2 K, ... */
+  KMOE_ERR_SHAPE = 2,      /* H or I not a multiple of 128, FC1 width != 2 x FC2 K, a size that the call's comment rules out */
   KMOE_ERR_ALIGN = 3,      /* a pointer is not aligned as documented */
   KMOE_ERR_ARCH = 4,       /* device is not sm_103 (GB300) or the kernels do not load */
   KMOE_ERR_WORKSPACE = 5,  /* workspace null or smaller than kmoe_workspace_size() */

@@ -127,7 +127,9 @@ const char* kmoe_status_string(int s) {
   switch (s) {
     case KMOE_OK: return "ok";
     case KMOE_ERR_ARG: return "invalid argument";
-    case KMOE_ERR_SHAPE: return "unsupported shape (H and I must be multiples of 128; FC1 rows = 2 x FC2 K)";
+    case KMOE_ERR_SHAPE:
+      return "unsupported shape (the layer: H and I must be multiples of 128, FC1 rows = 2 x FC2 K; other calls: see "
+             "their declaration)";
     case KMOE_ERR_ALIGN: return "misaligned pointer";
     case KMOE_ERR_ARCH: return "device is not compute capability 10.3 (GB300) or the kernels do not load";
     case KMOE_ERR_WORKSPACE: return "workspace missing or too small";
